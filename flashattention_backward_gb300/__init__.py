@@ -9,7 +9,8 @@ call fails, an exception is raised.
 Entry points mirror the C names: :func:`fa_fwd`, :func:`fa_bwd_preprocess`,
 :func:`fa_bwd`, :func:`fa_convert_dq`, :func:`fa_backward`, plus
 :func:`attention_forward` / :func:`attention_backward`, which allocate their
-outputs with torch and call those.
+outputs with torch and call those.  The paged key-value cache
+(:func:`attention_decode`, ``cache_*``, ``pages_*``) is in ``paged.py``.
 """
 
 from __future__ import annotations
@@ -20,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import _build
+from . import _build, paged
 
 __all__ = [
     "FaError",
@@ -46,9 +47,20 @@ __all__ = [
     "selftest_wait_timeout",
     "library_path",
     "load_library",
+    "FaCache",
+    "cache_for",
+    "attention_decode",
+    "fa_decode_workspace_bytes",
+    "cache_append",
+    "cache_copy_pages",
+    "pages_extend",
+    "pages_fork",
+    "pages_free",
+    "pages_compact",
+    "fa_pages_scratch_elems",
 ]
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE = range(6)
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE, FA_ERR_PAGES = range(7)
 FA_BF16, FA_FP32 = 0, 1
 FA_FLAG_DETERMINISTIC = 1
 TILE_ROWS = 128
@@ -129,6 +141,7 @@ def load_library() -> ctypes.CDLL:
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_version.argtypes = []
     lib.fa_version.restype = ctypes.c_int32
+    paged.declare(lib)
     _LIB = lib
     return lib
 
@@ -446,3 +459,18 @@ def set_wait_limit_ns(ns: int) -> None:
 
 def selftest_wait_timeout(limit_ns: int, stream=None) -> None:
     _check(load_library().fa_selftest_wait_timeout(int(limit_ns), _stream(stream)), "fa_selftest_wait_timeout")
+
+
+from .paged import (  # noqa: E402
+    FaCache,
+    attention_decode,
+    cache_append,
+    cache_copy_pages,
+    cache_for,
+    fa_decode_workspace_bytes,
+    fa_pages_scratch_elems,
+    pages_compact,
+    pages_extend,
+    pages_fork,
+    pages_free,
+)

@@ -510,6 +510,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "device wait timed out";
     case FA_ERR_DEVICE: return "device self check failed";
+    case FA_ERR_PAGES: return "page, length or index of a paged cache out of range, or too few free pages";
   }
   return "unknown status";
 }

@@ -1,0 +1,76 @@
+// Shared by the paged-cache translation units (fa_decode.cu, fa_cache.cu,
+// fa_pages.cu): exact division by a number known at launch, host checks of a
+// fa_cache, and the report of a bad page.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// n / d for 0 <= n < 2^31 and 1 <= d < 2^31 as one multiply-high, an addition
+// and a shift: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
+// floor(n / d) = (mulhi(n, m) + n) >> s (the round-up method of Granlund and
+// Montgomery; the sum stays below 2^32 because mulhi(n, m) <= n).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), s(0) {
+    while ((1ull << s) < div) ++s;
+    m = (uint32_t)((((1ull << s) - div) << 32) / div + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+  __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t* rem) const {
+    const uint32_t q = div(n);
+    *rem = n - q * d;
+    return q;
+  }
+};
+
+inline bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline int elem_size(int32_t dtype) { return dtype == FA_BF16 ? 2 : 4; }
+inline int64_t cache_rows(const fa_cache& c) { return (int64_t)c.page_rows * c.max_pages; }
+
+// The table's geometry: what the page calls read.
+inline fa_status check_pages(const fa_cache* c) {
+  if (!c || c->num_pages < 1 || c->page_rows < 1 || c->S < 1 || c->max_pages < 1 || c->H_kv < 1 || c->reserved != 0 ||
+      c->table_stride < c->max_pages)
+    return FA_ERR_INVALID_ARG;
+  if (c->num_pages > (1 << 30) || cache_rows(*c) > (1 << 30) || (int64_t)c->S * c->H_kv > (1 << 24))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// One row-shaped operand's strides: no two rows may overlap where it is
+// written, and every row starts on 16 bytes.
+inline bool good_stride(int64_t stride, int d, int es, bool written) {
+  return stride >= (written ? d : 0) && stride < (int64_t(1) << 48) && (stride * es) % 16 == 0;
+}
+
+inline fa_status check_cache(const fa_cache* c) {
+  const fa_status st = check_pages(c);
+  if (st != FA_OK) return st;
+  if (c->dtype != FA_BF16 && c->dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+  const bool known = c->d == 32 || c->d == 64 || c->d == 96 || c->d == 128 || c->d == 256;
+  if (!known && !(c->d == 16 && c->dtype == FA_FP32)) return FA_ERR_UNSUPPORTED;
+  const int es = elem_size(c->dtype);
+  if (!good_stride(c->stride_page, c->d, es, true) || !good_stride(c->stride_h, c->d, es, true) ||
+      !good_stride(c->stride_n, c->d, es, true))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+inline fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// SMs of the current device (looked up once per device).
+int sm_count();
+
+__device__ __forceinline__ void report_pages(int32_t* status) { atomicCAS(status, 0, (int32_t)FA_ERR_PAGES); }
+
+// Pages that hold n rows.
+__device__ __forceinline__ int pages_of(int64_t n, int page_rows) { return (int)((n + page_rows - 1) / page_rows); }
+
+}  // namespace fa

@@ -86,7 +86,9 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,  /* valid problem outside the supported set        */
   FA_ERR_CUDA = 3,         /* a CUDA runtime call or launch failed           */
   FA_ERR_TIMEOUT = 4,      /* device: a bounded wait ran out                 */
-  FA_ERR_DEVICE = 5        /* device: a kernel self check failed             */
+  FA_ERR_DEVICE = 5,       /* device: a kernel self check failed             */
+  FA_ERR_PAGES = 6         /* device: a page, length or index of the paged
+                            * cache out of range, or too few free pages      */
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_FP32 = 1 } fa_dtype;
@@ -247,6 +249,134 @@ fa_status fa_backward_host(const fa_problem* p, const void* Q, const void* K, co
 fa_status fa_backward_static_workspace(const fa_problem* p, const void* Q, const void* K, const void* V,
                                        const void* O, const void* dO, const float* L, void* dQ, void* dK,
                                        void* dV, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache: the attention of one new token, and the pages.
+ * ------------------------------------------------------------------------
+ * A cache is two pools, K and V, of num_pages pages each.  A page holds
+ * page_rows rows of H_kv heads: element (page, g, r, c) of either pool is at
+ * page * stride_page + g * stride_h + r * stride_n + c.  Row j of sequence s
+ * is row j % page_rows of page page_table[s * table_stride + j / page_rows].
+ * page_table, lengths and refs are int32 arrays on the device:
+ *   page_table  S rows of max_pages entries; entries behind a sequence's
+ *               pages are not read (the page calls below keep them at -1)
+ *   lengths     S: rows that each sequence has; 0 is an empty slot
+ *   refs        num_pages: how many table entries name the page; 0 is free.
+ *               Only the page calls below read it.
+ * Contents on the device that the host cannot see are checked by the
+ * kernels: a page, length or index out of range is never followed, the
+ * device status word receives FA_ERR_PAGES (see fa_get_device_status), and
+ * the row, pair or sequence it belongs to is treated as each call says.
+ *
+ * dtype FA_BF16 with d in {32, 64, 96, 128, 256}, or FA_FP32 with d in {16,
+ * 32, 64, 96, 128, 256}.  num_pages, page_rows, S, max_pages, H_kv >= 1,
+ * page_rows * max_pages <= 2^30, S * H_kv <= 2^24, and
+ * num_pages <= 2^30.  Offsets into the pools are 64-bit. */
+typedef struct {
+  int32_t num_pages, page_rows, H_kv, d;
+  int32_t dtype;     /* fa_dtype of both pools and of Q, O and the new rows */
+  int32_t S;         /* rows of page_table: sequences                       */
+  int32_t max_pages; /* columns of page_table                               */
+  int32_t reserved;  /* must be 0 */
+  int64_t stride_page, stride_h, stride_n; /* element strides of both pools; byte strides multiples of 16 */
+  int64_t table_stride;                    /* elements between rows of page_table, >= max_pages */
+} fa_cache;
+
+/* Attention of one token: for every sequence s with n = lengths[s] rows and
+ * every query head h, with key head g = h / (H / H_kv),
+ *   O[s,h] = sum_j softmax_j(scale Q[s,h] . K[j,g]) V[j,g]  over its n rows,
+ *   L[s,h] = logsumexp_j(scale Q[s,h] . K[j,g])             (natural log).
+ * n = 0 gives O = 0, L = +inf, as fa_fwd gives a query that sees no key.
+ * Rows behind n are not read.  A row on a page out of range counts as not
+ * visible, a negative length as 0 and one beyond page_rows * max_pages as
+ * that (FA_ERR_PAGES in each case).
+ * Q, O are [S, H, d] with element strides (q_stride_s, q_stride_h) and
+ * (o_stride_s, o_stride_h), 16-byte aligned with byte strides multiples of
+ * 16; O may not overlap Q.  L is a dense [S, H] float32 array.  H is a
+ * multiple of H_kv, S * H <= 2^24, scale > 0.
+ * The rows of all sequences are shared out evenly over the GPU, and a
+ * sequence that several thread blocks read is joined from their partial
+ * results, which pass through `workspace` (16-byte aligned,
+ * fa_decode_workspace_bytes(c, H) bytes, whose contents before the call do
+ * not matter; 0 bytes: may be NULL).  Calls that may run at the same time
+ * need a workspace each, also when they are replayed from graphs.
+ * Results are bitwise reproducible for the same S, H and lengths on the same
+ * kind of GPU. */
+size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H);
+fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
+                    const void* K_pages, const void* V_pages, const int32_t* page_table, const int32_t* lengths,
+                    void* O, int64_t o_stride_s, int64_t o_stride_h, float* L, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* New rows into their pages: row i < counts[s] of K[s, g] and V[s, g] becomes
+ * row start[s] + i of sequence s.  K, V are [S, H_kv, rows, d] with element
+ * strides (stride_s, stride_h, stride_n), byte strides multiples of 16.
+ * counts NULL: all `rows` rows of every sequence; counts outside 0 ... rows
+ * are cut to it (FA_ERR_PAGES).  A sequence whose start is negative is left
+ * alone (what fa_pages_extend returns when it refuses); a row whose page is
+ * out of range or that lies behind the table is dropped (FA_ERR_PAGES).
+ * Sequences must not share the pages written to (fa_pages_fork sees to
+ * that).  rows >= 1, S * H_kv * rows < 2^31. */
+fa_status fa_cache_append(const fa_cache* c, int32_t rows, const void* K, const void* V, int64_t stride_s,
+                          int64_t stride_h, int64_t stride_n, void* K_pages, void* V_pages, const int32_t* page_table,
+                          const int32_t* start, const int32_t* counts, void* stream);
+
+/* Rows from page to page of both pools: for each of the first
+ * min(*count, max_moves) triples (src, dst, rows) of `moves` (int32
+ * [max_moves, 3]; count NULL: max_moves), rows 0 ... rows - 1 of page src are
+ * copied to page dst.  A triple with src = -1 is skipped, one out of range
+ * too (FA_ERR_PAGES).  No dst may be the dst or the src of another triple:
+ * the moves that fa_pages_fork and fa_pages_compact write are of that kind;
+ * with others the rows of that page may come from either.  page_table is not
+ * read (c->S, max_pages and table_stride must still be valid). */
+fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_t* moves, const int32_t* count,
+                              void* K_pages, void* V_pages, void* stream);
+
+/* The page calls: whole numbers on the device, no host round trip, so that
+ * they can stand in a captured graph between the calls above.  A sequence
+ * with n rows has ceil(n / page_rows) pages.  Free pages are taken lowest
+ * number first, in the order of the sequences or pairs.  scratch is
+ * fa_pages_scratch_elems(c) int32, contents before the call do not matter;
+ * calls that may run at the same time need one each (and, of course, tables
+ * of their own).  Only the geometry of `c` is read, not its strides, dtype
+ * or d. */
+size_t fa_pages_scratch_elems(const fa_cache* c);
+
+/* Makes room for n_new[s] >= 0 more rows: start[s] = lengths[s], lengths[s]
+ * += n_new[s], and the pages that takes enter the table with refs = 1.  All
+ * or nothing: when there are too few free pages, a sequence would pass the
+ * table, or a length or n_new is out of range, nothing changes, every
+ * start[s] is -1 and FA_ERR_PAGES is recorded. */
+fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengths, int32_t* refs,
+                          const int32_t* n_new, int32_t* start, int32_t* scratch, void* stream);
+
+/* Pair i makes the empty sequence dst[i] a copy of src[i]: it shares its full
+ * pages (refs + 1), and a last page that is partly filled is replaced by a
+ * free one; moves[i] = (old page, new page, rows in it) for
+ * fa_cache_copy_pages, or (-1, -1, -1).  src may repeat.  All or nothing:
+ * with an index out of range, a dst that is not empty, comes twice or is also
+ * a src, a damaged table row or too few free pages, nothing changes, all
+ * moves are -1 and FA_ERR_PAGES is recorded.  1 <= pairs <= S. */
+fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, const int32_t* dst, int32_t* page_table,
+                        int32_t* lengths, int32_t* refs, int32_t* moves, int32_t* scratch, void* stream);
+
+/* Empties the sequences listed: refs - 1 for each of their pages, table
+ * entries -1, length 0.  An index of -1 is skipped, one out of range too
+ * (FA_ERR_PAGES); a sequence listed twice is emptied once. */
+fa_status fa_pages_free(const fa_cache* c, int32_t count, const int32_t* sequences, int32_t* page_table,
+                        int32_t* lengths, int32_t* refs, void* stream);
+
+/* Moves the pages in use to the front of the pool.  With n of them, the k-th
+ * page in use at n or behind goes to the k-th free page before n: the moves
+ * (src, dst, page_rows) go to `moves` (int32 [num_pages / 2, 3], the rest
+ * -1) and their number to *n_moves, for fa_cache_copy_pages.  table_out and
+ * refs_out receive the table and refs after the moves, entries behind a
+ * sequence's pages -1; they may be page_table and refs themselves, or copies
+ * (same strides), so that work in flight still reads the old ones.  An entry
+ * out of range becomes -1 (FA_ERR_PAGES). */
+fa_status fa_pages_compact(const fa_cache* c, const int32_t* page_table, const int32_t* lengths, const int32_t* refs,
+                           int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* n_moves, int32_t* scratch,
+                           void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
  * word.  *code receives FA_OK or the first device-side error recorded since

@@ -1,0 +1,270 @@
+"""fa_decode against the float64 restatement: head layouts, head dims, page
+sizes, lengths from nothing to tens of thousands, splits and joins, strides,
+streams and graphs.
+
+Tolerances are bounds, not fits.  With u = 2^-24, a score is a sum of d
+products whose absolute sum is at most A (as the oracle returns it), summed in
+fp32 with at most 2u of the sum an addition, so it is off by
+e_s <= 2 d u A + 4 u |s|, |s| <= A.  A weight exp(s - m) is then off by e_s plus the
+rounding of its exponent's product (4 u |s|), 2^-21 of the hardware exponential and,
+in bf16, 2^-16 (it is multiplied as the sum of two bf16 numbers, each rounded to
+2^-8 of its value).  Both the weighted sum and the sum of weights carry that
+error and at most 2 u n of their additions, so
+  |O - ref| <= half a step of the output type * |ref| + 2 V (e_w + 2 (n + 64) u)
+  |L - ref| <= e_s + e_w + 2 (n + 64) u + 8 u |L|
+with V the largest |v|, n the number of rows and 64 for the joining of parts."""
+
+import numpy as np
+import pytest
+import torch
+
+import flashattention_backward_gb300 as fa
+from oracle.paged_fp64 import decode
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    fa.load_library()
+    assert fa.get_device_status() == 0
+
+
+def make(S, H, Hk, d, page, lengths, dtype=torch.bfloat16, seed=0, rows_first=False, spare=2, junk=True, q_std=1.0):
+    """A cache with pages in random order; what no row reads is NaN."""
+    gen = torch.Generator().manual_seed(seed)
+    held = [-(-n // page) for n in lengths]
+    pages, columns = sum(held) + spare, max(held + [1]) + 1
+    order = torch.randperm(pages, generator=gen)
+    table = torch.full((S, columns), -1, dtype=torch.int32)
+    shape = (pages, page, Hk, d) if rows_first else (pages, Hk, page, d)
+    pools = []
+    for _ in range(2):
+        t = torch.randn(shape, generator=gen).to(dtype)
+        pools.append(t.permute(0, 2, 1, 3) if rows_first else t)
+    live = torch.zeros(pages, page, dtype=torch.bool)
+    k = 0
+    for s, n in enumerate(lengths):
+        ids = order[k:k + held[s]]
+        k += held[s]
+        table[s, :held[s]] = ids.int()
+        for c in range(held[s]):
+            live[ids[c], :max(0, min(page, n - c * page))] = True
+    if junk:
+        for t in pools:
+            t[~live[:, None, :].expand(-1, Hk, -1)] = float("nan")
+    q = (torch.randn(S, H, 1, d, generator=gen) * q_std).to(dtype)
+    lens = torch.tensor(lengths, dtype=torch.int32)
+    return [t.to(DEV) for t in (q, *pools, table, lens)]
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def check(got, q, kp, vp, table, lengths, scale):
+    o, L = got
+    d = q.shape[3]
+    ref, Lr, A, V = decode(f64(q)[:, :, 0], np.nan_to_num(f64(kp)), np.nan_to_num(f64(vp)), table.cpu().numpy(),
+                           lengths.cpu().numpy(), float(np.float32(scale)))
+    n = lengths.cpu().clamp(min=0).numpy()[:, None]
+    e_s = 2 * d * U * A + 4 * U * A
+    e_w = e_s + 4 * U * A + 2.0 ** -21 + (2.0 ** -16 if q.dtype == torch.bfloat16 else 0)
+    tol_o = HALF_STEP[q.dtype] * np.abs(ref) + (2 * V * (e_w + 2 * (n + 64) * U))[:, :, None]
+    x, y = f64(o)[:, :, 0], f64(L)[:, :, 0]
+    assert np.isfinite(x).all()
+    assert (np.abs(x - ref) <= tol_o).all(), float((np.abs(x - ref) - tol_o).max())
+    empty = np.isinf(Lr)
+    assert (x[empty] == 0).all() and np.array_equal(np.isposinf(y), empty)
+    tol_l = e_s + e_w + 2 * (n + 64) * U + 8 * U * np.abs(np.where(empty, 0, Lr))
+    assert (np.abs(y[~empty] - Lr[~empty]) <= tol_l[~empty]).all(), float(np.abs(y[~empty] - Lr[~empty]).max())
+
+
+def run_and_check(args, scale=None, **kw):
+    q, kp, vp, table, lengths = args
+    scale = q.shape[3] ** -0.5 if scale is None else scale
+    got = fa.attention_decode(q, kp, vp, table, lengths, scale, **kw)
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    check(got, q, kp, vp, table, lengths, scale)
+    return got
+
+
+BF16_DIMS, FP32_DIMS = (32, 64, 96, 128, 256), (16, 32, 64, 96, 128, 256)
+
+
+@pytest.mark.parametrize("d", BF16_DIMS)
+@pytest.mark.parametrize("H,Hk", [(4, 4), (6, 2), (16, 2), (12, 1), (16, 1), (40, 2)])
+def test_head_layouts_bf16(d, H, Hk):
+    lengths = [0, 1, 15, 16, 17, 63, 64, 65, 300]
+    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, seed=d + H))
+
+
+@pytest.mark.parametrize("d", FP32_DIMS)
+@pytest.mark.parametrize("H,Hk", [(3, 3), (6, 2), (9, 1), (16, 2)])
+def test_head_layouts_fp32(d, H, Hk):
+    lengths = [0, 1, 15, 16, 17, 63, 64, 65, 300]
+    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, torch.float32, seed=d + H))
+
+
+@pytest.mark.parametrize("page", [1, 2, 3, 7, 13, 16, 48, 64, 100, 256, 1000])
+@pytest.mark.parametrize("rows_first", [False, True])
+def test_page_sizes(page, rows_first):
+    lengths = [page - 1, page, page + 1, 2 * page, 259, 1]
+    for dtype in (torch.bfloat16, torch.float32):
+        run_and_check(make(6, 4, 2, 64, page, lengths, dtype, seed=page, rows_first=rows_first))
+
+
+@pytest.mark.parametrize("n", [1, 64, 65, 2048, 4000, 32768])
+@pytest.mark.parametrize("H,Hk,d,dtype", [(8, 1, 128, torch.bfloat16), (2, 2, 64, torch.bfloat16),
+                                          (2, 1, 256, torch.bfloat16), (2, 1, 96, torch.float32)])
+def test_one_sequence_over_the_whole_gpu(n, H, Hk, d, dtype):
+    run_and_check(make(1, H, Hk, d, 64, [n], dtype, seed=n))
+
+
+def test_many_short_and_one_long():
+    lengths = [4000] + [i % 5 for i in range(300)] + [1999]
+    run_and_check(make(len(lengths), 4, 2, 64, 16, lengths, seed=3))
+
+
+def test_all_empty():
+    run_and_check(make(3, 4, 2, 64, 16, [0, 0, 0]))
+
+
+def test_peaked_scores():
+    """Scores with a deviation of 4: the running maximum moves, most weights vanish."""
+    for dtype in (torch.bfloat16, torch.float32):
+        run_and_check(make(4, 8, 2, 128, 16, [3, 500, 2000, 77], dtype, seed=5, q_std=4.0))
+
+
+def test_rising_scores():
+    """Each key scores above the one before, so that every row raises the maximum."""
+    q, kp, vp, table, lengths = make(1, 4, 1, 64, 16, [700], seed=6, junk=False)
+    q.fill_(1.0)
+    for j in range(700):
+        kp[table[0, j // 16].item(), :, j % 16] = j / 64
+    run_and_check((q, kp, vp, table, lengths))
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1.0])
+def test_scale(scale):
+    run_and_check(make(3, 4, 2, 64, 16, [100, 7, 64], seed=8), scale)
+
+
+def test_strided_queries_and_given_outputs():
+    q, kp, vp, table, lengths = make(5, 8, 2, 64, 16, [100, 0, 7, 64, 1000], seed=9)
+    fused = torch.randn(5, 12, 64, device=DEV).to(torch.bfloat16)  # queries, keys and values of one projection
+    view = fused[:, 2:10, None, :]
+    o_all = torch.full((5, 10, 1, 64), 7.0, device=DEV, dtype=torch.bfloat16)
+    out = (o_all[:, 1:9], torch.empty(5, 8, 1, device=DEV))
+    ws = torch.empty(fa.fa_decode_workspace_bytes(fa.cache_for(kp, vp, table), 8), dtype=torch.uint8, device=DEV)
+    got = run_and_check((view, kp, vp, table, lengths), out=out, workspace=ws)
+    assert got[0].data_ptr() == out[0].data_ptr()
+    assert (o_all[:, 0] == 7).all() and (o_all[:, 9] == 7).all()
+
+
+def test_shared_pages():
+    """Sequences that name the same pages, as forks do."""
+    q, kp, vp, table, lengths = make(4, 8, 2, 128, 16, [320, 320, 320, 320], seed=10)
+    table[1:, :10] = table[0, :10]
+    run_and_check((q, kp, vp, table, lengths))
+
+
+def test_offsets_beyond_32_bits():
+    """Pages further than 2^31 elements (and 2^32 bytes) into the pools."""
+    pages, page, d = 70000, 256, 128  # 2.29e9 elements a pool
+    kp, vp = (torch.empty(pages, 1, page, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ids = [69999, 3, 65600, 69990]
+    gen = torch.Generator().manual_seed(11)
+    small = [torch.randn(4, 1, page, d, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    for i, p in enumerate(ids):
+        kp[p], vp[p] = small[0][i], small[1][i]
+    q = torch.randn(1, 4, 1, d, generator=gen).to(torch.bfloat16).to(DEV)
+    lengths = torch.tensor([1000], dtype=torch.int32, device=DEV)
+    got = fa.attention_decode(q, kp, vp, torch.tensor([ids], dtype=torch.int32, device=DEV), lengths)
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    check(got, q, *small, torch.tensor([[0, 1, 2, 3]], dtype=torch.int32), lengths, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_bad_pages_and_lengths_are_not_followed(dtype):
+    q, kp, vp, table, lengths = make(4, 4, 2, 64, 16, [100, 50, 300, 20], dtype, seed=12)
+    table[0, 2], table[2, 5] = 1 << 20, -7
+    got = fa.attention_decode(q, kp, vp, table, lengths)
+    assert fa.get_device_status() == fa.FA_ERR_PAGES
+    check(got, q, kp, vp, table, lengths, 64 ** -0.5)
+    lengths = torch.tensor([-5, 50, 1 << 30, 20], dtype=torch.int32, device=DEV)
+    got = fa.attention_decode(q, kp, vp, table, lengths)
+    assert fa.get_device_status() == fa.FA_ERR_PAGES
+    check((got[0][[0, 1, 3]], got[1][[0, 1, 3]]), q[[0, 1, 3]], kp, vp, table[[0, 1, 3]], lengths[[0, 1, 3]], 64 ** -0.5)
+    with pytest.raises(fa.FaError) as err:
+        fa.attention_decode(q, kp, vp, table, lengths, check_status=True)
+    assert err.value.code == fa.FA_ERR_PAGES
+    assert fa.get_device_status() == 0
+
+
+def test_same_call_same_bits():
+    args = make(7, 8, 2, 128, 16, [4000, 1, 900, 0, 77, 3333, 512], seed=13)
+    a = fa.attention_decode(*args)
+    for _ in range(5):
+        b = fa.attention_decode(*args)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_at_once():
+    args = [make(4, 8, 2, 128, 16, [4000, 100, 1700, 64], seed=20 + i) for i in range(2)]
+    want = [fa.attention_decode(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for a, st in zip(args, streams):
+            got.append(fa.attention_decode(*a, stream=st))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g[0], want[i % 2][0]) and torch.equal(g[1], want[i % 2][1])
+    assert fa.get_device_status() == 0
+
+
+def test_graph_follows_lengths_that_change():
+    """A captured call reads lengths and table at each replay; two graphs replayed at once have workspaces of their own."""
+    q, kp, vp, table, lengths = make(3, 8, 2, 64, 16, [2000, 900, 50], seed=30, junk=False)
+    pairs = []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(stream):
+            fa.attention_decode(q, kp, vp, table, lengths)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=stream):
+                got = fa.attention_decode(q, kp, vp, table, lengths)
+        pairs.append((stream, graph, got))
+    for new in ([2000, 900, 50], [1, 0, 16], [700, 777, 50]):
+        lengths.copy_(torch.tensor(new, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for stream, graph, _ in pairs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, got in pairs:
+            check(got, q, kp, vp, table, lengths, 64 ** -0.5)
+    assert fa.get_device_status() == 0
+
+
+def test_agrees_with_the_forward_over_the_same_rows():
+    """fa_fwd of one query row (causal, aligned bottom-right: it sees all keys) over a dense copy of the cache."""
+    S, H, d, n = 2, 4, 128, 1000
+    q, kp, vp, table, lengths = make(S, H, H, d, 8, [n] * S, seed=31)
+    at = table[:, : n // 8].long()
+    k, v = (t[at].permute(0, 2, 1, 3, 4).reshape(S, H, n, d).contiguous() for t in (kp, vp))
+    o, L = fa.attention_forward(q, k, v, d ** -0.5, causal=True)
+    o2, L2 = run_and_check((q, kp, vp, table, lengths))
+    # the forward rounds its weights to bf16 (2^-8 of each, at most 2^-8 of max |v| in the sum) and its output
+    assert (o.float() - o2.float()).abs().max() <= 2 * 2.0 ** -8 * v.float().abs().max()
+    assert (L.reshape(S, H) - L2.reshape(S, H)).abs().max() <= 1e-3
