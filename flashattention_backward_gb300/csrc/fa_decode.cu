@@ -195,25 +195,23 @@ __device__ __forceinline__ void store4(char* row, int col, float4 x) {
 }
 
 // ------------------------------------------------------- bf16: tensor cores
-// A warp takes 16 rows of each tile with mma.m16n8k16, whose operands come
-// straight from what each lane has copied for itself:
+// A warp takes 16 rows of each tile with mma.m16n8k16:
 //
 //  S = Q K^T     A = 16 query heads x 16 columns, B = 16 columns x 8 keys.
 //                A sum may be taken in any order, so the 16 columns of a step are
-//                those that make a lane's share of B a run of 16 bytes of a key:
-//                lane (g, q) holds columns 32 c + 8 q ... + 7 of key g, two
-//                steps' worth, and the same columns of Q for A.
+//                those that make a lane's share of B a run of 16 bytes of a key,
+//                two steps' worth, and the same columns of Q are A's.
 //  O^T += V^T P^T  A = 16 columns x 16 keys, B = 16 keys x 8 heads: S's
 //                accumulators are P^T's operand as they stand.  A's pairs of
-//                keys come from two rows: lane (g, q) holds columns 64 c + 8 g
+//                keys come from two rows: lane (g, q) reads columns 64 c + 8 g
 //                ... + 7 of keys 2q, 2q + 1, 2q + 8, 2q + 9, and byte permutes pair
 //                them.  Column 64 c + 8 g + 2 i + r is row g + 8 r of product i.
 //
-// So no lane reads what another copied: cp.async into a ring of a lane's own,
-// whose completion a lane waits for alone (no barrier in the loop), and
-// conflict-free 16-byte shared-memory accesses.  tcgen05 would want 64 or 128
-// rows of A where there are 1 to 16 query heads, and its shared-memory
-// operands would cost a barrier a tile, for a product that is not the limit.
+// A warp copies its own 16 rows (cp.async into a ring of its own) and waits for
+// them alone: no block barrier in the loop, no transposition, conflict-free
+// 16-byte shared-memory reads.  tcgen05 would want 64 or 128 rows of A where
+// there are 1 to 16 query heads, and a barrier a tile, for a product that is
+// not the limit.
 //
 // P is multiplied as the sum of two bf16 numbers (p rounded, and what is left
 // rounded): the second product costs nothing beside the loads, and leaves the
@@ -223,11 +221,20 @@ struct Mma {
   static constexpr int kRows = 16;             // of a tile, a warp
   static constexpr int kTile = kWarps * kRows;
   static constexpr int kVW = D % 64 ? 32 : 64; // columns of V in a block: 8 or 16 bytes a lane
-  static constexpr int kStageBytes = kRows * D * 2 * 2;  // K and V rows of a warp
+  static constexpr int kPieces = D / 8;        // of 16 bytes in a row
+  // 16 bytes between rows: the 8 lanes of an access's quarter then take 8
+  // different groups of 4 banks, of K (2 keys x 4 pieces, 2 apart) as of V (4 pairs
+  // of keys, 2 pieces)
+  static constexpr int kPitch = D * 2 + 16;
+  static constexpr int kStageBytes = 2 * kRows * kPitch;  // K and V rows of a warp
   // Bytes in flight an SM: (stages - 1) of blocks x warps x 64 d.  Shared
   // memory holds 228 KB an SM, and 8 to 16 warps keep the issue slots fed.
   static constexpr int kBlocks = D == 32 ? 4 : D == 64 ? 3 : D == 256 ? 1 : 2;  // an SM
-  static constexpr int kStages = D == 128 || D == 256 ? 3 : 4;
+  static constexpr int kStages = D == 32 || D == 96 ? 4 : 3;
+  // the place in a row of the piece that lane q multiplies in step c, in pieces
+  __host__ __device__ static constexpr int k_piece(int c, int q) {
+    return c == D / 32 - 1 && c % 2 == 0 ? 4 * c + q : 8 * (c / 2) + 2 * q + c % 2;
+  }
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kPad = kVW + 4;         // floats of a row of the exchange buffer
   static constexpr int kExchange = kWarps * 8 * kPad * 4;
@@ -236,10 +243,6 @@ struct Mma {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, bool on) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const char* src, bool on) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -302,35 +305,22 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     row_off = (int64_t)(load.item / a.split) * a.ph + (int64_t)r * a.pn;
   };
   // Copies of the tile looked up, into stage st; returns which of its 16 rows
-  // are there.  Rows that are not are filled with zeros, and not read.
+  // are there.  Rows that are not are filled with zeros, and not read.  The
+  // pieces of a row go to neighbouring lanes, so that a request takes whole
+  // lines of a row.
   auto copy = [&](int st) -> uint32_t {
     const bool ok = row_in && row_page >= 0 && row_page < a.num_pages;
     if (row_in && !ok) report_pages(a.status);
     const int64_t off = ok ? row_page * a.pp + row_off : 0;
     const uint32_t seen = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-    const uint32_t k_at = ring + st * M::kStageBytes + lane * 16;
+    const uint32_t to = ring + st * M::kStageBytes;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t o = __shfl_sync(0xffffffffu, off, g + 8 * r);
-      const char* src = a.K + o + q * 16;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) cp_async16(k_at + (c * 2 + r) * 512, src + c * 64, (seen >> (g + 8 * r)) & 1);
-    }
-    constexpr int kLaneV = VW / 4;  // bytes of V a lane copies of a block's row
-    const uint32_t v_at = ring + st * M::kStageBytes + M::kStageBytes / 2 + lane * kLaneV;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 2 * q + (r & 1) + (r >> 1) * 8;
-      const int64_t o = __shfl_sync(0xffffffffu, off, row);
-      const char* src = a.V + o + g * kLaneV;
-#pragma unroll
-      for (int c = 0; c < D / VW; ++c) {
-        const uint32_t dst = v_at + (c * 4 + r) * 32 * kLaneV;
-        if constexpr (VW == 64)
-          cp_async16(dst, src + c * 128, (seen >> row) & 1);
-        else
-          cp_async8(dst, src + c * 64, (seen >> row) & 1);
-      }
+    for (int i = 0; i < M::kPieces / 2; ++i) {
+      const int row = (i * 32 + lane) / M::kPieces, piece = (i * 32 + lane) % M::kPieces;
+      const int64_t from = __shfl_sync(0xffffffffu, off, row) + piece * 16;
+      const bool on = (seen >> row) & 1;
+      cp_async16(to + row * M::kPitch + piece * 16, a.K + from, on);
+      cp_async16(to + M::kStageBytes / 2 + row * M::kPitch + piece * 16, a.V + from, on);
     }
     return seen;
   };
@@ -361,20 +351,20 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
 
   for (int i = 0; i < count; ++i) {
     cp_wait<kStages - 2>();
+    __syncwarp();  // the warp's copies are all there, and its reads of the stage refilled next are done
     const uint32_t seen = (uint32_t)seen_queue & 0xffffu;
-    // the stage read one iteration ago: every lane is done with its own pieces
     produce(stage == 0 ? kStages - 1 : stage - 1);
 
     if (i == 0 || at.t == 0) {
       int kv, heads;
       const int h0 = item_first_head(a, at.item, &kv, &heads);
-      const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh + q * 16;
+      const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
         const bool on = g + 8 * u < heads;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(row + (g + 8 * u) * a.qh + c * 64))
+          const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(row + (g + 8 * u) * a.qh + M::k_piece(c, q) * 16))
                              : make_uint4(0, 0, 0, 0);
           qf[u][c][0] = x.x, qf[u][c][1] = x.y, qf[u][c][2] = x.z, qf[u][c][3] = x.w;
         }
@@ -391,11 +381,11 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     }
 
     if (seen) {
-      const uint32_t k_at = ring + stage * M::kStageBytes + lane * 16;
+      const uint32_t k_at = ring + stage * M::kStageBytes + g * M::kPitch;
       float s[2][4] = {};
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        const uint4 k0 = lds16(k_at + c * 1024), k1 = lds16(k_at + c * 1024 + 512);
+        const uint4 k0 = lds16(k_at + M::k_piece(c, q) * 16), k1 = lds16(k_at + 8 * M::kPitch + M::k_piece(c, q) * 16);
         const uint32_t b0 = NH > 1 ? qf[NH - 1][c][0] : 0u, b1 = NH > 1 ? qf[NH - 1][c][1] : 0u;
         const uint32_t b2 = NH > 1 ? qf[NH - 1][c][2] : 0u, b3 = NH > 1 ? qf[NH - 1][c][3] : 0u;
         mma16816(s[0], qf[0][c][0], b0, qf[0][c][1], b1, k0.x, k0.y);
@@ -448,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
         }
       }
       constexpr int kLaneV = VW / 4, kWords = VW / 16;
-      const uint32_t v_at = ring + stage * M::kStageBytes + M::kStageBytes / 2 + lane * kLaneV;
+      const uint32_t v_at = ring + stage * M::kStageBytes + M::kStageBytes / 2 + 2 * q * M::kPitch + g * kLaneV;
 #pragma unroll
       for (int c = 0; c < D / VW; ++c) {
         uint32_t w[4][kWords];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t from = v_at + (c * 4 + r) * 32 * kLaneV;
+          const uint32_t from = v_at + ((r & 1) + (r >> 1) * 8) * M::kPitch + c * VW * 2;
           if constexpr (VW == 64) {
             const uint4 x = lds16(from);
             w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
