@@ -86,11 +86,20 @@ __device__ __forceinline__ int tiles_of(int rows) {
   return rows <= kTile ? 1 : (rows + kTile - 1) / kTile;  // an empty item still writes its zeros
 }
 
+// What beginning and ending an item costs, in tiles: an item of n tiles is
+// kItemCost + n units of work, and the runs are of equal units.  A run that
+// begins inside the first kItemCost units of an item begins with its first
+// tile.  So a run may be empty only between two items, never inside one.
+
+
+#endif
+constexpr int kItemCost = 1;
+
 struct Share {
-  int64_t total;       // tiles of all items
+  int64_t total;       // units of all items
   int64_t first, end;  // this block's run of them
-  int64_t base;        // number of the first tile of sequence s
-  int s;               // sequence of the first tile
+  int64_t base;        // the first unit of sequence s
+  int s;               // sequence of the first unit
   int workers;         // blocks that have a run
 };
 
@@ -107,16 +116,15 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sums) {
   return x;
 }
 
-// False: more blocks than tiles, and this one has none.
+// False: more blocks than units, and this one has none.
 template <int kTile>
 __device__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
   __shared__ int64_t found_base;
   __shared__ int found_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t mine = 0;
-  for (int s = threadIdx.x; s < a.S; s += kThreads) mine += (int64_t)tiles_of<kTile>(rows_of(a, s)) * a.items;
+  for (int s = threadIdx.x; s < a.S; s += kThreads) mine += (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items;
   out->total = block_sum(mine, sums);
-  // no run is empty, so that a joined item's parts are all there
   out->workers = (int)(out->total < a.workers ? out->total : a.workers);
   const int w = blockIdx.x;
   if (w >= out->workers) return false;
@@ -125,7 +133,7 @@ __device__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
   int64_t before = 0;
   for (int at = 0; at < a.S; at += kThreads) {
     const int s = at + threadIdx.x;
-    const int64_t n = s < a.S ? (int64_t)tiles_of<kTile>(rows_of(a, s)) * a.items : 0;
+    const int64_t n = s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
     int64_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -152,21 +160,27 @@ __device__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
   return true;
 }
 
-// A place in the row of tiles: tile t of item `item` of sequence s.
+// A place in the row of tiles: tile t of item `item` of sequence s, which is
+// unit `unit` of all.
 template <int kTile>
 struct Place {
   int s, item, t, rows, tiles;
+  int64_t unit;
   __device__ __forceinline__ void set(const DecodeParams& a, const Share& sh) {
     s = sh.s;
     rows = rows_of(a, s);
     tiles = tiles_of<kTile>(rows);
     const int64_t k = sh.first - sh.base;
-    item = (int)(k / tiles);
-    t = (int)(k - (int64_t)item * tiles);
+    item = (int)(k / (kItemCost + tiles));
+    const int64_t begin = (int64_t)item * (kItemCost + tiles);
+    t = max((int)(k - begin) - kItemCost, 0);
+    unit = sh.base + begin + kItemCost + t;
   }
   __device__ __forceinline__ void next(const DecodeParams& a) {
+    ++unit;
     if (++t < tiles) return;
     t = 0;
+    unit += kItemCost;
     if (++item < a.items) return;
     item = 0;
     if (++s < a.S) {
@@ -245,6 +259,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, bool o
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l1(const char* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -282,14 +297,17 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   float* exchange = reinterpret_cast<float*>(smem + M::kRing);
 
   Share share;
-  if (!share_out<kTile>(a, sums, &share)) {
+  Place<kTile> load, at;
+  bool some = share_out<kTile>(a, sums, &share);
+  if (some) {
+    at.set(a, share);
+    some = at.unit < share.end;
+  }
+  if (!some) {
     if (threadIdx.x == 0 && a.records) a.records[blockIdx.x].item = -1;
     return;
   }
-  const int count = (int)(share.end - share.first);
-  Place<kTile> load, at;
-  load.set(a, share);
-  at = load;
+  load = at;
 
   // The row that this lane looks up in the tile that is loaded next: its page
   // is asked for one tile ahead of the copies that need it.
@@ -303,6 +321,12 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     row_in = j < load.rows;
     row_page = row_in ? __ldg(a.table + load.s * a.table_stride + col) : -1;
     row_off = (int64_t)(load.item / a.split) * a.ph + (int64_t)r * a.pn;
+    if (load.t == 0) {  // a new item: its queries into L1
+      int kv, heads;
+      const char* row = a.Q + load.s * a.qs + (int64_t)item_first_head(a, load.item, &kv, &heads) * a.qh;
+      constexpr int kLines = (D * 2 + 127) / 128;
+      for (int k = lane; k < heads * kLines; k += 32) prefetch_l1(row + (k / kLines) * a.qh + (k % kLines) * 128);
+    }
   };
   // Copies of the tile looked up, into stage st; returns which of its 16 rows
   // are there.  Rows that are not are filled with zeros, and not read.  The
@@ -326,15 +350,12 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   };
   // seen masks of the tiles in flight, the oldest in the low 16 bits
   uint64_t seen_queue = 0;
-  int issued = 0;
   auto produce = [&](int st) {
     uint32_t seen = 0;
-    if (issued < count) {
+    if (load.unit < share.end) {
       seen = copy(st);
-      if (++issued < count) {
-        load.next(a);
-        look_up();
-      }
+      load.next(a);
+      if (load.unit < share.end) look_up();
     }
     cp_commit();
     seen_queue = (seen_queue >> 16) | ((uint64_t)seen << (16 * (kStages - 2)));
@@ -348,14 +369,18 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   float m[NH], l[NH];                 // of heads g, g + 8; l of this lane's keys alone
   int begin = at.t;                   // tile at which the item (or this block's part of it) began
   int stage = 0;
+  bool first = true, last = false;    // item of the run
 
-  for (int i = 0; i < count; ++i) {
+  for (bool fresh = true; !last; fresh = false) {
+    Place<kTile> next = at;
+    next.next(a);
+    last = next.unit >= share.end;
     cp_wait<kStages - 2>();
     __syncwarp();  // the warp's copies are all there, and its reads of the stage refilled next are done
     const uint32_t seen = (uint32_t)seen_queue & 0xffffu;
     produce(stage == 0 ? kStages - 1 : stage - 1);
 
-    if (i == 0 || at.t == 0) {
+    if (fresh || at.t == 0) {
       int kv, heads;
       const int h0 = item_first_head(a, at.item, &kv, &heads);
       const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
@@ -467,13 +492,14 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
-    if (at.t + 1 == at.tiles || i + 1 == count) {
+    if (at.t + 1 == at.tiles || last) {
       // ---- the item ends here, or goes on in the next block's run
-      if (i + 1 == count) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      if (last) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       const bool whole = begin == 0 && at.t + 1 == at.tiles;
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
-      const int slot = 2 * blockIdx.x + (i > at.t - begin ? 1 : 0);
+      const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+      first = false;
       int kv, heads;
       const int h0 = item_first_head(a, at.item, &kv, &heads);
       __syncthreads();  // ml and the exchange buffer have been read
@@ -541,19 +567,19 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             a.part_ml[(int64_t)slot * kHeads + 8 * u + head] = make_float2(top, sum);
         }
       }
-      if (i + 1 == count && threadIdx.x == 0 && a.records) {
+      if (last && threadIdx.x == 0 && a.records) {
         Record r;
         // ours to join if it began here and goes on
         r.item = begin == 0 && at.t + 1 != at.tiles ? at.s * a.items + at.item : -1;
         r.first = slot;
         r.pad = 0;
-        // the block whose run holds the item's last tile, tile end - 1 of all
-        const int64_t end = share.first + i + (at.tiles - at.t);
+        // the block whose run holds the item's last tile, unit end - 1 of all
+        const int64_t end = at.unit + (at.tiles - at.t);
         r.following = (int)((end * share.workers - 1) / share.total) - (int)blockIdx.x;
         a.records[blockIdx.x] = r;
       }
     }
-    at.next(a);
+    at = next;
   }
 }
 
