@@ -89,10 +89,9 @@ __device__ __forceinline__ int tiles_of(int rows) {
 // What beginning and ending an item costs, in tiles: an item of n tiles is
 // kItemCost + n units of work, and the runs are of equal units.  A run that
 // begins inside the first kItemCost units of an item begins with its first
-// tile.  So a run may be empty only between two items, never inside one.
-
-
-#endif
+// tile.  So a run may be empty only between two items, never inside one.  1 is
+// what measured best: 32 sequences of up to 2048 rows, 32 heads of d 64 (items
+// of up to 32 tiles) took 56.5 us with 0, 46.3 with 1, 46.5 with 2, 47.4 with 3.
 constexpr int kItemCost = 1;
 
 struct Share {
