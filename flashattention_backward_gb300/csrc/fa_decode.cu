@@ -42,13 +42,14 @@ constexpr int kMaxWorkers = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The item whose first tile lies in a block's run and whose last does not: the
-// block of the join with the same number adds its parts up.
+// An item whose first tile lies in a block's run and whose last does not, for
+// the join.  At most one a block and at most one an item: there are as many
+// records as blocks or as items, whichever is less, numbered by block or by item.
 struct Record {
   int item;       // s * items + index within the sequence; -1: none
-  int first;      // the first part; the others are part 2 (w + k) of the k-th block behind
-  int following;  // how many others
-  int pad;
+  int block;      // whose run the item begins in
+  int slot;       // the block's part of it, 0 or 1; the others are part 0 of the blocks behind
+  int following;  // how many of those
 };
 
 struct DecodeParams {
@@ -57,7 +58,8 @@ struct DecodeParams {
   float* L;
   const int32_t *table, *lengths;
   int32_t* status;
-  Record* records;    // [workers]; null when no item has two tiles: nothing to join
+  Record* records;    // null when no item has two tiles: nothing to join
+  int by_item;        // records are numbered by item
   float2* part_ml;    // [2 workers][heads of an item]
   float* part_o;      // [2 workers][heads of an item][d]
   FastDiv page_rows;
@@ -102,56 +104,64 @@ struct Share {
   int workers;         // blocks that have a run
 };
 
-// Sum over the block; sums: kWarps entries.
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sums) {
+// Sum over the threads before this one (return value) and over the block;
+// sums: kWarps entries of shared memory.
+__device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* sums, int64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the last call's readers of sums are done
+  if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
+  x -= n;
+  *all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) x += sums[w];
+  for (int k = 0; k < kWarps; ++k) {
+    if (k < warp) x += sums[k];
+    *all += sums[k];
+  }
   return x;
 }
 
-// False: more blocks than units, and this one has none.
+// This block's run; false if there are more blocks than units, and it has
+// none.  Thread t looks at sequences t, t + kThreads, ...: up to kThreads of
+// them are loaded and summed once, of more the sums are taken twice, for the
+// total and for the run's place.
 template <int kTile>
-__device__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
+__device__ __forceinline__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
   __shared__ int64_t found_base;
   __shared__ int found_s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t mine = 0;
-  for (int s = threadIdx.x; s < a.S; s += kThreads) mine += (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items;
-  out->total = block_sum(mine, sums);
+  const auto units = [&](int s) -> int64_t {
+    return s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
+  };
+  int64_t n = units(threadIdx.x), more = 0, all;
+  int64_t lo = block_scan(n, sums, &all);
+  out->total = all;
+  if (a.S > kThreads) {
+    for (int s = kThreads + threadIdx.x; s < a.S; s += kThreads) more += units(s);
+    block_scan(more, sums, &more);
+    out->total += more;
+  }
   out->workers = (int)(out->total < a.workers ? out->total : a.workers);
   const int w = blockIdx.x;
   if (w >= out->workers) return false;
   out->first = out->total * w / out->workers;
   out->end = out->total * (w + 1) / out->workers;
-  int64_t before = 0;
-  for (int at = 0; at < a.S; at += kThreads) {
-    const int s = at + threadIdx.x;
-    const int64_t n = s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
-    int64_t x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    int64_t lo = before + x - n;
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) lo += sums[k];
-      before += sums[k];
-    }
+  for (int at = 0;;) {
     if (n > 0 && lo <= out->first && out->first < lo + n) {
       found_base = lo;
-      found_s = s;
+      found_s = at + threadIdx.x;
     }
-    if (before > out->first) break;
+    if (all > out->first) break;
+    at += kThreads;
+    n = units(at + threadIdx.x);
+    int64_t here;
+    lo = all + block_scan(n, sums, &here);
+    all += here;
   }
   __syncthreads();
   out->base = found_base;
@@ -302,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     at.set(a, share);
     some = at.unit < share.end;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
   if (!some) {
-    if (threadIdx.x == 0 && a.records) a.records[blockIdx.x].item = -1;
+    if (threadIdx.x == 0 && a.records && !a.by_item) a.records[blockIdx.x].item = -1;
     return;
   }
   load = at;
@@ -493,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
 
     if (at.t + 1 == at.tiles || last) {
       // ---- the item ends here, or goes on in the next block's run
-      if (last) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       const bool whole = begin == 0 && at.t + 1 == at.tiles;
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
@@ -566,16 +576,17 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             a.part_ml[(int64_t)slot * kHeads + 8 * u + head] = make_float2(top, sum);
         }
       }
-      if (last && threadIdx.x == 0 && a.records) {
+      if (threadIdx.x == 0 && a.records && (a.by_item ? begin == 0 : last)) {
         Record r;
-        // ours to join if it began here and goes on
-        r.item = begin == 0 && at.t + 1 != at.tiles ? at.s * a.items + at.item : -1;
-        r.first = slot;
-        r.pad = 0;
+        const int item = at.s * a.items + at.item;
+        // to be joined if it began here and goes on
+        r.item = begin == 0 && at.t + 1 != at.tiles ? item : -1;
+        r.block = blockIdx.x;
+        r.slot = slot & 1;
         // the block whose run holds the item's last tile, unit end - 1 of all
         const int64_t end = at.unit + (at.tiles - at.t);
         r.following = (int)((end * share.workers - 1) / share.total) - (int)blockIdx.x;
-        a.records[blockIdx.x] = r;
+        a.records[a.by_item ? item : blockIdx.x] = r;
       }
     }
     at = next;
@@ -646,14 +657,18 @@ __global__ void __launch_bounds__(kThreads) decode_fp32_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------- joining
-// Block (w, h): head h of the item that record w names.  D / 4 threads hold a
-// row of o, and the block's groups of so many threads take the parts in turn.
+// Block (r, h): head h of the item that record r names.  D / 4 threads hold a
+// row of o, and the block's groups of so many threads take the parts in turn,
+// kAhead loads at a time: what bounds the join is the latency of two dependent
+// loads, the record's and the parts', and of its own launch.
+constexpr int kJoinThreads = 256;
+
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_constant__ DecodeParams a, int part_heads) {
-  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
-  __shared__ float red[kWarps];
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
+                                                                   int part_heads) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
   __shared__ float4 os[kGroups][kLanes];
-  __shared__ float ls[kGroups];
+  __shared__ float2 mls[kGroups];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Record r = a.records[blockIdx.x];
   if (r.item < 0) return;
@@ -661,48 +676,60 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const __grid_cons
   int kv, heads;
   const int h = item_first_head(a, r.item - s * a.items, &kv, &heads) + head;
   if (head >= heads) return;
-  auto part = [&](int k) -> int64_t {
-    return (int64_t)(k == 0 ? r.first : 2 * ((int)blockIdx.x + k)) * part_heads + head;
-  };
-  float top = -INFINITY;
-  for (int k = threadIdx.x; k <= r.following; k += kThreads) top = fmaxf(top, a.part_ml[part(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[w]);
-  const float base = base_of(top);
   const int grp = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   if (grp < kGroups) {
-    for (int k = grp; k <= r.following; k += kGroups) {
-      const int64_t p = part(k);
-      const float2 ml = a.part_ml[p];
-      const float f = ptx::ex2(ml.x - base);
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
-      o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-      l = fmaf(f, ml.y, l);
+    for (int k0 = grp; k0 <= r.following; k0 += kGroups * kAhead) {
+      float2 ml[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int k = k0 + e * kGroups;
+        ml[e] = make_float2(-INFINITY, 0.f);
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k > r.following) continue;
+        const int64_t p = (int64_t)(2 * (r.block + k) + (k == 0 ? r.slot : 0)) * part_heads + head;
+        ml[e] = a.part_ml[p];
+        v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) top = fmaxf(top, ml[e].x);
+      const float base = base_of(top), f = ptx::ex2(m - base);
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const float w = ptx::ex2(ml[e].x - base);
+        o.x = fmaf(w, v[e].x, o.x), o.y = fmaf(w, v[e].y, o.y), o.z = fmaf(w, v[e].z, o.z), o.w = fmaf(w, v[e].w, o.w);
+        l = fmaf(w, ml[e].y, l);
+      }
+      m = top;
     }
     os[grp][x] = o;
-    if (x == 0) ls[grp] = l;
+    if (x == 0) mls[grp] = make_float2(m, l);
   }
   __syncthreads();
   if (threadIdx.x >= kLanes) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) m = fmaxf(m, mls[k].x);
+  const float base = base_of(m);
   o = make_float4(0.f, 0.f, 0.f, 0.f);
   l = 0.f;
-#pragma unroll
+#pragma unroll 8
   for (int k = 0; k < kGroups; ++k) {
     const float4 v = os[k][x];
-    o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-    l += ls[k];
+    const float w = ptx::ex2(mls[k].x - base);
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    l = fmaf(w, mls[k].y, l);
   }
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
   o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   store4<T>(a.O + s * a.os + (int64_t)h * a.oh, 4 * x, o);
-  if (threadIdx.x == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (top + log2f(l)) * kLn2;
+  if (threadIdx.x == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ----------------------------------------------------------------- launching
@@ -732,10 +759,10 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 template <class T, int D>
 cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.workers, (unsigned)a.item_heads);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(a.by_item ? a.S * a.items : a.workers), (unsigned)a.item_heads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
-  // may start while the last blocks of the kernel before it finish, and waits for them itself
+  // its blocks may be there before the kernel in front ends, and wait for that themselves
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -766,6 +793,7 @@ cudaError_t launch_mma(const Cut& k, DecodeParams a, cudaStream_t s) {
   const int resident = sm_count() * M::kBlocks;
   if (resident < 1) return cudaErrorInvalidDevice;
   if (a.workers > resident) a.workers = resident;
+  a.by_item = (int64_t)a.S * a.items <= a.workers;
   decode_mma_kernel<D, NH><<<a.workers, kThreads, M::kSmem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
