@@ -42,24 +42,12 @@ constexpr int kMaxWorkers = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// An item whose first tile lies in a block's run and whose last does not, for
-// the join.  At most one a block and at most one an item: there are as many
-// records as blocks or as items, whichever is less, numbered by block or by item.
-struct Record {
-  int item;       // s * items + index within the sequence; -1: none
-  int block;      // whose run the item begins in
-  int slot;       // the block's part of it, 0 or 1; the others are part 0 of the blocks behind
-  int following;  // how many of those
-};
-
 struct DecodeParams {
   const char *Q, *K, *V;
   char* O;
   float* L;
   const int32_t *table, *lengths;
   int32_t* status;
-  Record* records;    // null when no item has two tiles: nothing to join
-  int by_item;        // records are numbered by item
   float2* part_ml;    // [2 workers][heads of an item]
   float* part_o;      // [2 workers][heads of an item][d]
   FastDiv page_rows;
@@ -97,15 +85,16 @@ __device__ __forceinline__ int tiles_of(int rows) {
 constexpr int kItemCost = 1;
 
 struct Share {
-  int64_t total;       // units of all items
-  int64_t first, end;  // this block's run of them
-  int64_t base;        // the first unit of sequence s
-  int s;               // sequence of the first unit
-  int workers;         // blocks that have a run
+  int64_t total;  // units of all items
+  int workers;    // blocks that have a run
+  __device__ __forceinline__ int64_t first(int w) const { return total * w / workers; }
+  // the block whose run holds unit x: the largest w with first(w) <= x
+  __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * workers - 1) / total); }
 };
 
-// Sum over the threads before this one (return value) and over the block;
-// sums: kWarps entries of shared memory.
+// Sum over the threads before this one (return value) and over the block of NT
+// threads; sums: NT / 32 entries of shared memory.
+template <int NT>
 __device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* sums, int64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = n;
@@ -120,54 +109,62 @@ __device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* sums, int64_t*
   x -= n;
   *all = 0;
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
+  for (int k = 0; k < NT / 32; ++k) {
     if (k < warp) x += sums[k];
     *all += sums[k];
   }
   return x;
 }
 
-// This block's run; false if there are more blocks than units, and it has
-// none.  Thread t looks at sequences t, t + kThreads, ...: up to kThreads of
-// them are loaded and summed once, of more the sums are taken twice, for the
-// total and for the run's place.
-template <int kTile>
-__device__ __forceinline__ bool share_out(const DecodeParams& a, int64_t* sums, Share* out) {
-  __shared__ int64_t found_base;
-  __shared__ int found_s;
-  const auto units = [&](int s) -> int64_t {
+// The sequences' units, summed over a block of NT threads.  Thread t looks at
+// sequences t, t + NT, ...: up to NT of them are loaded and summed once, of more
+// the sums are taken twice, for the total and for a place among them.
+template <int kTile, int NT>
+struct Units {
+  const DecodeParams& a;
+  int64_t* sums;     // NT / 32 entries of shared memory
+  int64_t n, lo, all;  // of the first NT sequences: this thread's, those before it, all
+  __device__ __forceinline__ int64_t of(int s) const {
     return s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
-  };
-  int64_t n = units(threadIdx.x), more = 0, all;
-  int64_t lo = block_scan(n, sums, &all);
-  out->total = all;
-  if (a.S > kThreads) {
-    for (int s = kThreads + threadIdx.x; s < a.S; s += kThreads) more += units(s);
-    block_scan(more, sums, &more);
-    out->total += more;
   }
-  out->workers = (int)(out->total < a.workers ? out->total : a.workers);
-  const int w = blockIdx.x;
-  if (w >= out->workers) return false;
-  out->first = out->total * w / out->workers;
-  out->end = out->total * (w + 1) / out->workers;
-  for (int at = 0;;) {
-    if (n > 0 && lo <= out->first && out->first < lo + n) {
-      found_base = lo;
-      found_s = at + threadIdx.x;
+  __device__ __forceinline__ Units(const DecodeParams& p, int64_t* shared) : a(p), sums(shared) {
+    n = of(threadIdx.x);
+    lo = block_scan<NT>(n, sums, &all);
+  }
+  __device__ __forceinline__ Share share() {
+    Share sh;
+    sh.total = all;
+    if (a.S > NT) {
+      int64_t more = 0;
+      for (int s = NT + threadIdx.x; s < a.S; s += NT) more += of(s);
+      block_scan<NT>(more, sums, &more);
+      sh.total += more;
     }
-    if (all > out->first) break;
-    at += kThreads;
-    n = units(at + threadIdx.x);
-    int64_t here;
-    lo = all + block_scan(n, sums, &here);
-    all += here;
+    sh.workers = (int)(sh.total < a.workers ? sh.total : a.workers);
+    return sh;
   }
-  __syncthreads();
-  out->base = found_base;
-  out->s = found_s;
-  return true;
-}
+  // The sequence that holds unit x (x < 0: sequence `want`), and its first unit.
+  __device__ __forceinline__ int find(int64_t x, int want, int64_t* base) {
+    __shared__ int64_t found_base;
+    __shared__ int found;
+    for (int at = 0;;) {
+      const int s = at + threadIdx.x;
+      if (x < 0 ? s == want : n > 0 && lo <= x && x < lo + n) {
+        found_base = lo;
+        found = s;
+      }
+      at += NT;
+      if (x < 0 ? want < at : all > x) break;
+      n = of(at + threadIdx.x);
+      int64_t here;
+      lo = all + block_scan<NT>(n, sums, &here);
+      all += here;
+    }
+    __syncthreads();
+    *base = found_base;
+    return found;
+  }
+};
 
 // A place in the row of tiles: tile t of item `item` of sequence s, which is
 // unit `unit` of all.
@@ -175,15 +172,15 @@ template <int kTile>
 struct Place {
   int s, item, t, rows, tiles;
   int64_t unit;
-  __device__ __forceinline__ void set(const DecodeParams& a, const Share& sh) {
-    s = sh.s;
+  // the first tile at or behind unit x of sequence s, whose first unit is base
+  __device__ __forceinline__ void set(const DecodeParams& a, int seq, int64_t base, int64_t x) {
+    s = seq;
     rows = rows_of(a, s);
     tiles = tiles_of<kTile>(rows);
-    const int64_t k = sh.first - sh.base;
-    item = (int)(k / (kItemCost + tiles));
-    const int64_t begin = (int64_t)item * (kItemCost + tiles);
-    t = max((int)(k - begin) - kItemCost, 0);
-    unit = sh.base + begin + kItemCost + t;
+    item = (int)((x - base) / (kItemCost + tiles));
+    const int64_t begin = base + (int64_t)item * (kItemCost + tiles);
+    t = max((int)(x - begin) - kItemCost, 0);
+    unit = begin + kItemCost + t;
   }
   __device__ __forceinline__ void next(const DecodeParams& a) {
     ++unit;
@@ -305,18 +302,20 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * M::kStageBytes;
   float* exchange = reinterpret_cast<float*>(smem + M::kRing);
 
-  Share share;
-  Place<kTile> load, at;
-  bool some = share_out<kTile>(a, sums, &share);
-  if (some) {
-    at.set(a, share);
-    some = at.unit < share.end;
-  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
-  if (!some) {
-    if (threadIdx.x == 0 && a.records && !a.by_item) a.records[blockIdx.x].item = -1;
-    return;
+  Place<kTile> load, at;
+  int64_t end;
+  {
+    Units<kTile, kThreads> units(a, sums);
+    const Share share = units.share();
+    if ((int)blockIdx.x >= share.workers) return;
+    const int64_t x = share.first(blockIdx.x);
+    end = share.first(blockIdx.x + 1);
+    int64_t base;
+    const int s = units.find(x, 0, &base);
+    at.set(a, s, base, x);
   }
+  if (at.unit >= end) return;
   load = at;
 
   // The row that this lane looks up in the tile that is loaded next: its page
@@ -362,10 +361,10 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   uint64_t seen_queue = 0;
   auto produce = [&](int st) {
     uint32_t seen = 0;
-    if (load.unit < share.end) {
+    if (load.unit < end) {
       seen = copy(st);
       load.next(a);
-      if (load.unit < share.end) look_up();
+      if (load.unit < end) look_up();
     }
     cp_commit();
     seen_queue = (seen_queue >> 16) | ((uint64_t)seen << (16 * (kStages - 2)));
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   for (bool fresh = true; !last; fresh = false) {
     Place<kTile> next = at;
     next.next(a);
-    last = next.unit >= share.end;
+    last = next.unit >= end;
     cp_wait<kStages - 2>();
     __syncwarp();  // the warp's copies are all there, and its reads of the stage refilled next are done
     const uint32_t seen = (uint32_t)seen_queue & 0xffffu;
@@ -576,18 +575,6 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             a.part_ml[(int64_t)slot * kHeads + 8 * u + head] = make_float2(top, sum);
         }
       }
-      if (threadIdx.x == 0 && a.records && (a.by_item ? begin == 0 : last)) {
-        Record r;
-        const int item = at.s * a.items + at.item;
-        // to be joined if it began here and goes on
-        r.item = begin == 0 && at.t + 1 != at.tiles ? item : -1;
-        r.block = blockIdx.x;
-        r.slot = slot & 1;
-        // the block whose run holds the item's last tile, unit end - 1 of all
-        const int64_t end = at.unit + (at.tiles - at.t);
-        r.following = (int)((end * share.workers - 1) / share.total) - (int)blockIdx.x;
-        a.records[a.by_item ? item : blockIdx.x] = r;
-      }
     }
     at = next;
   }
@@ -657,30 +644,55 @@ __global__ void __launch_bounds__(kThreads) decode_fp32_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------- joining
-// Block (r, h): head h of the item that record r names.  D / 4 threads hold a
-// row of o, and the block's groups of so many threads take the parts in turn,
-// kAhead loads at a time: what bounds the join is the latency of two dependent
-// loads, the record's and the parts', and of its own launch.
+// Block (r, h): head h of one item, item r if there are no more items than runs
+// (by_item), else the one that run r ends inside of if it also begins there:
+// every item of several parts has one such run.  Which parts it has follows
+// from the lengths, so the blocks find that out while the kernel in front
+// still runs.  D / 4 threads hold a row of o, and the block's groups of so many
+// threads take the parts in turn, kAhead loads at a time.
 constexpr int kJoinThreads = 256;
 
-template <class T, int D>
+template <class T, int D, int kTile>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
-                                                                   int part_heads) {
+                                                                   int part_heads, int by_item) {
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
   __shared__ float4 os[kGroups][kLanes];
   __shared__ float2 mls[kGroups];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Record r = a.records[blockIdx.x];
-  if (r.item < 0) return;
-  const int s = r.item / a.items, head = blockIdx.y;
+  __shared__ int64_t sums[kJoinThreads / 32];
+  int s = 0, item = 0, block = 0, slot = 0, following = 0;
+  {
+    Units<kTile, kJoinThreads> units(a, sums);
+    const Share share = units.share();
+    int64_t base = 0;
+    if (by_item) {
+      s = blockIdx.x / a.items;
+      item = blockIdx.x - s * a.items;
+      units.find(-1, s, &base);
+    } else if ((int)blockIdx.x < share.workers) {
+      const int64_t x = share.first(blockIdx.x + 1) - 1;
+      s = units.find(x, 0, &base);
+      item = (int)((x - base) / (kItemCost + tiles_of<kTile>(rows_of(a, s))));
+    }
+    const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
+    block = share.block_of(begin + kItemCost);
+    if (by_item || block == (int)blockIdx.x) following = share.block_of(begin + kItemCost + tiles - 1) - block;
+    // a run that holds tiles before the item has it as its second part
+    slot = share.first(block) < begin ? 1 : 0;
+  }
+  const int head = blockIdx.y;
   int kv, heads;
-  const int h = item_first_head(a, r.item - s * a.items, &kv, &heads) + head;
-  if (head >= heads) return;
+  const int h = item_first_head(a, item, &kv, &heads) + head;
+  const bool some = following > 0 && head < heads;
+  // What comes after this kernel on its stream waits for this kernel alone, so
+  // it may not end before the one in front, even if it has nothing to join:
+  // block (0, 0) waits in any case.
+  if (some || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!some) return;
   const int grp = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
   if (grp < kGroups) {
-    for (int k0 = grp; k0 <= r.following; k0 += kGroups * kAhead) {
+    for (int k0 = grp; k0 <= following; k0 += kGroups * kAhead) {
       float2 ml[kAhead];
       float4 v[kAhead];
 #pragma unroll
@@ -688,8 +700,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         const int k = k0 + e * kGroups;
         ml[e] = make_float2(-INFINITY, 0.f);
         v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k > r.following) continue;
-        const int64_t p = (int64_t)(2 * (r.block + k) + (k == 0 ? r.slot : 0)) * part_heads + head;
+        if (k > following) continue;
+        const int64_t p = (int64_t)(2 * (block + k) + (k == 0 ? slot : 0)) * part_heads + head;
         ml[e] = a.part_ml[p];
         v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
       }
@@ -754,12 +766,11 @@ Cut cut_of(const fa_cache& c, int H) {
   return k;
 }
 
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
-
-template <class T, int D>
+template <class T, int D, int kTile>
 cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.by_item ? a.S * a.items : a.workers), (unsigned)a.item_heads);
+  const int by_item = (int64_t)a.S * a.items <= a.workers;
+  cfg.gridDim = dim3((unsigned)(by_item ? a.S * a.items : a.workers), (unsigned)a.item_heads);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   // its blocks may be there before the kernel in front ends, and wait for that themselves
@@ -768,7 +779,7 @@ cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D>, a, part_heads);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, kTile>, a, part_heads, by_item);
 }
 
 // Raises a kernel's shared-memory limit, once a device.
@@ -793,11 +804,10 @@ cudaError_t launch_mma(const Cut& k, DecodeParams a, cudaStream_t s) {
   const int resident = sm_count() * M::kBlocks;
   if (resident < 1) return cudaErrorInvalidDevice;
   if (a.workers > resident) a.workers = resident;
-  a.by_item = (int64_t)a.S * a.items <= a.workers;
   decode_mma_kernel<D, NH><<<a.workers, kThreads, M::kSmem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<__nv_bfloat16, D>(a, k.part_heads, s);
+  return launch_join<__nv_bfloat16, D, M::kTile>(a, k.part_heads, s);
 }
 
 template <int D>
@@ -829,8 +839,7 @@ size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H) {
   if (fa::check_heads(c, H) != FA_OK) return 0;
   const fa::Cut k = fa::cut_of(*c, H);
   if (k.most_tiles <= 1) return 0;
-  return fa::align16(sizeof(fa::Record) * k.workers) +
-         2 * (size_t)k.workers * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
+  return 2 * (size_t)k.workers * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
 }
 
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
@@ -859,10 +868,8 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
   a.L = L;
   a.table = page_table;
   a.lengths = lengths;
-  char* ws = need > 0 ? (char*)workspace : nullptr;
-  a.records = (fa::Record*)ws;
-  a.part_o = ws ? (float*)(ws + fa::align16(sizeof(fa::Record) * k.workers)) : nullptr;
-  a.part_ml = ws ? (float2*)(a.part_o + 2 * (size_t)k.workers * k.part_heads * c->d) : nullptr;
+  a.part_o = (float*)workspace;
+  a.part_ml = (float2*)(a.part_o + (need > 0 ? 2 * (size_t)k.workers * k.part_heads * c->d : 0));
   a.page_rows = fa::FastDiv(c->page_rows);
   a.S = c->S;
   a.H = H;
