@@ -1,0 +1,476 @@
+// Shared by the kernels of fa_decode (fa_decode.cu, bf16, and
+// fa_decode_fp32.cu): how the work is shared out, and the joining of parts.
+//
+// Work.  An item is one sequence, one key-value head and some of its query
+// heads; a tile is kTile rows of an item.  All tiles of all items in order are
+// cut into equal runs, one for each of `workers` blocks (as many as are
+// resident at a time).  A block finds its run from the lengths itself: the host
+// knows none of them.  A run may end inside an item.  What a block has then
+// goes to the workspace as (m, l, o), at most two such parts a block: one of an
+// item that began in an earlier block's run and one of an item that goes on in
+// the next one's.  decode_join_kernel adds the parts of an item up, in the order
+// of the blocks: no atomics, the same sums each time.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "fa_paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWorkers = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct DecodeParams {
+  const char *Q, *K, *V;
+  char* O;
+  float* L;
+  const int32_t *table, *lengths;
+  int32_t* status;
+  float2* part_ml;    // [2 workers][heads of an item]
+  float* part_o;      // [2 workers][heads of an item][d]
+  FastDiv page_rows;
+  int S, H, group;    // group: query heads that share a key-value head
+  int split;          // items a group is cut into
+  int item_heads;     // query heads of an item (the last of a group may have fewer)
+  int items;          // of a sequence: H_kv * split
+  int num_pages, max_pages;
+  int cap;            // page_rows * max_pages
+  int workers;
+  int64_t table_stride;
+  int64_t qs, qh, os, oh;  // byte strides
+  int64_t pp, ph, pn;
+  float scale2;       // scale * log2(e)
+};
+
+// ------------------------------------------------------------- sharing out
+__device__ __forceinline__ int rows_of(const DecodeParams& a, int s) {
+  const int n = __ldg(a.lengths + s);
+  if (n < 0 || n > a.cap) report_pages(a.status);
+  return min(max(n, 0), a.cap);
+}
+
+template <int kTile>
+__device__ __forceinline__ int tiles_of(int rows) {
+  return rows <= kTile ? 1 : (rows + kTile - 1) / kTile;  // an empty item still writes its zeros
+}
+
+// What beginning and ending an item costs, in tiles: an item of n tiles is
+// kItemCost + n units of work, and the runs are of equal units.  A run that
+// begins inside the first kItemCost units of an item begins with its first
+// tile.  So a run may be empty only between two items, never inside one.  1 is
+// what measured best: 32 sequences of up to 2048 rows, 32 heads of d 64 (items
+// of up to 32 tiles) took 56.5 us with 0, 46.3 with 1, 46.5 with 2, 47.4 with 3.
+constexpr int kItemCost = 1;
+
+struct Share {
+  int64_t total;  // units of all items
+  int workers;    // blocks that have a run
+  __device__ __forceinline__ int64_t first(int w) const { return total * w / workers; }
+  // the block whose run holds unit x: the largest w with first(w) <= x
+  __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * workers - 1) / total); }
+};
+
+// Sum over the threads before this one (return value) and over the block of NT
+// threads; sums: NT / 32 entries of shared memory.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* sums, int64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the last call's readers of sums are done
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  x -= n;
+  *all = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 32; ++k) {
+    if (k < warp) x += sums[k];
+    *all += sums[k];
+  }
+  return x;
+}
+
+// The sequences' units, summed over a block of NT threads.  Thread t looks at
+// sequences t, t + NT, ...: up to NT of them are loaded and summed once, of more
+// the sums are taken twice, for the total and for a place among them.
+template <int kTile, int NT>
+struct Units {
+  const DecodeParams& a;
+  int64_t* sums;     // NT / 32 entries of shared memory
+  int64_t n, lo, all;  // of the first NT sequences: this thread's, those before it, all
+  __device__ __forceinline__ int64_t of(int s) const {
+    return s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
+  }
+  __device__ __forceinline__ Units(const DecodeParams& p, int64_t* shared) : a(p), sums(shared) {
+    n = of(threadIdx.x);
+    lo = block_scan<NT>(n, sums, &all);
+  }
+  __device__ __forceinline__ Share share() {
+    Share sh;
+    sh.total = all;
+    if (a.S > NT) {
+      int64_t more = 0;
+      for (int s = NT + threadIdx.x; s < a.S; s += NT) more += of(s);
+      block_scan<NT>(more, sums, &more);
+      sh.total += more;
+    }
+    sh.workers = (int)(sh.total < a.workers ? sh.total : a.workers);
+    return sh;
+  }
+  // The sequence that holds unit x (x < 0: sequence `want`), and its first unit.
+  __device__ __forceinline__ int find(int64_t x, int want, int64_t* base) {
+    __shared__ int64_t found_base;
+    __shared__ int found;
+    for (int at = 0;;) {
+      const int s = at + threadIdx.x;
+      if (x < 0 ? s == want : n > 0 && lo <= x && x < lo + n) {
+        found_base = lo;
+        found = s;
+      }
+      at += NT;
+      if (x < 0 ? want < at : all > x) break;
+      n = of(at + threadIdx.x);
+      int64_t here;
+      lo = all + block_scan<NT>(n, sums, &here);
+      all += here;
+    }
+    __syncthreads();
+    *base = found_base;
+    return found;
+  }
+};
+
+// A place in the row of tiles: tile t of item `item` of sequence s, which is
+// unit `unit` of all.
+template <int kTile>
+struct Place {
+  int s, item, t, rows, tiles;
+  int64_t unit;
+  // the first tile at or behind unit x of sequence s, whose first unit is base
+  __device__ __forceinline__ void set(const DecodeParams& a, int seq, int64_t base, int64_t x) {
+    s = seq;
+    rows = rows_of(a, s);
+    tiles = tiles_of<kTile>(rows);
+    item = (int)((x - base) / (kItemCost + tiles));
+    const int64_t begin = base + (int64_t)item * (kItemCost + tiles);
+    t = max((int)(x - begin) - kItemCost, 0);
+    unit = begin + kItemCost + t;
+  }
+  __device__ __forceinline__ void next(const DecodeParams& a) {
+    ++unit;
+    if (++t < tiles) return;
+    t = 0;
+    unit += kItemCost;
+    if (++item < a.items) return;
+    item = 0;
+    if (++s < a.S) {
+      rows = rows_of(a, s);
+      tiles = tiles_of<kTile>(rows);
+    }
+  }
+};
+
+// The query heads of an item: the first one, and how many.
+__device__ __forceinline__ int item_first_head(const DecodeParams& a, int item, int* kv, int* heads) {
+  *kv = item / a.split;
+  const int part = item - *kv * a.split;
+  *heads = min(a.item_heads, a.group - part * a.item_heads);
+  return *kv * a.group + part * a.item_heads;
+}
+
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+template <class T>
+__device__ __forceinline__ void store4(char* row, int col, float4 x) {
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4*>(row + 4 * col) = x;
+  else
+    *reinterpret_cast<uint2*>(row + 2 * col) = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
+}
+
+// ------------------------------------------------------- asynchronous copies
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, bool on) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l1(const char* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp's copies of its rows of each tile, ahead of their use: rows warp *
+// kRows ... of the tile, K then V, kPieces pieces of 16 bytes each, kPitch
+// bytes apart, in a ring of kStages in shared memory.
+template <int kTile, int kRows, int kPieces, int kPitch, int kStages>
+struct Loader {
+  static constexpr int kStageBytes = 2 * kRows * kPitch;
+  static_assert(kStages >= 3 && kStages <= 5, "the masks of kStages - 1 tiles share 64 bits");
+  const DecodeParams& a;
+  Place<kTile> at;      // the tile that is copied next
+  const int64_t end;    // of the run
+  const uint32_t ring;  // of this warp
+  uint64_t queue = 0;   // which rows of the tiles in flight are there, the oldest in the low 16 bits
+  // The row that this lane looks up in that tile: its page is asked for one
+  // tile ahead of the copies that need it.
+  int page = -1;
+  bool in = false;
+  int64_t off = 0;
+
+  __device__ __forceinline__ Loader(const DecodeParams& p, const Place<kTile>& first, int64_t e, uint32_t r)
+      : a(p), at(first), end(e), ring(r) {
+    look_up();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) produce(i);
+  }
+  __device__ __forceinline__ void look_up() {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = at.t * kTile + warp * kRows + (lane & (kRows - 1));
+    uint32_t r;
+    const uint32_t col = a.page_rows.div((uint32_t)j, &r);
+    in = j < at.rows;
+    page = in ? __ldg(a.table + at.s * a.table_stride + col) : -1;
+    off = (int64_t)(at.item / a.split) * a.ph + (int64_t)r * a.pn;
+    if (at.t == 0) {  // a new item: its queries into L1
+      int kv, heads;
+      const char* row = a.Q + at.s * a.qs + (int64_t)item_first_head(a, at.item, &kv, &heads) * a.qh;
+      constexpr int kLines = (kPieces * 16 + 127) / 128;
+      for (int k = lane; k < heads * kLines; k += 32) prefetch_l1(row + (k / kLines) * a.qh + (k % kLines) * 128);
+    }
+  }
+  // Copies of the tile looked up, into stage st; returns which of its rows are
+  // there.  Rows that are not are filled with zeros, and not read.  The pieces
+  // of a row go to neighbouring lanes, so that a request takes whole lines.
+  __device__ __forceinline__ uint32_t copy(int st) {
+    const int lane = threadIdx.x & 31;
+    const bool ok = in && page >= 0 && page < a.num_pages;
+    if (in && !ok) report_pages(a.status);
+    const int64_t from_row = ok ? page * a.pp + off : 0;
+    const uint32_t seen = __ballot_sync(0xffffffffu, ok) & ((1u << kRows) - 1);
+    const uint32_t to = ring + st * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < kRows * kPieces / 32; ++i) {
+      const int row = (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
+      const int64_t from = __shfl_sync(0xffffffffu, from_row, row) + piece * 16;
+      const bool on = (seen >> row) & 1;
+      cp_async16(to + row * kPitch + piece * 16, a.K + from, on);
+      cp_async16(to + (kRows + row) * kPitch + piece * 16, a.V + from, on);
+    }
+    return seen;
+  }
+  __device__ __forceinline__ void produce(int st) {
+    uint32_t seen = 0;
+    if (at.unit < end) {
+      seen = copy(st);
+      at.next(a);
+      if (at.unit < end) look_up();
+    }
+    cp_commit();
+    queue = (queue >> 16) | ((uint64_t)seen << (16 * (kStages - 2)));
+  }
+  // Waits for the oldest tile in flight, in stage st, asks for another, and
+  // returns which rows of it are there.
+  __device__ __forceinline__ uint32_t next(int st) {
+    cp_wait<kStages - 2>();
+    __syncwarp();  // the warp's copies are all there, and its reads of the stage refilled next are done
+    const uint32_t seen = (uint32_t)queue & 0xffffu;
+    produce(st == 0 ? kStages - 1 : st - 1);
+    return seen;
+  }
+};
+
+// This block's run: its first tile and its last unit; false if it has none.
+template <int kTile>
+__device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, int64_t* end) {
+  __shared__ int64_t sums[kWarps];
+  Units<kTile, kThreads> units(a, sums);
+  const Share share = units.share();
+  if ((int)blockIdx.x >= share.workers) return false;
+  const int64_t x = share.first(blockIdx.x);
+  *end = share.first(blockIdx.x + 1);
+  int64_t base;
+  const int s = units.find(x, 0, &base);
+  at->set(a, s, base, x);
+  return at->unit < *end;
+}
+
+// ------------------------------------------------------------------- joining
+// Block (r, h): head h of one item, item r if there are no more items than runs
+// (by_item), else the one that run r ends inside of if it also begins there:
+// every item of several parts has one such run.  Which parts it has follows
+// from the lengths, so the blocks find that out while the kernel in front
+// still runs.  D / 4 threads hold a row of o, and the block's groups of so many
+// threads take the parts in turn, kAhead loads at a time.
+constexpr int kJoinThreads = 256;
+
+template <class T, int D, int kTile>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
+                                                                   int part_heads, int by_item) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
+  __shared__ float4 os[kGroups][kLanes];
+  __shared__ float2 mls[kGroups];
+  __shared__ int64_t sums[kJoinThreads / 32];
+  int s = 0, item = 0, block = 0, slot = 0, following = 0;
+  {
+    Units<kTile, kJoinThreads> units(a, sums);
+    const Share share = units.share();
+    int64_t base = 0;
+    if (by_item) {
+      s = blockIdx.x / a.items;
+      item = blockIdx.x - s * a.items;
+      units.find(-1, s, &base);
+    } else if ((int)blockIdx.x < share.workers) {
+      const int64_t x = share.first(blockIdx.x + 1) - 1;
+      s = units.find(x, 0, &base);
+      item = (int)((x - base) / (kItemCost + tiles_of<kTile>(rows_of(a, s))));
+    }
+    const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
+    block = share.block_of(begin + kItemCost);
+    if (by_item || block == (int)blockIdx.x) following = share.block_of(begin + kItemCost + tiles - 1) - block;
+    // a run that holds tiles before the item has it as its second part
+    slot = share.first(block) < begin ? 1 : 0;
+  }
+  const int head = blockIdx.y;
+  int kv, heads;
+  const int h = item_first_head(a, item, &kv, &heads) + head;
+  const bool some = following > 0 && head < heads;
+  // What comes after this kernel on its stream waits for this kernel alone, so
+  // it may not end before the one in front, even if it has nothing to join:
+  // block (0, 0) waits in any case.
+  if (some || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!some) return;
+  const int grp = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  if (grp < kGroups) {
+    for (int k0 = grp; k0 <= following; k0 += kGroups * kAhead) {
+      float2 ml[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const int k = k0 + e * kGroups;
+        ml[e] = make_float2(-INFINITY, 0.f);
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k > following) continue;
+        const int64_t p = (int64_t)(2 * (block + k) + (k == 0 ? slot : 0)) * part_heads + head;
+        ml[e] = a.part_ml[p];
+        v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) top = fmaxf(top, ml[e].x);
+      const float base = base_of(top), f = ptx::ex2(m - base);
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const float w = ptx::ex2(ml[e].x - base);
+        o.x = fmaf(w, v[e].x, o.x), o.y = fmaf(w, v[e].y, o.y), o.z = fmaf(w, v[e].z, o.z), o.w = fmaf(w, v[e].w, o.w);
+        l = fmaf(w, ml[e].y, l);
+      }
+      m = top;
+    }
+    os[grp][x] = o;
+    if (x == 0) mls[grp] = make_float2(m, l);
+  }
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) m = fmaxf(m, mls[k].x);
+  const float base = base_of(m);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < kGroups; ++k) {
+    const float4 v = os[k][x];
+    const float w = ptx::ex2(mls[k].x - base);
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    l = fmaf(w, mls[k].y, l);
+  }
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  store4<T>(a.O + s * a.os + (int64_t)h * a.oh, 4 * x, o);
+  if (threadIdx.x == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ----------------------------------------------------------------- launching
+// How a problem is cut: what the workspace's size and the launch go by.
+struct Cut {
+  int split, item_heads, part_heads;  // items a group is cut into, heads of an item, heads of a part's slots
+  int64_t most_tiles;                 // of an item
+  int workers;                        // at most
+};
+
+// Rows of a tile.
+inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 256 ? 32 : 64; }
+
+inline Cut cut_of(const fa_cache& c, int H) {
+  Cut k;
+  const int group = H / c.H_kv;
+  // up to 16 query heads (8 in fp32) share one reading of the cache; larger
+  // groups are cut evenly, and read it again (from L2 where it holds an item)
+  k.split = (int)ceil_div(group, c.dtype == FA_BF16 ? 16 : 8);
+  k.item_heads = (int)ceil_div(group, k.split);
+  if (c.dtype == FA_BF16)
+    k.part_heads = k.item_heads <= 8 ? 8 : 16;
+  else
+    k.part_heads = k.item_heads == 1 ? 1 : k.item_heads <= 4 ? 4 : 8;
+  k.most_tiles = ceil_div(cache_rows(c), tile_rows(c));
+  const int64_t tiles = (int64_t)c.S * c.H_kv * k.split * k.most_tiles;
+  k.workers = (int)(tiles < kMaxWorkers ? tiles : kMaxWorkers);
+  return k;
+}
+
+template <class T, int D, int kTile>
+cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const int by_item = (int64_t)a.S * a.items <= a.workers;
+  cfg.gridDim = dim3((unsigned)(by_item ? a.S * a.items : a.workers), (unsigned)a.item_heads);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  // its blocks may be there before the kernel in front ends, and wait for that themselves
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, kTile>, a, part_heads, by_item);
+}
+
+// How many blocks of a kernel the device holds at a time; raises the kernel's
+// shared-memory limit.  Asked for once a device, and kept in known[device].
+inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int>* known, int* blocks) {
+  int dev = 0, a_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  *blocks = known[dev].load(std::memory_order_acquire);
+  if (*blocks > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a_sm, kernel, kThreads, smem);
+  if (e != cudaSuccess) return e;
+  *blocks = a_sm * sm_count();
+  if (*blocks < 1) return cudaErrorInvalidConfiguration;
+  known[dev].store(*blocks, std::memory_order_release);
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);
+cudaError_t launch_decode_fp32(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);
+
+}  // namespace fa
