@@ -31,6 +31,8 @@ from typing import Optional
 
 import torch
 
+import flashattention_backward_gb300 as _pkg
+
 _BF16, _FP32 = 0, 1
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -72,17 +74,11 @@ def declare(lib: ctypes.CDLL) -> None:
         getattr(lib, "fa_" + name).restype = ctypes.c_int
 
 
-def _api():
-    import flashattention_backward_gb300 as fa
-
-    return fa
-
-
 def _done(code: int, what: str, stream, check_status: bool) -> None:
     if code != 0:
-        raise _api().FaError(code, what)
+        raise _pkg.FaError(code, what)
     if check_status:
-        _api()._raise_on_device_error(stream, what + " (device)")
+        _pkg._raise_on_device_error(stream, what + " (device)")
 
 
 def _raw_stream(device: torch.device, stream) -> int:
@@ -91,13 +87,14 @@ def _raw_stream(device: torch.device, stream) -> int:
     if device.index != index:
         raise ValueError(f"the tensors are on {device}, the current device is cuda:{index}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the number alone: torch.cuda.current_stream() takes 3 us to wrap it
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _lend(stream, *tensors) -> None:
-    """Tensors allocated here and used on a stream given by the caller: their
-    memory may not be handed out again before that stream is done with it."""
+    """Tensors of this call and a stream given by the caller: their memory may
+    not be handed out again before that stream is done with it."""
     if stream is not None:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream))
@@ -140,15 +137,16 @@ def _table(c: FaCache, page_table: torch.Tensor, device) -> int:
     return page_table.data_ptr()
 
 
+_DTYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
+
+
 def cache_for(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: Optional[torch.Tensor] = None) -> FaCache:
     """Descriptor of two pools and, if given, the page table over them."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [pages, kv_heads, page_rows, d] tensors of one shape")
-    if k_pages.dtype == torch.bfloat16:
-        dtype = _BF16
-    elif k_pages.dtype == torch.float32:
-        dtype = _FP32
-    else:
+    code = _DTYPES.get(k_pages.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {k_pages.dtype}")
     if v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages must share the dtype")
@@ -158,15 +156,15 @@ def cache_for(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: Optional
     strides = _row_strides(k_pages)
     if v_pages.stride() != k_pages.stride() and _row_strides(v_pages) != strides:
         raise ValueError("k_pages and v_pages must share their strides")
-    pages, heads, rows, d = k_pages.shape
-    c = FaCache(pages, rows, heads, d, dtype, 1, 1, 0, *strides, 1)
+    pages, heads, rows, d = shape
+    c = FaCache(pages, rows, heads, d, code, 1, 1, 0, *strides, 1)
     if page_table is not None:
         _table(c, page_table, device)
     return c
 
 
 def _library():
-    return _api().load_library()
+    return _pkg._LIB or _pkg.load_library()
 
 
 def fa_decode_workspace_bytes(c: FaCache, heads: int) -> int:
@@ -188,43 +186,47 @@ def attention_decode(q, k_pages, v_pages, page_table, lengths, scale: Optional[f
     c = cache_for(k_pages, v_pages)
     device = k_pages.device
     table = _table(c, page_table, device)
-    if q.dim() != 4 or q.shape[0] != c.S or q.shape[2] != 1 or q.shape[3] != c.d:
-        raise ValueError(f"q must be a [{c.S}, heads, 1, {c.d}] tensor")
+    shape = q.shape
+    S, d = c.S, c.d
+    if len(shape) != 4 or shape[0] != S or shape[2] != 1 or shape[3] != d:
+        raise ValueError(f"q must be a [{S}, heads, 1, {d}] tensor")
     if q.dtype != k_pages.dtype or q.device != device:
         raise ValueError("q must have the dtype and device of the pools")
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("attention_decode has no gradient: call it under torch.no_grad()")
-    heads = q.shape[1]
+    heads = shape[1]
     raw = _raw_stream(device, stream)
-    lens = _ints("lengths", lengths, (c.S,), device)
+    lens = _ints("lengths", lengths, (S,), device)
     qs, qh, _ = _row_strides(q)
     lib = _library()
     ref = ctypes.byref(c)
     need = lib.fa_decode_workspace_bytes(ref, heads)
-    given = out is not None
-    if given:
+    if out is not None:
         o, L = out
-        if o.shape != q.shape or o.dtype != q.dtype or o.device != device:
+        if o.shape != shape or o.dtype != q.dtype or o.device != device:
             raise ValueError("out[0] must have the shape, dtype and device of q")
-        if L.shape != q.shape[:3] or L.dtype != torch.float32 or L.device != device or not L.is_contiguous():
-            raise ValueError(f"out[1] must be a contiguous float32 tensor of shape {tuple(q.shape[:3])}")
+        if L.shape != shape[:3] or L.dtype != torch.float32 or L.device != device or not L.is_contiguous():
+            raise ValueError(f"out[1] must be a contiguous float32 tensor of shape {tuple(shape[:3])}")
         os, oh, _ = _row_strides(o)
     else:
-        o = torch.empty((c.S, heads, 1, c.d), dtype=q.dtype, device=device)
-        L = torch.empty((c.S, heads, 1), dtype=torch.float32, device=device)
-        os, oh = heads * c.d, c.d
-    if workspace is None:
-        own = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        ws, ws_bytes = (own.data_ptr(), need) if need else (0, 0)
-    else:
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=device)
+        L = torch.empty(shape[:3], dtype=torch.float32, device=device)
+        os, oh = heads * d, d
+    if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        own, ws, ws_bytes = None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = workspace.data_ptr()
+    else:
+        ws = 0
     if stream is not None:
-        _lend(stream, *(t for t in ((None, None) if given else (o, L)) + (own,) if t is not None))
-    code = lib.fa_decode(ref, heads, c.d ** -0.5 if scale is None else scale, q.data_ptr(), qs, qh, k_pages.data_ptr(),
-                         v_pages.data_ptr(), table, lens, o.data_ptr(), os, oh, L.data_ptr(), ws, ws_bytes, raw)
-    _done(code, "fa_decode", stream, check_status)
+        _lend(stream, *(t for t in (o, L, workspace) if t is not None))
+    code = lib.fa_decode(ref, heads, d ** -0.5 if scale is None else scale, q.data_ptr(), qs, qh, k_pages.data_ptr(),
+                         v_pages.data_ptr(), table, lens, o.data_ptr(), os, oh, L.data_ptr(), ws, need, raw)
+    if code or check_status:
+        _done(code, "fa_decode", stream, check_status)
     return o, L
 
 
