@@ -313,11 +313,11 @@ cudaError_t launch_mma(const Cut& k, DecodeParams a, cudaStream_t s) {
   int resident = 0;
   cudaError_t e = resident_blocks((const void*)decode_mma_kernel<D, NH>, M::kSmem, known, &resident);
   if (e != cudaSuccess) return e;
-  if (a.workers > resident) a.workers = resident;
-  decode_mma_kernel<D, NH><<<a.workers, kThreads, M::kSmem, s>>>(a);
+  const int blocks = blocks_of(k, resident, &a);
+  decode_mma_kernel<D, NH><<<blocks, kThreads, M::kSmem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<__nv_bfloat16, D, M::kTile>(a, k.part_heads, s);
+  return launch_join<__nv_bfloat16, D, M::kTile>(k, a, blocks, s);
 }
 
 template <int D>
@@ -355,7 +355,7 @@ size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H) {
   if (fa::check_heads(c, H) != FA_OK) return 0;
   const fa::Cut k = fa::cut_of(*c, H);
   if (k.most_tiles <= 1) return 0;
-  return 2 * (size_t)k.workers * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
+  return (size_t)k.parts() * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
 }
 
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
@@ -385,7 +385,7 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
   a.table = page_table;
   a.lengths = lengths;
   a.part_o = (float*)workspace;
-  a.part_ml = (float2*)(a.part_o + (need > 0 ? 2 * (size_t)k.workers * k.part_heads * c->d : 0));
+  a.part_ml = (float2*)(a.part_o + (need > 0 ? (size_t)k.parts() * k.part_heads * c->d : 0));
   a.page_rows = fa::FastDiv(c->page_rows);
   a.S = c->S;
   a.H = H;
@@ -396,7 +396,6 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
   a.num_pages = c->num_pages;
   a.max_pages = c->max_pages;
   a.cap = (int)fa::cache_rows(*c);
-  a.workers = k.workers;
   a.table_stride = c->table_stride;
   a.qs = q_stride_s * es;
   a.qh = q_stride_h * es;

@@ -3,13 +3,12 @@
 //
 // Work.  An item is one sequence, one key-value head and some of its query
 // heads; a tile is kTile rows of an item.  All tiles of all items in order are
-// cut into equal runs, one for each of `workers` blocks (as many as are
-// resident at a time).  A block finds its run from the lengths itself: the host
-// knows none of them.  A run may end inside an item.  What a block has then
-// goes to the workspace as (m, l, o), at most two such parts a block: one of an
-// item that began in an earlier block's run and one of an item that goes on in
-// the next one's.  decode_join_kernel adds the parts of an item up, in the order
-// of the blocks: no atomics, the same sums each time.
+// cut into runs, one for each block.  A block finds its run from the lengths
+// itself: the host knows none of them.  A run may end inside an item.  What a
+// block has then goes to the workspace as (m, l, o), at most two such parts a
+// run: one of an item that began in an earlier run and one of an item that
+// goes on in the next one.  decode_join_kernel adds the parts of an item up, in
+// the order of the runs: no atomics, the same sums each time.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,7 +24,7 @@
 namespace fa {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxWorkers = 1024;
+constexpr int kMaxRuns = 1280;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -35,8 +34,8 @@ struct DecodeParams {
   float* L;
   const int32_t *table, *lengths;
   int32_t* status;
-  float2* part_ml;    // [2 workers][heads of an item]
-  float* part_o;      // [2 workers][heads of an item][d]
+  float2* part_ml;    // [2 runs][heads of an item]
+  float* part_o;      // [2 runs][heads of an item][d]
   FastDiv page_rows;
   int S, H, group;    // group: query heads that share a key-value head
   int split;          // items a group is cut into
@@ -44,7 +43,7 @@ struct DecodeParams {
   int items;          // of a sequence: H_kv * split
   int num_pages, max_pages;
   int cap;            // page_rows * max_pages
-  int workers;
+  int resident;       // blocks that run at a time
   int64_t table_stride;
   int64_t qs, qh, os, oh;  // byte strides
   int64_t pp, ph, pn;
@@ -71,12 +70,40 @@ __device__ __forceinline__ int tiles_of(int rows) {
 // of up to 32 tiles) took 56.5 us with 0, 46.3 with 1, 46.5 with 2, 47.4 with 3.
 constexpr int kItemCost = 1;
 
+// The runs.  SMs do not get equal shares of the memory's bandwidth: with equal
+// runs the first was done after 74 % of the time, on average they were after
+// 88 % (32 sequences of 8192 rows, 8 heads of d 128).  So where there is enough
+// to do, the blocks that are resident from the start get kBigShare of the
+// units, and the rest is cut into kSmallRuns times as many small runs, for
+// blocks that the hardware starts where one has ended.  Who takes which changes
+// from call to call, where the runs end does not.  64 sequences of up to 8192
+// rows (100 units a resident block) took 164.1 us with equal runs, 158.7 with
+// these, 157.9 to 159.7 with two or three times as many small ones; 32 of up to
+// 2048 (33 units) took 44.9 and, with small runs, 47 to 50: a block's start
+// costs as much as two tiles.  Hence kMinUnits.
+constexpr double kBigShare = 0.9;
+constexpr int kSmallRuns = 1;
+constexpr int kMinUnits = 64;  // of a resident block, for there to be small runs
+
 struct Share {
-  int64_t total;  // units of all items
-  int workers;    // blocks that have a run
-  __device__ __forceinline__ int64_t first(int w) const { return total * w / workers; }
-  // the block whose run holds unit x: the largest w with first(w) <= x
-  __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * workers - 1) / total); }
+  int64_t big_units, small_units;  // units of all items: in big and in small runs
+  int big, small;                  // runs
+  __device__ __forceinline__ Share(int64_t total, int resident) {
+    big = (int)(total < resident ? total : resident);
+    const bool tail = total >= (int64_t)resident * kMinUnits;
+    big_units = tail ? (int64_t)((double)total * kBigShare) : total;
+    small_units = total - big_units;
+    small = tail ? resident * kSmallRuns : 0;
+  }
+  __device__ __forceinline__ int runs() const { return big + small; }
+  __device__ __forceinline__ int64_t first(int w) const {
+    return w <= big ? big_units * w / big : big_units + small_units * (w - big) / small;
+  }
+  // the run that holds unit x: the largest w with first(w) <= x
+  __device__ __forceinline__ int run_of(int64_t x) const {
+    return x < big_units ? (int)(((x + 1) * big - 1) / big_units)
+                         : big + (int)(((x - big_units + 1) * small - 1) / small_units);
+  }
 };
 
 // Sum over the threads before this one (return value) and over the block of NT
@@ -119,16 +146,14 @@ struct Units {
     lo = block_scan<NT>(n, sums, &all);
   }
   __device__ __forceinline__ Share share() {
-    Share sh;
-    sh.total = all;
+    int64_t total = all;
     if (a.S > NT) {
       int64_t more = 0;
       for (int s = NT + threadIdx.x; s < a.S; s += NT) more += of(s);
       block_scan<NT>(more, sums, &more);
-      sh.total += more;
+      total += more;
     }
-    sh.workers = (int)(sh.total < a.workers ? sh.total : a.workers);
-    return sh;
+    return Share(total, a.resident);
   }
   // The sequence that holds unit x (x < 0: sequence `want`), and its first unit.
   __device__ __forceinline__ int find(int64_t x, int want, int64_t* base) {
@@ -299,7 +324,7 @@ __device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, 
   __shared__ int64_t sums[kWarps];
   Units<kTile, kThreads> units(a, sums);
   const Share share = units.share();
-  if ((int)blockIdx.x >= share.workers) return false;
+  if ((int)blockIdx.x >= share.runs()) return false;
   const int64_t x = share.first(blockIdx.x);
   *end = share.first(blockIdx.x + 1);
   int64_t base;
@@ -309,22 +334,24 @@ __device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, 
 }
 
 // ------------------------------------------------------------------- joining
-// Block (r, h): head h of one item, item r if there are no more items than runs
-// (by_item), else the one that run r ends inside of if it also begins there:
-// every item of several parts has one such run.  Which parts it has follows
-// from the lengths, so the blocks find that out while the kernel in front
-// still runs.  D / 4 threads hold a row of o, and the block's groups of so many
-// threads take the parts in turn, kAhead loads at a time.
+// Block (r, y): some heads (`together` of them, from y * together) of one item,
+// item r if there are no more items than runs (by_item), else the one that run
+// r ends inside of if it also begins there: every item of several parts has
+// one such run.  Which parts it has follows from the lengths, so the blocks can
+// find that out while the kernel in front still runs.  D / 4 threads hold a row
+// of o; of the block's groups of so many threads, `together` take a head each
+// and the others share its parts, kAhead loads at a time.
 constexpr int kJoinThreads = 256;
 
-template <class T, int D, int kTile>
+template <class T, int D, int kTile, bool kAlone>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
-                                                                   int part_heads, int by_item) {
+                                                                   int part_heads, int by_item, int heads_together) {
+  const int together = kAlone ? 1 : heads_together;
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
   __shared__ float4 os[kGroups][kLanes];
   __shared__ float2 mls[kGroups];
   __shared__ int64_t sums[kJoinThreads / 32];
-  int s = 0, item = 0, block = 0, slot = 0, following = 0;
+  int s = 0, item = 0, run = 0, slot = 0, following = 0;
   {
     Units<kTile, kJoinThreads> units(a, sums);
     const Share share = units.share();
@@ -333,40 +360,41 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       s = blockIdx.x / a.items;
       item = blockIdx.x - s * a.items;
       units.find(-1, s, &base);
-    } else if ((int)blockIdx.x < share.workers) {
+    } else if ((int)blockIdx.x < share.runs()) {
       const int64_t x = share.first(blockIdx.x + 1) - 1;
       s = units.find(x, 0, &base);
       item = (int)((x - base) / (kItemCost + tiles_of<kTile>(rows_of(a, s))));
     }
     const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
-    block = share.block_of(begin + kItemCost);
-    if (by_item || block == (int)blockIdx.x) following = share.block_of(begin + kItemCost + tiles - 1) - block;
+    run = share.run_of(begin + kItemCost);
+    if (by_item || run == (int)blockIdx.x) following = share.run_of(begin + kItemCost + tiles - 1) - run;
     // a run that holds tiles before the item has it as its second part
-    slot = share.first(block) < begin ? 1 : 0;
+    slot = share.first(run) < begin ? 1 : 0;
   }
-  const int head = blockIdx.y;
   int kv, heads;
-  const int h = item_first_head(a, item, &kv, &heads) + head;
-  const bool some = following > 0 && head < heads;
+  const int h0 = item_first_head(a, item, &kv, &heads), head0 = blockIdx.y * together;
+  const bool some = following > 0 && head0 < heads;
   // What comes after this kernel on its stream waits for this kernel alone, so
   // it may not end before the one in front, even if it has nothing to join:
   // block (0, 0) waits in any case.
   if (some || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!some) return;
   const int grp = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  if (grp < kGroups) {
-    for (int k0 = grp; k0 <= following; k0 += kGroups * kAhead) {
+  const int sharing = kGroups / together;  // groups that share a head's parts
+  if (grp < together * sharing) {
+    const int head = min(head0 + grp % together, heads - 1);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int k0 = grp / together; k0 <= following; k0 += sharing * kAhead) {
       float2 ml[kAhead];
       float4 v[kAhead];
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
-        const int k = k0 + e * kGroups;
+        const int k = k0 + e * sharing;
         ml[e] = make_float2(-INFINITY, 0.f);
         v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k > following) continue;
-        const int64_t p = (int64_t)(2 * (block + k) + (k == 0 ? slot : 0)) * part_heads + head;
+        const int64_t p = (int64_t)(2 * (run + k) + (k == 0 ? slot : 0)) * part_heads + head;
         ml[e] = a.part_ml[p];
         v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
       }
@@ -388,15 +416,15 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     if (x == 0) mls[grp] = make_float2(m, l);
   }
   __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  m = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kGroups; ++k) m = fmaxf(m, mls[k].x);
-  const float base = base_of(m);
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-  l = 0.f;
+  if (grp >= together || head0 + grp >= heads) return;
+  float m = -INFINITY;
 #pragma unroll 8
-  for (int k = 0; k < kGroups; ++k) {
+  for (int k = grp; k < together * sharing; k += together) m = fmaxf(m, mls[k].x);
+  const float base = base_of(m);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
+  for (int k = grp; k < together * sharing; k += together) {
     const float4 v = os[k][x];
     const float w = ptx::ex2(mls[k].x - base);
     o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
@@ -405,16 +433,18 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
   o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  store4<T>(a.O + s * a.os + (int64_t)h * a.oh, 4 * x, o);
-  if (threadIdx.x == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (m + log2f(l)) * kLn2;
+  store4<T>(a.O + s * a.os + (int64_t)(h0 + head0 + grp) * a.oh, 4 * x, o);
+  if (x == 0) a.L[(int64_t)s * a.H + h0 + head0 + grp] = none ? INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ----------------------------------------------------------------- launching
 // How a problem is cut: what the workspace's size and the launch go by.
 struct Cut {
   int split, item_heads, part_heads;  // items a group is cut into, heads of an item, heads of a part's slots
-  int64_t most_tiles;                 // of an item
-  int workers;                        // at most
+  int64_t tiles, most_tiles;          // at most: of all items, of one
+  // units are tiles and kItemCost for every item, and no item has less than one tile
+  int64_t units() const { return tiles * (1 + kItemCost); }
+  int64_t parts() const { return 2 * (units() < kMaxRuns ? units() : kMaxRuns); }
 };
 
 // Rows of a tile.
@@ -432,16 +462,30 @@ inline Cut cut_of(const fa_cache& c, int H) {
   else
     k.part_heads = k.item_heads == 1 ? 1 : k.item_heads <= 4 ? 4 : 8;
   k.most_tiles = ceil_div(cache_rows(c), tile_rows(c));
-  const int64_t tiles = (int64_t)c.S * c.H_kv * k.split * k.most_tiles;
-  k.workers = (int)(tiles < kMaxWorkers ? tiles : kMaxWorkers);
+  k.tiles = (int64_t)c.S * c.H_kv * k.split * k.most_tiles;
   return k;
 }
 
+// The blocks of a launch: every run that the lengths can lead to.  Sets a->resident.
+inline int blocks_of(const Cut& k, int resident, DecodeParams* a) {
+  if (resident > kMaxRuns / (1 + kSmallRuns)) resident = kMaxRuns / (1 + kSmallRuns);
+  a->resident = resident;
+  if (k.units() >= (int64_t)resident * kMinUnits) return resident * (1 + kSmallRuns);
+  return (int)(k.units() < resident ? k.units() : resident);
+}
+
 template <class T, int D, int kTile>
-cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
+cudaError_t launch_join(const Cut& k, const DecodeParams& a, int blocks, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int by_item = (int64_t)a.S * a.items <= a.workers;
-  cfg.gridDim = dim3((unsigned)(by_item ? a.S * a.items : a.workers), (unsigned)a.item_heads);
+  const int64_t items = (int64_t)a.S * a.items;
+  const int by_item = items <= blocks;
+  const int64_t x = by_item ? items : blocks;
+  // one head a block while that leaves few blocks: the parts are then read by
+  // all of its groups, which counts for few items of many parts
+  int together = 1;
+  while (x * ceil_div(a.item_heads, together) > 1024 && together < a.item_heads && 2 * together <= kJoinThreads / (D / 4))
+    together *= 2;
+  cfg.gridDim = dim3((unsigned)x, (unsigned)ceil_div(a.item_heads, together));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   // its blocks may be there before the kernel in front ends, and wait for that themselves
@@ -450,7 +494,8 @@ cudaError_t launch_join(const DecodeParams& a, int part_heads, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, kTile>, a, part_heads, by_item);
+  return cudaLaunchKernelEx(&cfg, together == 1 ? decode_join_kernel<T, D, kTile, true> : decode_join_kernel<T, D, kTile, false>,
+                            a, k.part_heads, by_item, together);
 }
 
 // How many blocks of a kernel the device holds at a time; raises the kernel's

@@ -282,11 +282,11 @@ cudaError_t launch_simt(const Cut& k, DecodeParams a, cudaStream_t s) {
   int resident = 0;
   cudaError_t e = resident_blocks((const void*)decode_simt_kernel<D, HR>, M::kSmem, known, &resident);
   if (e != cudaSuccess) return e;
-  if (a.workers > resident) a.workers = resident;
-  decode_simt_kernel<D, HR><<<a.workers, kThreads, M::kSmem, s>>>(a);
+  const int blocks = blocks_of(k, resident, &a);
+  decode_simt_kernel<D, HR><<<blocks, kThreads, M::kSmem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<float, D, M::kTile>(a, k.part_heads, s);
+  return launch_join<float, D, M::kTile>(k, a, blocks, s);
 }
 
 template <int D>
