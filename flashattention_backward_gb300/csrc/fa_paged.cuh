@@ -70,7 +70,4 @@ int sm_count();
 
 __device__ __forceinline__ void report_pages(int32_t* status) { atomicCAS(status, 0, (int32_t)FA_ERR_PAGES); }
 
-// Pages that hold n rows.
-__device__ __forceinline__ int pages_of(int64_t n, int page_rows) { return (int)((n + page_rows - 1) / page_rows); }
-
 }  // namespace fa

@@ -24,9 +24,12 @@ constexpr int kStep = kThreads * kPer;
 
 struct Pages {
   int32_t num_pages, page_rows, S, max_pages;
+  int32_t rows;          // of a sequence at most: page_rows * max_pages
+  FastDiv by_page_rows;
   int64_t table_stride;
   int32_t* status;
-  __device__ int64_t rows() const { return (int64_t)page_rows * max_pages; }
+  // pages that n rows take, 0 <= n <= rows
+  __device__ __forceinline__ int pages(int n) const { return (int)by_page_rows.div((uint32_t)(n + page_rows - 1)); }
 };
 
 // Exclusive prefix sum of one number a thread over the block; *total is the
@@ -90,13 +93,15 @@ __device__ __forceinline__ int rank_pages(int first, int last, int most, int* su
   return done;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_extend_kernel(const Pages g, int32_t* table, int32_t* lengths,
+__global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g, int32_t* table, int32_t* lengths,
                                                                 int32_t* refs, const int32_t* n_new, int32_t* start,
                                                                 int32_t* scratch) {
   __shared__ int sums[kWarps];
   __shared__ unsigned long long wanted;
   int32_t* free_pages = scratch;                // [num_pages]
-  int32_t* first_of = scratch + g.num_pages;    // [S]: pages wanted by the sequences before
+  __shared__ int first_of_few[kThreads];
+  // [S]: pages wanted by the sequences before
+  int32_t* first_of = g.S <= kThreads ? first_of_few : scratch + g.num_pages;
   if (threadIdx.x == 0) wanted = 0;
   __syncthreads();
   bool bad = false;
@@ -105,11 +110,11 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const Pages g, i
     const int s = base + threadIdx.x;
     int need = 0;
     if (s < g.S) {
-      const int64_t n = lengths[s], more = n_new[s];
-      if (n < 0 || more < 0 || n + more > g.rows())
+      const int n = lengths[s], more = n_new[s];
+      if (n < 0 || more < 0 || (int64_t)n + more > g.rows)
         bad = true;
       else
-        need = pages_of(n + more, g.page_rows) - pages_of(n, g.page_rows);
+        need = g.pages(n + more) - g.pages(n);
     }
     // more than there are pages: the call is refused below, and the prefix
     // sums in 32 bits may then wrap without being used
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const Pages g, i
         hi = mid - 1;
     }
     const int page = free_pages[k];
-    table[lo * g.table_stride + pages_of(lengths[lo], g.page_rows) + (k - first_of[lo])] = page;
+    table[lo * g.table_stride + g.pages(lengths[lo]) + (k - first_of[lo])] = page;
     refs[page] = 1;
   }
   __syncthreads();  // lengths above are the ones before the call
@@ -152,13 +157,38 @@ __global__ void __launch_bounds__(kThreads) pages_extend_kernel(const Pages g, i
   }
 }
 
-__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const Pages g, int pairs, const int32_t* src,
+// Calls f(i, a, b, rows of a) with one warp a pair, kThreads pairs at a time:
+// the indexes and lengths of a batch are loaded by a thread each and read from
+// shared memory, so that a warp's pairs do not wait for one another's loads.
+struct PairBatch {
+  int src[kThreads], dst[kThreads], rows[kThreads];
+};
+template <class F>
+__device__ __forceinline__ void for_pairs(int pairs, const int32_t* src, const int32_t* dst, const int32_t* lengths,
+                                          PairBatch* batch, F f) {
+  for (int base = 0; base < pairs; base += kThreads) {
+    const int i = base + threadIdx.x;
+    __syncthreads();  // the last batch has been read
+    if (i < pairs) {
+      batch->src[threadIdx.x] = src[i];
+      batch->dst[threadIdx.x] = dst[i];
+      batch->rows[threadIdx.x] = lengths[src[i]];
+    }
+    __syncthreads();
+    const int n = min(pairs - base, kThreads);
+#pragma unroll 4
+    for (int k = threadIdx.x >> 5; k < n; k += kWarps) f(base + k, batch->src[k], batch->dst[k], batch->rows[k]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, int pairs, const int32_t* src,
                                                               const int32_t* dst, int32_t* table, int32_t* lengths,
                                                               int32_t* refs, int32_t* moves, int32_t* scratch) {
   __shared__ int sums[kWarps];
+  __shared__ PairBatch batch;
   int32_t* free_pages = scratch;             // [num_pages]
   int32_t* mark = scratch + g.num_pages;     // [S]: 1 a source, 2 a destination
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   for (int s = threadIdx.x; s < g.S; s += kThreads) mark[s] = 0;
   __syncthreads();
   bool bad = false;
@@ -168,47 +198,50 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const Pages g, int
       bad = true;
       continue;
     }
+    const int rows = lengths[a], none = lengths[b];
     atomicOr(&mark[a], 1);
-    if (atomicOr(&mark[b], 2) & 2) bad = true;
-    if (lengths[a] < 0 || lengths[a] > g.rows() || lengths[b] != 0) bad = true;
+    bad |= (atomicOr(&mark[b], 2) & 2) || rows < 0 || rows > g.rows || none != 0;
   }
   bool refused = __syncthreads_or(bad);
-  if (!refused) {
-    for (int s = threadIdx.x; s < g.S; s += kThreads)
-      if (mark[s] == 3) bad = true;
-    // a source's entries are followed below: look at them before anything changes
-    for (int i = warp; i < pairs; i += kWarps) {
-      const int a = src[i], held = pages_of(lengths[a], g.page_rows);
-      for (int c = lane; c < held; c += 32) {
-        const int p = table[a * g.table_stride + c];
-        if (p < 0 || p >= g.num_pages) bad = true;
-      }
-    }
-    refused = __syncthreads_or(bad);
-  }
   int tails = 0;
   if (!refused) {
+    for (int s = threadIdx.x; s < g.S; s += kThreads) bad |= mark[s] == 3;
+    // a source's entries are followed below: look at them before anything changes
+    for_pairs(pairs, src, dst, lengths, &batch, [&](int, int a, int, int rows) {
+      const int held = g.pages(rows);
+      for (int c = lane; c < held; c += 32) {
+        const int p = table[a * g.table_stride + c];
+        bad |= p < 0 || p >= g.num_pages;
+      }
+    });
     for (int base = 0; base < pairs; base += kThreads) {
       const int i = base + threadIdx.x;
-      const int tail = i < pairs && lengths[src[i]] % g.page_rows != 0;
+      int tail = 0;
+      if (i < pairs) {
+        uint32_t rest;
+        g.by_page_rows.div((uint32_t)lengths[src[i]], &rest);
+        tail = rest != 0;
+      }
       int total;
       const int rank = block_scan(tail, sums, &total);
       if (i < pairs) moves[3 * (int64_t)i + 1] = tails + rank;
       tails += total;
     }
-    if (tails > 0)
+    refused = __syncthreads_or(bad);
+    if (!refused && tails > 0)
       refused = rank_pages(0, g.num_pages, tails, sums, [&](int p) { return refs[p] <= 0; },
                            [&](int p, int r) { free_pages[r] = p; }) < tails;
   }
   __syncthreads();
   if (refused) {
-    for (int i = threadIdx.x; i < 3 * pairs; i += kThreads) moves[i] = -1;
+    for (int64_t i = threadIdx.x; i < 3 * (int64_t)pairs; i += kThreads) moves[i] = -1;
     if (threadIdx.x == 0) report_pages(g.status);
     return;
   }
-  for (int i = warp; i < pairs; i += kWarps) {
-    const int a = src[i], b = dst[i];
-    const int n = lengths[a], full = n / g.page_rows, rest = n - full * g.page_rows;
+  // no source is a destination: nothing read here is written here
+  for_pairs(pairs, src, dst, lengths, &batch, [&](int i, int a, int b, int rows) {
+    uint32_t rest;
+    const int full = (int)g.by_page_rows.div((uint32_t)rows, &rest);
     for (int c = lane; c < full; c += 32) {
       const int p = table[a * g.table_stride + c];
       table[b * g.table_stride + c] = p;
@@ -224,10 +257,10 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const Pages g, int
       }
       moves[3 * (int64_t)i] = from;
       moves[3 * (int64_t)i + 1] = to;
-      moves[3 * (int64_t)i + 2] = rest ? rest : -1;
-      lengths[b] = n;
+      moves[3 * (int64_t)i + 2] = rest ? (int)rest : -1;
+      lengths[b] = rows;
     }
-  }
+  });
 }
 
 // One block a listed sequence.
@@ -243,8 +276,8 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const Pages g, const in
   // other finds it empty
   if (threadIdx.x == 0) rows = atomicExch(&lengths[s], 0);
   __syncthreads();
-  bool bad = rows < 0 || rows > g.rows();
-  const int held = bad ? (rows < 0 ? 0 : g.max_pages) : pages_of(rows, g.page_rows);
+  bool bad = rows < 0 || rows > g.rows;
+  const int held = g.pages(min(max(rows, 0), g.rows));
   for (int c = threadIdx.x; c < held; c += blockDim.x) {
     int32_t* e = &table[s * g.table_stride + c];
     const int p = *e;
@@ -259,7 +292,7 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const Pages g, const in
   if (bad) report_pages(g.status);
 }
 
-__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const Pages g, const int32_t* refs, int32_t* refs_out,
+__global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages g, const int32_t* refs, int32_t* refs_out,
                                                                  int32_t* moves, int32_t* n_moves, int32_t* scratch) {
   __shared__ int sums[kWarps];
   int32_t* to = scratch;                    // [num_pages]: where a page goes
@@ -301,8 +334,8 @@ __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const 
                                                            int32_t* table_out) {
   const int64_t row = blockIdx.x * g.table_stride;
   const int n = lengths[blockIdx.x];
-  bool bad = n < 0 || n > g.rows();
-  const int held = bad ? (n < 0 ? 0 : g.max_pages) : pages_of(n, g.page_rows);
+  bool bad = n < 0 || n > g.rows;
+  const int held = g.pages(min(max(n, 0), g.rows));
   for (int c = threadIdx.x; c < g.max_pages; c += blockDim.x) {
     int p = -1;
     if (c < held) {
@@ -320,6 +353,8 @@ bool geometry(const fa_cache& c, Pages* g) {
   g->page_rows = c.page_rows;
   g->S = c.S;
   g->max_pages = c.max_pages;
+  g->rows = (int32_t)cache_rows(c);
+  g->by_page_rows = FastDiv(c.page_rows);
   g->table_stride = c.table_stride;
   g->status = device_status_word();
   return g->status != nullptr;
