@@ -57,7 +57,6 @@ __all__ = [
     "pages_fork",
     "pages_free",
     "pages_compact",
-    "fa_pages_scratch_elems",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE, FA_ERR_PAGES = range(7)
@@ -468,7 +467,6 @@ from .paged import (  # noqa: E402
     cache_copy_pages,
     cache_for,
     fa_decode_workspace_bytes,
-    fa_pages_scratch_elems,
     pages_compact,
     pages_extend,
     pages_fork,

@@ -5,10 +5,12 @@
 // Which page goes where is a prefix sum: the k-th free page, in rising order,
 // goes to the k-th demand, in the order of the sequences or pairs.  So the
 // result does not depend on the order in which threads run, and there is no
-// free list to keep.  One thread block does it: the arrays are a few hundred
-// kilobytes at most in ordinary use (4 bytes a page), and what bounds the
-// calls is the latency of a handful of dependent passes, not bandwidth.
+// free list to keep.  One thread block does it (a cluster in pages_fork): the
+// arrays are a few hundred kilobytes at most in ordinary use (4 bytes a page),
+// and what bounds the calls is the latency of a handful of dependent passes,
+// not bandwidth.
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,23 +35,24 @@ struct Pages {
 };
 
 // Exclusive prefix sum of one number a thread over the block; *total is the
-// block's sum.  sums: kWarps + 1 ints of shared memory.  Every thread calls it.
-__device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
+// block's sum.  sums: kWarps numbers of shared memory.  Every thread calls it.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T* sums, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int y = x;
+  T y = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    const T z = __shfl_up_sync(0xffffffffu, y, o);
     if (lane >= o) y += z;
   }
   __syncthreads();  // the last call's readers of sums are done
   if (lane == 31) sums[warp] = y;
   __syncthreads();
   if (warp == 0) {
-    int s = sums[lane];  // kWarps == 32
+    T s = sums[lane];  // kWarps == 32
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(0xffffffffu, s, o);
+      const T z = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += z;
     }
     sums[lane] = s;
@@ -94,14 +97,14 @@ __device__ __forceinline__ int rank_pages(int first, int last, int most, int* su
 }
 
 __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g, int32_t* table, int32_t* lengths,
-                                                                int32_t* refs, const int32_t* n_new, int32_t* start,
-                                                                int32_t* scratch) {
+                                                                   int32_t* refs, const int32_t* n_new,
+                                                                   int32_t* start) {
   __shared__ int sums[kWarps];
   __shared__ unsigned long long wanted;
-  int32_t* free_pages = scratch;                // [num_pages]
   __shared__ int first_of_few[kThreads];
-  // [S]: pages wanted by the sequences before
-  int32_t* first_of = g.S <= kThreads ? first_of_few : scratch + g.num_pages;
+  // [S]: pages wanted by the sequences before; many of them are kept in `start`,
+  // whose values are only known at the end
+  int* first_of = g.S <= kThreads ? first_of_few : start;
   if (threadIdx.x == 0) wanted = 0;
   __syncthreads();
   bool bad = false;
@@ -126,17 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g
   }
   bool refused = __syncthreads_or(bad) || wanted > (unsigned long long)g.num_pages;
   const int want = refused ? 0 : (int)wanted;
-  if (!refused && want > 0)
-    refused = rank_pages(0, g.num_pages, want, sums, [&](int p) { return refs[p] <= 0; },
-                         [&](int p, int r) { free_pages[r] = p; }) < want;
-  if (refused) {
-    for (int s = threadIdx.x; s < g.S; s += kThreads) start[s] = -1;
-    if (threadIdx.x == 0) report_pages(g.status);
-    return;
-  }
-  __syncthreads();  // free_pages and first_of are read across threads
-  // k-th new page: of the last sequence whose first one is at or before k
-  for (int k = threadIdx.x; k < want; k += kThreads) {
+  // the k-th new page belongs to the last sequence whose first one is at or before k
+  const auto entry = [&](int k) -> int32_t* {
     int lo = 0, hi = g.S - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -145,52 +139,59 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g
       else
         hi = mid - 1;
     }
-    const int page = free_pages[k];
-    table[lo * g.table_stride + g.pages(lengths[lo]) + (k - first_of[lo])] = page;
-    refs[page] = 1;
-  }
-  __syncthreads();  // lengths above are the ones before the call
-  for (int s = threadIdx.x; s < g.S; s += kThreads) {
-    const int n = lengths[s];
-    start[s] = n;
-    lengths[s] = n + n_new[s];
-  }
-}
-
-// Calls f(i, a, b, rows of a) with one warp a pair, kThreads pairs at a time:
-// the indexes and lengths of a batch are loaded by a thread each and read from
-// shared memory, so that a warp's pairs do not wait for one another's loads.
-struct PairBatch {
-  int src[kThreads], dst[kThreads], rows[kThreads];
-};
-template <class F>
-__device__ __forceinline__ void for_pairs(int pairs, const int32_t* src, const int32_t* dst, const int32_t* lengths,
-                                          PairBatch* batch, F f) {
-  for (int base = 0; base < pairs; base += kThreads) {
-    const int i = base + threadIdx.x;
-    __syncthreads();  // the last batch has been read
-    if (i < pairs) {
-      batch->src[threadIdx.x] = src[i];
-      batch->dst[threadIdx.x] = dst[i];
-      batch->rows[threadIdx.x] = lengths[src[i]];
+    return &table[lo * g.table_stride + g.pages(lengths[lo]) + (k - first_of[lo])];
+  };
+  if (want > 0) {
+    const int found = rank_pages(0, g.num_pages, want, sums, [&](int p) { return refs[p] <= 0; }, [&](int p, int k) {
+      *entry(k) = p;
+      refs[p] = 1;
+    });
+    if (found < want) {  // too few: give them back
+      refused = true;
+      __syncthreads();
+      for (int k = threadIdx.x; k < found; k += kThreads) {
+        int32_t* e = entry(k);
+        refs[*e] = 0;
+        *e = -1;
+      }
     }
-    __syncthreads();
-    const int n = min(pairs - base, kThreads);
-#pragma unroll 4
-    for (int k = threadIdx.x >> 5; k < n; k += kWarps) f(base + k, batch->src[k], batch->dst[k], batch->rows[k]);
+    __syncthreads();  // lengths and first_of above are the ones before the call
   }
+  for (int s = threadIdx.x; s < g.S; s += kThreads) {
+    if (refused) {
+      start[s] = -1;
+    } else {
+      const int n = lengths[s];
+      start[s] = n;
+      lengths[s] = n + n_new[s];
+    }
+  }
+  if (refused && threadIdx.x == 0) report_pages(g.status);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, int pairs, const int32_t* src,
-                                                              const int32_t* dst, int32_t* table, int32_t* lengths,
-                                                              int32_t* refs, int32_t* moves, int32_t* scratch) {
+// A cluster of kForkBlocks blocks.  All of them work out the same plan (who gets
+// which free page), which only reads what the call changes; then, with the
+// cluster's barrier between, each looks at and copies the table rows of its
+// share of the pairs.  The references are what costs: one SM sends about one
+// scattered atomic a cycle, 3.7 us for 224 pairs of 32 pages; in one block the
+// call took 17 us.
+// marks: two bits a sequence in shared memory, whether it is a source and
+// whether it is a destination.
+constexpr int kForkBlocks = 8;
+
+__global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kThreads, 1)
+    pages_fork_kernel(const Pages g, int pairs, const int32_t* src, const int32_t* dst, int32_t* table,
+                      int32_t* lengths, int32_t* refs, int32_t* moves) {
+  namespace cg = cooperative_groups;
   __shared__ int sums[kWarps];
-  __shared__ PairBatch batch;
-  int32_t* free_pages = scratch;             // [num_pages]
-  int32_t* mark = scratch + g.num_pages;     // [S]: 1 a source, 2 a destination
+  __shared__ int any_bad;      // of the cluster, in block 0
+  extern __shared__ unsigned marks[];  // 16 sequences a word
+  const cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31;
-  for (int s = threadIdx.x; s < g.S; s += kThreads) mark[s] = 0;
-  __syncthreads();
+  const int first = blockIdx.x * kWarps + (threadIdx.x >> 5), step = kForkBlocks * kWarps;  // this warp's pairs
+  for (int w = threadIdx.x; w < (g.S + 15) / 16; w += kThreads) marks[w] = 0;
+  if (threadIdx.x == 0) any_bad = 0;
+  cluster.sync();
   bool bad = false;
   for (int i = threadIdx.x; i < pairs; i += kThreads) {
     const int a = src[i], b = dst[i];
@@ -199,21 +200,26 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, 
       continue;
     }
     const int rows = lengths[a], none = lengths[b];
-    atomicOr(&mark[a], 1);
-    bad |= (atomicOr(&mark[b], 2) & 2) || rows < 0 || rows > g.rows || none != 0;
+    atomicOr(&marks[a / 16], 1u << (a % 16 * 2));
+    const unsigned is_dst = 2u << (b % 16 * 2);
+    bad |= (atomicOr(&marks[b / 16], is_dst) & is_dst) || rows < 0 || rows > g.rows || none != 0;
   }
-  bool refused = __syncthreads_or(bad);
+  bool refused = __syncthreads_or(bad);  // the same in all blocks
   int tails = 0;
   if (!refused) {
-    for (int s = threadIdx.x; s < g.S; s += kThreads) bad |= mark[s] == 3;
+    for (int w = threadIdx.x; w < (g.S + 15) / 16; w += kThreads) bad |= (marks[w] & (marks[w] >> 1) & 0x55555555u) != 0;
     // a source's entries are followed below: look at them before anything changes
-    for_pairs(pairs, src, dst, lengths, &batch, [&](int, int a, int, int rows) {
-      const int held = g.pages(rows);
+    for (int i = first; i < pairs; i += step) {
+      const int a = src[i], held = g.pages(lengths[a]);
       for (int c = lane; c < held; c += 32) {
         const int p = table[a * g.table_stride + c];
         bad |= p < 0 || p >= g.num_pages;
       }
-    });
+    }
+    if (bad) atomicOr(cluster.map_shared_rank(&any_bad, 0), 1);
+    // the k-th pair with a partly filled page gets the k-th free page: until
+    // then the first number of move k says which pair that is.  All blocks
+    // write the same numbers.
     for (int base = 0; base < pairs; base += kThreads) {
       const int i = base + threadIdx.x;
       int tail = 0;
@@ -224,22 +230,28 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, 
       }
       int total;
       const int rank = block_scan(tail, sums, &total);
-      if (i < pairs) moves[3 * (int64_t)i + 1] = tails + rank;
+      if (tail) moves[3 * (int64_t)(tails + rank)] = i;
       tails += total;
     }
-    refused = __syncthreads_or(bad);
-    if (!refused && tails > 0)
-      refused = rank_pages(0, g.num_pages, tails, sums, [&](int p) { return refs[p] <= 0; },
-                           [&](int p, int r) { free_pages[r] = p; }) < tails;
+    __syncthreads();
+    if (tails > 0)
+      refused = rank_pages(0, g.num_pages, tails, sums, [&](int p) { return refs[p] <= 0; }, [&](int p, int k) {
+                  moves[3 * (int64_t)moves[3 * (int64_t)k] + 1] = p;
+                }) < tails;
   }
-  __syncthreads();
+  cluster.sync();  // every block has its plan: what it was made from may change
+  refused |= *cluster.map_shared_rank(&any_bad, 0) != 0;
+  cluster.sync();  // block 0's flag has been read
   if (refused) {
-    for (int64_t i = threadIdx.x; i < 3 * (int64_t)pairs; i += kThreads) moves[i] = -1;
-    if (threadIdx.x == 0) report_pages(g.status);
+    if (blockIdx.x == 0) {
+      for (int64_t i = threadIdx.x; i < 3 * (int64_t)pairs; i += kThreads) moves[i] = -1;
+      if (threadIdx.x == 0) report_pages(g.status);
+    }
     return;
   }
   // no source is a destination: nothing read here is written here
-  for_pairs(pairs, src, dst, lengths, &batch, [&](int i, int a, int b, int rows) {
+  for (int i = first; i < pairs; i += step) {
+    const int a = src[i], b = dst[i], rows = lengths[a];
     uint32_t rest;
     const int full = (int)g.by_page_rows.div((uint32_t)rows, &rest);
     for (int c = lane; c < full; c += 32) {
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, 
       int from = -1, to = -1;
       if (rest) {
         from = table[a * g.table_stride + full];
-        to = free_pages[moves[3 * (int64_t)i + 1]];
+        to = moves[3 * (int64_t)i + 1];
         table[b * g.table_stride + full] = to;
         refs[to] = 1;  // a free page: in no table, so no other thread counts it
       }
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const Pages g, 
       moves[3 * (int64_t)i + 2] = rest ? (int)rest : -1;
       lengths[b] = rows;
     }
-  });
+  }
 }
 
 // One block a listed sequence.
@@ -292,33 +304,26 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const Pages g, const in
   if (bad) report_pages(g.status);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages g, const int32_t* refs, int32_t* refs_out,
-                                                                 int32_t* moves, int32_t* n_moves, int32_t* scratch) {
+__global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages g, const int32_t* refs,
+                                                                    int32_t* refs_out, int32_t* moves,
+                                                                    int32_t* n_moves) {
   __shared__ int sums[kWarps];
-  int32_t* to = scratch;                    // [num_pages]: where a page goes
-  int32_t* holes = scratch + g.num_pages;   // [num_pages / 2]
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const auto used = [&](int p) { return refs[p] > 0; };
   int mine = 0, n;
-  for (int p = threadIdx.x; p < g.num_pages; p += kThreads) {
-    const bool live = used(p);
-    to[p] = live ? p : -1;
-    mine += live;
-  }
+  for (int p = threadIdx.x; p < g.num_pages; p += kThreads) mine += used(p);
   block_scan(mine, sums, &n);
-  // free pages before n, rising; a page that stays keeps its count
-  rank_pages(0, n, n, sums, [&](int p) { return refs[p] <= 0; }, [&](int p, int r) { holes[r] = p; });
+  // free pages before n, rising, into the moves; at most num_pages / 2 of them
+  rank_pages(0, n, n, sums, [&](int p) { return !used(p); }, [&](int p, int k) { moves[3 * (int64_t)k + 1] = p; });
   __syncthreads();
-  if (refs_out != refs)
+  if (refs_out != refs)  // a page that stays keeps its count
     for (int p = threadIdx.x; p < n; p += kThreads) refs_out[p] = refs[p];
-  __syncthreads();  // the holes' zeros before the counts that move into them
-  // pages in use at n or behind: as many as there are holes
-  const int count = rank_pages(n, g.num_pages, g.num_pages, sums, used, [&](int p, int r) {
-    const int d = holes[r];
-    to[p] = d;
-    moves[3 * (int64_t)r] = p;
-    moves[3 * (int64_t)r + 1] = d;
-    moves[3 * (int64_t)r + 2] = g.page_rows;
-    refs_out[d] = refs[p];
+  __syncthreads();
+  // pages in use at n or behind: as many as there are free ones before n
+  const int count = rank_pages(n, g.num_pages, g.num_pages, sums, used, [&](int p, int k) {
+    moves[3 * (int64_t)k] = p;
+    moves[3 * (int64_t)k + 2] = g.page_rows;
+    refs_out[moves[3 * (int64_t)k + 1]] = refs[p];
   });
   __syncthreads();  // counts behind n are read above
   for (int p = n + threadIdx.x; p < g.num_pages; p += kThreads) refs_out[p] = 0;
@@ -327,20 +332,46 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages 
   if (threadIdx.x == 0) *n_moves = count;
 }
 
-// Table entries after a compaction: one block a sequence.  An entry that
-// names a page that refs calls free is damaged and becomes -1.
+// Table entries after a compaction: one block a sequence.  The moves are in
+// rising order of their sources, which lie behind all pages that stay.  An
+// entry that names no page in use is damaged and becomes -1.
 __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const int32_t* table,
-                                                           const int32_t* lengths, const int32_t* to,
+                                                           const int32_t* lengths, const int32_t* refs_out,
+                                                           const int32_t* moves, const int32_t* n_moves,
                                                            int32_t* table_out) {
   const int64_t row = blockIdx.x * g.table_stride;
   const int n = lengths[blockIdx.x];
   bool bad = n < 0 || n > g.rows;
   const int held = g.pages(min(max(n, 0), g.rows));
+  // the kernel in front writes no table: entries may be read ahead of it
+  int ahead = threadIdx.x < held ? table[row + threadIdx.x] : -1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int count = *n_moves;
   for (int c = threadIdx.x; c < g.max_pages; c += blockDim.x) {
     int p = -1;
     if (c < held) {
-      p = table[row + c];
-      p = p < 0 || p >= g.num_pages ? -1 : to[p];
+      p = c == (int)threadIdx.x ? ahead : table[row + c];
+      if (p < 0 || p >= g.num_pages) {
+        p = -1;
+      } else {
+        // the first move whose source is at or behind p, eight ways at a time
+        int lo = 0, hi = count;
+        while (lo < hi) {
+          const int step = (hi - lo + 7) / 8;
+          int below = 0;
+#pragma unroll
+          for (int k = 1; k < 8; ++k) {
+            const int at = lo + k * step - 1;
+            if (at < hi && moves[3 * (int64_t)at] < p) below = k;
+          }
+          if (below < 7) hi = min(hi, lo + (below + 1) * step - 1);
+          lo += below * step;
+        }
+        if (lo < count && moves[3 * (int64_t)lo] == p)
+          p = moves[3 * (int64_t)lo + 1];
+        else if (refs_out[p] <= 0)
+          p = -1;
+      }
       bad |= p < 0;
     }
     table_out[row + c] = p;
@@ -365,38 +396,33 @@ bool geometry(const fa_cache& c, Pages* g) {
 
 extern "C" {
 
-size_t fa_pages_scratch_elems(const fa_cache* c) {
-  if (fa::check_pages(c) != FA_OK) return 0;
-  return (size_t)c->num_pages + (size_t)(c->num_pages > c->S ? c->num_pages : c->S);
-}
-
 fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengths, int32_t* refs,
-                          const int32_t* n_new, int32_t* start, int32_t* scratch, void* stream) {
+                          const int32_t* n_new, int32_t* start, void* stream) {
   fa::NvtxRange range("fa_pages_extend");
   const fa_status st = fa::check_pages(c);
   if (st != FA_OK) return st;
   if (!fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(refs) || !fa::aligned4(n_new) ||
-      !fa::aligned4(start) || !fa::aligned4(scratch))
+      !fa::aligned4(start))
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
-  fa::pages_extend_kernel<<<1, fa::kThreads, 0, (cudaStream_t)stream>>>(g, page_table, lengths, refs, n_new, start,
-                                                                        scratch);
+  fa::pages_extend_kernel<<<1, fa::kThreads, 0, (cudaStream_t)stream>>>(g, page_table, lengths, refs, n_new, start);
   return fa::status_of(cudaGetLastError());
 }
 
 fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, const int32_t* dst, int32_t* page_table,
-                        int32_t* lengths, int32_t* refs, int32_t* moves, int32_t* scratch, void* stream) {
+                        int32_t* lengths, int32_t* refs, int32_t* moves, void* stream) {
   fa::NvtxRange range("fa_pages_fork");
   const fa_status st = fa::check_pages(c);
   if (st != FA_OK) return st;
+  if (c->S > 65536) return FA_ERR_UNSUPPORTED;  // its marks are kept in shared memory
   if (pairs < 1 || pairs > c->S || !fa::aligned4(src) || !fa::aligned4(dst) || !fa::aligned4(page_table) ||
-      !fa::aligned4(lengths) || !fa::aligned4(refs) || !fa::aligned4(moves) || !fa::aligned4(scratch))
+      !fa::aligned4(lengths) || !fa::aligned4(refs) || !fa::aligned4(moves))
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
-  fa::pages_fork_kernel<<<1, fa::kThreads, 0, (cudaStream_t)stream>>>(g, pairs, src, dst, page_table, lengths, refs,
-                                                                      moves, scratch);
+  fa::pages_fork_kernel<<<fa::kForkBlocks, fa::kThreads, (c->S + 15) / 16 * 4, (cudaStream_t)stream>>>(
+      g, pairs, src, dst, page_table, lengths, refs, moves);
   return fa::status_of(cudaGetLastError());
 }
 
@@ -416,21 +442,32 @@ fa_status fa_pages_free(const fa_cache* c, int32_t count, const int32_t* sequenc
 }
 
 fa_status fa_pages_compact(const fa_cache* c, const int32_t* page_table, const int32_t* lengths, const int32_t* refs,
-                           int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* n_moves, int32_t* scratch,
-                           void* stream) {
+                           int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* n_moves, void* stream) {
   fa::NvtxRange range("fa_pages_compact");
   const fa_status st = fa::check_pages(c);
   if (st != FA_OK) return st;
   if (!fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(refs) || !fa::aligned4(table_out) ||
-      !fa::aligned4(refs_out) || (c->num_pages > 1 && !fa::aligned4(moves)) || !fa::aligned4(n_moves) ||
-      !fa::aligned4(scratch))
+      !fa::aligned4(refs_out) || (c->num_pages > 1 && !fa::aligned4(moves)) || !fa::aligned4(n_moves))
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
   const cudaStream_t s = (cudaStream_t)stream;
-  fa::pages_compact_kernel<<<1, fa::kThreads, 0, s>>>(g, refs, refs_out, moves, n_moves, scratch);
-  fa::pages_rename_kernel<<<c->S, 128, 0, s>>>(g, page_table, lengths, scratch, table_out);
-  return fa::status_of(cudaGetLastError());
+  fa::pages_compact_kernel<<<1, fa::kThreads, 0, s>>>(g, refs, refs_out, moves, n_moves);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return FA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c->S);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  // its blocks may be there before the kernel in front ends, and wait for that themselves
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa::pages_rename_kernel, g, page_table, lengths, (const int32_t*)refs_out,
+                         (const int32_t*)moves, (const int32_t*)n_moves, table_out);
+  return fa::status_of(e);
 }
 
 }  // extern "C"

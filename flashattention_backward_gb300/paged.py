@@ -63,12 +63,10 @@ def declare(lib: ctypes.CDLL) -> None:
                               _sz, _vp]
     lib.fa_cache_append.argtypes = [P, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
     lib.fa_cache_copy_pages.argtypes = [P, _i32, _vp, _vp, _vp, _vp, _vp]
-    lib.fa_pages_scratch_elems.argtypes = [P]
-    lib.fa_pages_scratch_elems.restype = _sz
-    lib.fa_pages_extend.argtypes = [P] + [_vp] * 7
-    lib.fa_pages_fork.argtypes = [P, _i32] + [_vp] * 8
+    lib.fa_pages_extend.argtypes = [P] + [_vp] * 6
+    lib.fa_pages_fork.argtypes = [P, _i32] + [_vp] * 7
     lib.fa_pages_free.argtypes = [P, _i32] + [_vp] * 5
-    lib.fa_pages_compact.argtypes = [P] + [_vp] * 9
+    lib.fa_pages_compact.argtypes = [P] + [_vp] * 8
     for name in ("decode", "cache_append", "cache_copy_pages", "pages_extend", "pages_fork", "pages_free",
                  "pages_compact"):
         getattr(lib, "fa_" + name).restype = ctypes.c_int
@@ -255,7 +253,8 @@ def cache_append(k, v, k_pages, v_pages, page_table, start, counts=None, stream=
     n = 0 if counts is None else _ints("counts", counts, (c.S,), device)
     code = _library().fa_cache_append(ctypes.byref(c), rows, k.data_ptr(), v.data_ptr(), *strides, k_pages.data_ptr(),
                                       v_pages.data_ptr(), table, at, n, raw)
-    _done(code, "fa_cache_append", stream, check_status)
+    if code or check_status:
+        _done(code, "fa_cache_append", stream, check_status)
 
 
 def cache_copy_pages(k_pages, v_pages, moves, count=None, stream=None, check_status: bool = False) -> None:
@@ -272,7 +271,8 @@ def cache_copy_pages(k_pages, v_pages, moves, count=None, stream=None, check_sta
     n = 0 if count is None else _ints("count", count, (1,), device)
     code = _library().fa_cache_copy_pages(ctypes.byref(c), moves.shape[0], m, n, k_pages.data_ptr(),
                                           v_pages.data_ptr(), raw)
-    _done(code, "fa_cache_copy_pages", stream, check_status)
+    if code or check_status:
+        _done(code, "fa_cache_copy_pages", stream, check_status)
 
 
 def _pages(page_table, lengths, refs, page_rows: int, stream):
@@ -286,18 +286,6 @@ def _pages(page_table, lengths, refs, page_rows: int, stream):
     return c, device, raw, table, _ints("lengths", lengths, (c.S,), device), _ints("refs", refs, (c.num_pages,), device)
 
 
-def fa_pages_scratch_elems(c: FaCache) -> int:
-    return int(_library().fa_pages_scratch_elems(ctypes.byref(c)))
-
-
-def _new(c: FaCache, device, stream, *shapes):
-    """int32 results of the given shapes, and the call's scratch."""
-    got = [torch.empty(s, dtype=torch.int32, device=device) for s in shapes]
-    got.append(torch.empty(_library().fa_pages_scratch_elems(ctypes.byref(c)), dtype=torch.int32, device=device))
-    _lend(stream, *got)
-    return got
-
-
 def pages_extend(page_table, lengths, refs, n_new, page_rows: int, stream=None, check_status: bool = False):
     """Makes room for ``n_new[s]`` (int32 [S]) more rows of every sequence:
     updates the table, ``lengths`` and ``refs`` and returns ``start``, the
@@ -305,9 +293,12 @@ def pages_extend(page_table, lengths, refs, n_new, page_rows: int, stream=None, 
     the table, nothing changes and every start is -1."""
     c, device, raw, table, lens, r = _pages(page_table, lengths, refs, page_rows, stream)
     n = _ints("n_new", n_new, (c.S,), device)
-    start, scratch = _new(c, device, stream, (c.S,))
-    code = _library().fa_pages_extend(ctypes.byref(c), table, lens, r, n, start.data_ptr(), scratch.data_ptr(), raw)
-    _done(code, "fa_pages_extend", stream, check_status)
+    start = torch.empty_like(lengths)
+    if stream is not None:
+        _lend(stream, start)
+    code = _library().fa_pages_extend(ctypes.byref(c), table, lens, r, n, start.data_ptr(), raw)
+    if code or check_status:
+        _done(code, "fa_pages_extend", stream, check_status)
     return start
 
 
@@ -324,10 +315,12 @@ def pages_fork(page_table, lengths, refs, src, dst, page_rows: int, stream=None,
     a, b = _ints("src", src, (n,), device), _ints("dst", dst, (n,), device)
     if n == 0:
         return torch.empty((0, 3), dtype=torch.int32, device=device)
-    moves, scratch = _new(c, device, stream, (n, 3))
-    code = _library().fa_pages_fork(ctypes.byref(c), n, a, b, table, lens, r, moves.data_ptr(), scratch.data_ptr(),
-                                    raw)
-    _done(code, "fa_pages_fork", stream, check_status)
+    moves = torch.empty((n, 3), dtype=torch.int32, device=device)
+    if stream is not None:
+        _lend(stream, moves)
+    code = _library().fa_pages_fork(ctypes.byref(c), n, a, b, table, lens, r, moves.data_ptr(), raw)
+    if code or check_status:
+        _done(code, "fa_pages_fork", stream, check_status)
     return moves
 
 
@@ -340,7 +333,8 @@ def pages_free(page_table, lengths, refs, sequences, page_rows: int, stream=None
     n = sequences.shape[0]
     code = _library().fa_pages_free(ctypes.byref(c), n, _ints("sequences", sequences, (n,), device), table, lens, r,
                                     raw)
-    _done(code, "fa_pages_free", stream, check_status)
+    if code or check_status:
+        _done(code, "fa_pages_free", stream, check_status)
 
 
 def pages_compact(page_table, lengths, refs, page_rows: int, out=None, stream=None, check_status: bool = False):
@@ -356,8 +350,12 @@ def pages_compact(page_table, lengths, refs, page_rows: int, out=None, stream=No
                 out[0].dtype != torch.int32 or out[0].device != device:
             raise ValueError("out[0] must have the shape, strides, dtype and device of page_table")
         table_out, refs_out = out[0].data_ptr(), _ints("out[1]", out[1], (c.num_pages,), device)
-    moves, count, scratch = _new(c, device, stream, (c.num_pages // 2, 3), (1,))
+    moves = torch.empty((c.num_pages // 2, 3), dtype=torch.int32, device=device)
+    count = torch.empty(1, dtype=torch.int32, device=device)
+    if stream is not None:
+        _lend(stream, moves, count)
     code = _library().fa_pages_compact(ctypes.byref(c), table, lens, r, table_out, refs_out, moves.data_ptr(),
-                                       count.data_ptr(), scratch.data_ptr(), raw)
-    _done(code, "fa_pages_compact", stream, check_status)
+                                       count.data_ptr(), raw)
+    if code or check_status:
+        _done(code, "fa_pages_compact", stream, check_status)
     return moves, count

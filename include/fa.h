@@ -335,12 +335,9 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
 /* The page calls: whole numbers on the device, no host round trip, so that
  * they can stand in a captured graph between the calls above.  A sequence
  * with n rows has ceil(n / page_rows) pages.  Free pages are taken lowest
- * number first, in the order of the sequences or pairs.  scratch is
- * fa_pages_scratch_elems(c) int32, contents before the call do not matter;
- * calls that may run at the same time need one each (and, of course, tables
- * of their own).  Only the geometry of `c` is read, not its strides, dtype
- * or d. */
-size_t fa_pages_scratch_elems(const fa_cache* c);
+ * number first, in the order of the sequences or pairs.  Only the geometry of
+ * `c` is read, not its strides, dtype or d.  Calls on the same table, lengths
+ * or refs have to be ordered on one stream. */
 
 /* Makes room for n_new[s] >= 0 more rows: start[s] = lengths[s], lengths[s]
  * += n_new[s], and the pages that takes enter the table with refs = 1.  All
@@ -348,7 +345,7 @@ size_t fa_pages_scratch_elems(const fa_cache* c);
  * table, or a length or n_new is out of range, nothing changes, every
  * start[s] is -1 and FA_ERR_PAGES is recorded. */
 fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengths, int32_t* refs,
-                          const int32_t* n_new, int32_t* start, int32_t* scratch, void* stream);
+                          const int32_t* n_new, int32_t* start, void* stream);
 
 /* Pair i makes the empty sequence dst[i] a copy of src[i]: it shares its full
  * pages (refs + 1), and a last page that is partly filled is replaced by a
@@ -356,9 +353,9 @@ fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengt
  * fa_cache_copy_pages, or (-1, -1, -1).  src may repeat.  All or nothing:
  * with an index out of range, a dst that is not empty, comes twice or is also
  * a src, a damaged table row or too few free pages, nothing changes, all
- * moves are -1 and FA_ERR_PAGES is recorded.  1 <= pairs <= S. */
+ * moves are -1 and FA_ERR_PAGES is recorded.  1 <= pairs <= S <= 65536. */
 fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, const int32_t* dst, int32_t* page_table,
-                        int32_t* lengths, int32_t* refs, int32_t* moves, int32_t* scratch, void* stream);
+                        int32_t* lengths, int32_t* refs, int32_t* moves, void* stream);
 
 /* Empties the sequences listed: refs - 1 for each of their pages, table
  * entries -1, length 0.  An index of -1 is skipped, one out of range too
@@ -373,10 +370,9 @@ fa_status fa_pages_free(const fa_cache* c, int32_t count, const int32_t* sequenc
  * refs_out receive the table and refs after the moves, entries behind a
  * sequence's pages -1; they may be page_table and refs themselves, or copies
  * (same strides), so that work in flight still reads the old ones.  An entry
- * out of range becomes -1 (FA_ERR_PAGES). */
+ * that names no page in use becomes -1 (FA_ERR_PAGES). */
 fa_status fa_pages_compact(const fa_cache* c, const int32_t* page_table, const int32_t* lengths, const int32_t* refs,
-                           int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* n_moves, int32_t* scratch,
-                           void* stream);
+                           int32_t* table_out, int32_t* refs_out, int32_t* moves, int32_t* n_moves, void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
  * word.  *code receives FA_OK or the first device-side error recorded since

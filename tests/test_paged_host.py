@@ -40,10 +40,10 @@ def _calls(lib, c):
 
 def _page_calls(lib, c):
     ref = ctypes.byref(c) if c is not None else None
-    yield lib.fa_pages_extend(ref, BAD, BAD, BAD, BAD, BAD, BAD, None)
-    yield lib.fa_pages_fork(ref, 1, BAD, BAD, BAD, BAD, BAD, BAD, BAD, None)
+    yield lib.fa_pages_extend(ref, BAD, BAD, BAD, BAD, BAD, None)
+    yield lib.fa_pages_fork(ref, 1, BAD, BAD, BAD, BAD, BAD, BAD, None)
     yield lib.fa_pages_free(ref, 1, BAD, BAD, BAD, BAD, None)
-    yield lib.fa_pages_compact(ref, BAD, BAD, BAD, BAD, BAD, BAD, BAD, BAD, None)
+    yield lib.fa_pages_compact(ref, BAD, BAD, BAD, BAD, BAD, BAD, BAD, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -57,7 +57,7 @@ def test_geometry_is_checked_by_every_call(lib, kw, code):
     c = _cache(**kw)
     for r in list(_calls(lib, c)) + list(_page_calls(lib, c)):
         assert r == code
-    assert fa.fa_decode_workspace_bytes(c, 4) == 0 and fa.fa_pages_scratch_elems(c) == 0
+    assert fa.fa_decode_workspace_bytes(c, 4) == 0
     assert all(r == INVALID for r in list(_calls(lib, None)) + list(_page_calls(lib, None)))
 
 
@@ -91,21 +91,21 @@ def test_pointers_and_sizes_are_checked(lib):
     for args in ([c, -1, BAD, BAD, BAD, BAD, None], [c, 1, 0, BAD, BAD, BAD, None], [c, 1, BAD, BAD + 2, BAD, BAD, None],
                  [c, 1, BAD, BAD, 0, BAD, None], [c, 1, BAD, BAD, BAD, BAD + 8, None]):
         assert lib.fa_cache_copy_pages(*args) == INVALID
-    for f, n in ((lib.fa_pages_extend, 6), (lib.fa_pages_compact, 8)):
+    for f, n in ((lib.fa_pages_extend, 5), (lib.fa_pages_compact, 7)):
         for i in range(n):
             assert f(c, *[BAD if j != i else 0 for j in range(n)], None) == INVALID
-    for i in range(7):
-        assert lib.fa_pages_fork(c, 1, *[BAD if j != i else BAD + 2 for j in range(7)], None) == INVALID
-    assert lib.fa_pages_fork(c, 0, *[BAD] * 7, None) == INVALID
-    assert lib.fa_pages_fork(c, 4, *[BAD] * 7, None) == INVALID  # more pairs than sequences
+    for i in range(6):
+        assert lib.fa_pages_fork(c, 1, *[BAD if j != i else BAD + 2 for j in range(6)], None) == INVALID
+    assert lib.fa_pages_fork(c, 0, *[BAD] * 6, None) == INVALID
+    assert lib.fa_pages_fork(c, 4, *[BAD] * 6, None) == INVALID  # more pairs than sequences
+    many = ctypes.byref(_cache(S=65537, H_kv=1))
+    assert lib.fa_pages_fork(many, 1, *[BAD] * 6, None) == UNSUPPORTED
     assert lib.fa_pages_free(c, -1, *[BAD] * 4, None) == INVALID
     for i in range(4):
         assert lib.fa_pages_free(c, 1, *[BAD if j != i else 0 for j in range(4)], None) == INVALID
 
 
-def test_sizes_of_scratch_and_workspace(lib):
-    assert fa.fa_pages_scratch_elems(_cache()) >= 100 + 50
-    assert fa.fa_pages_scratch_elems(_cache(S=5000, H_kv=1)) >= 100 + 5000
+def test_size_of_the_workspace(lib):
     assert fa.fa_decode_workspace_bytes(_cache(), 3) == 0  # not a multiple of the cache's heads
     # what passes through it is bounded by the GPU, not by the lengths
     big = _cache(S=1000, max_pages=1 << 20, table_stride=1 << 20)
