@@ -289,7 +289,9 @@ typedef struct {
  * n = 0 gives O = 0, L = +inf, as fa_fwd gives a query that sees no key.
  * Rows behind n are not read.  A row on a page out of range counts as not
  * visible, a negative length as 0 and one beyond page_rows * max_pages as
- * that (FA_ERR_PAGES in each case).
+ * that (FA_ERR_PAGES in each case).  In bf16 the weights are multiplied as
+ * the sum of two bf16 numbers, so that O is rounded once, to bf16; an infinite
+ * value in a visible row of V gives NaN.
  * Q, O are [S, H, d] with element strides (q_stride_s, q_stride_h) and
  * (o_stride_s, o_stride_h), 16-byte aligned with byte strides multiples of
  * 16; O may not overlap Q.  L is a dense [S, H] float32 array.  H is a
@@ -301,7 +303,8 @@ typedef struct {
  * not matter; 0 bytes: may be NULL).  Calls that may run at the same time
  * need a workspace each, also when they are replayed from graphs.
  * Results are bitwise reproducible for the same S, H and lengths on the same
- * kind of GPU. */
+ * kind of GPU.  As with every call that keeps a status word, the first one on
+ * a device belongs before any stream capture. */
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H);
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
                     const void* K_pages, const void* V_pages, const int32_t* page_table, const int32_t* lengths,

@@ -132,6 +132,31 @@ def test_many_short_and_one_long():
     run_and_check(make(len(lengths), 4, 2, 64, 16, lengths, seed=3))
 
 
+@pytest.mark.parametrize("d,dtype,H,Hk", [(32, torch.bfloat16, 2, 2), (64, torch.bfloat16, 32, 2), (128, torch.float32, 8, 2)])
+def test_more_items_than_runs(d, dtype, H, Hk):
+    """The join goes by runs then, and takes several heads a block."""
+    lengths = [700 if i % 97 == 0 else (i * 37) % 130 for i in range(700)]
+    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, dtype, seed=4))
+
+
+@pytest.mark.parametrize("d,dtype,Hk,S,n", [(128, torch.bfloat16, 1, 9, 150000), (256, torch.bfloat16, 2, 40, 12000),
+                                            (32, torch.float32, 2, 40, 30000)])
+def test_enough_rows_for_small_runs(d, dtype, Hk, S, n):
+    """Past 64 tiles for each resident block the work ends in small runs.  All sequences read the same pages, each a
+    different number of them; two of the sequences are compared."""
+    q, kp, vp, table, _ = make(1, 4, Hk, d, 64, [n], dtype, seed=21)
+    q = torch.randn(S, 4, 1, d, generator=torch.Generator().manual_seed(22)).to(dtype).to(DEV)
+    lengths = torch.tensor([n - 77 * s for s in range(S)], dtype=torch.int32, device=DEV)
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count * (1 if d == 256 else 2 if d == 128 else 3)
+    assert S * Hk * (n - 77 * S) / 64 > 64 * blocks
+    o, L = fa.attention_decode(q, kp, vp, table.expand(S, -1).contiguous(), lengths)
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    for s in (0, S - 1):
+        one = slice(s, s + 1)
+        check((o[one], L[one]), q[one], kp, vp, table, lengths[one], d ** -0.5)
+
+
 def test_all_empty():
     run_and_check(make(3, 4, 2, 64, 16, [0, 0, 0]))
 

@@ -33,7 +33,7 @@ def _cache(**kw):
 def _calls(lib, c):
     """Every entry point that takes the pools, then those that take the table alone."""
     ref = ctypes.byref(c) if c is not None else None
-    yield lib.fa_decode(ref, 4, 0.125, BAD, 256, 64, BAD, BAD, BAD, BAD, BAD, 256, 64, BAD, BAD, 1 << 40, None)
+    yield lib.fa_decode(ref, 4, 0.125, BAD, 256, 64, BAD, BAD, BAD, BAD, 2 * BAD, 256, 64, BAD, BAD, 1 << 40, None)
     yield lib.fa_cache_append(ref, 1, BAD, BAD, 128, 64, 64, BAD, BAD, BAD, BAD, BAD, None)
     yield lib.fa_cache_copy_pages(ref, 1, BAD, BAD, BAD, BAD, None)
 
@@ -73,9 +73,9 @@ def test_pools_are_checked(lib, kw, code):
 
 def test_pointers_and_sizes_are_checked(lib):
     c = ctypes.byref(_cache())
-    ok = [c, 4, 0.125, BAD, 256, 64, BAD, BAD, BAD, BAD, BAD, 256, 64, BAD, BAD, 1 << 40, None]
+    ok = [c, 4, 0.125, BAD, 256, 64, BAD, BAD, BAD, BAD, 2 * BAD, 256, 64, BAD, BAD, 1 << 40, None]
     for i, x in [(1, 0), (1, 3), (1, -2), (2, 0.0), (2, float("nan")), (2, float("inf")), (2, -1.0), (3, 0), (3, BAD + 8),
-                 (4, 4), (5, -64), (6, BAD + 2), (7, 0), (8, 0), (8, BAD + 2), (9, 0), (10, BAD + 4), (11, 60), (12, 0),
+                 (4, 4), (5, -64), (6, BAD + 2), (7, 0), (8, 0), (8, BAD + 2), (9, 0), (10, BAD + 4), (10, BAD), (11, 60), (12, 0),
                  (13, 0)]:
         args = list(ok)
         args[i] = x
