@@ -124,41 +124,44 @@ def _ints(what: str, t: torch.Tensor, shape, device) -> int:
     return t.data_ptr()
 
 
-def _table(c: FaCache, page_table: torch.Tensor, device) -> int:
+def _table(page_table: torch.Tensor, device):
+    """Sequences, columns, row stride and address of a page table."""
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != device:
         raise ValueError(f"page_table must be a 2-D int32 tensor on {device}")
-    c.S, c.max_pages = page_table.shape
+    S, columns = page_table.shape
     row, column = page_table.stride()
-    if column != 1 and c.max_pages > 1:
+    if column != 1 and columns > 1:
         raise ValueError("the rows of page_table must be contiguous")
-    c.table_stride = row if c.S > 1 else c.max_pages
-    return page_table.data_ptr()
+    return S, columns, row if S > 1 else columns, page_table.data_ptr()
 
 
 _DTYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
 
 
-def cache_for(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: Optional[torch.Tensor] = None) -> FaCache:
-    """Descriptor of two pools and, if given, the page table over them."""
-    shape = k_pages.shape
+def _cache(k_pages, v_pages, page_table):
+    """Descriptor, device and address of the page table (which may be None)."""
+    shape, strides, dtype, device = k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.device
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [pages, kv_heads, page_rows, d] tensors of one shape")
-    code = _DTYPES.get(k_pages.dtype)
+    code = _DTYPES.get(dtype)
     if code is None:
-        raise TypeError(f"unsupported dtype {k_pages.dtype}")
-    if v_pages.dtype != k_pages.dtype:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if v_pages.dtype != dtype:
         raise ValueError("k_pages and v_pages must share the dtype")
-    device = k_pages.device
-    if not k_pages.is_cuda or v_pages.device != device:
+    if device.type != "cuda" or v_pages.device != device:
         raise ValueError("the pools must be on one CUDA device")
+    same = v_pages.stride() == strides
     strides = _row_strides(k_pages)
-    if v_pages.stride() != k_pages.stride() and _row_strides(v_pages) != strides:
+    if not same and _row_strides(v_pages) != strides:
         raise ValueError("k_pages and v_pages must share their strides")
+    S, columns, row, table = (1, 1, 1, 0) if page_table is None else _table(page_table, device)
     pages, heads, rows, d = shape
-    c = FaCache(pages, rows, heads, d, code, 1, 1, 0, *strides, 1)
-    if page_table is not None:
-        _table(c, page_table, device)
-    return c
+    return FaCache(pages, rows, heads, d, code, S, columns, 0, *strides, row), device, table
+
+
+def cache_for(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: Optional[torch.Tensor] = None) -> FaCache:
+    """Descriptor of two pools and, if given, the page table over them."""
+    return _cache(k_pages, v_pages, page_table)[0]
 
 
 def _library():
@@ -181,9 +184,7 @@ def attention_decode(q, k_pages, v_pages, page_table, lengths, scale: Optional[f
     :func:`fa_decode_workspace_bytes`, otherwise one is allocated for the
     call.  Calls that may run at the same time, replays of captured graphs
     among them, need a workspace each."""
-    c = cache_for(k_pages, v_pages)
-    device = k_pages.device
-    table = _table(c, page_table, device)
+    c, device, table = _cache(k_pages, v_pages, page_table)
     shape = q.shape
     S, d = c.S, c.d
     if len(shape) != 4 or shape[0] != S or shape[2] != 1 or shape[3] != d:
@@ -235,9 +236,7 @@ def cache_append(k, v, k_pages, v_pages, page_table, start, counts=None, stream=
     i < ``counts[s]`` (all rows without counts).  The pages must be there
     (:func:`pages_extend`, which also gives ``start``); a sequence with a
     negative start is left alone."""
-    c = cache_for(k_pages, v_pages)
-    device = k_pages.device
-    table = _table(c, page_table, device)
+    c, device, table = _cache(k_pages, v_pages, page_table)
     if k.dim() != 4 or k.shape[0] != c.S or k.shape[1] != c.H_kv or k.shape[3] != c.d or v.shape != k.shape:
         raise ValueError(f"k and v must be [{c.S}, {c.H_kv}, rows, {c.d}] tensors")
     if k.dtype != k_pages.dtype or v.dtype != k.dtype or k.device != device or v.device != device:
@@ -262,8 +261,7 @@ def cache_copy_pages(k_pages, v_pages, moves, count=None, stream=None, check_sta
     (src, dst, rows), with src -1 skipped, as :func:`pages_fork` and
     :func:`pages_compact` return it; ``count`` (int32 [1]) says how many of
     them count.  No dst may be the dst or src of another move."""
-    c = cache_for(k_pages, v_pages)
-    device = k_pages.device
+    c, device, _ = _cache(k_pages, v_pages, None)
     if moves.dim() != 2:
         raise ValueError("moves must be an [n, 3] tensor")
     raw = _raw_stream(device, stream)
@@ -280,10 +278,11 @@ def _pages(page_table, lengths, refs, page_rows: int, stream):
     if refs.dim() != 1 or not refs.is_cuda:
         raise ValueError("refs must be a 1-D CUDA tensor")
     device = refs.device
-    c = FaCache(refs.shape[0], int(page_rows), 1, 0, 0, 1, 1, 0, 0, 0, 0, 1)
-    table = _table(c, page_table, device)
+    pages = refs.shape[0]
+    S, columns, row, table = _table(page_table, device)
+    c = FaCache(pages, int(page_rows), 1, 0, 0, S, columns, 0, 0, 0, 0, row)
     raw = _raw_stream(device, stream)
-    return c, device, raw, table, _ints("lengths", lengths, (c.S,), device), _ints("refs", refs, (c.num_pages,), device)
+    return c, device, raw, table, _ints("lengths", lengths, (S,), device), _ints("refs", refs, (pages,), device)
 
 
 def pages_extend(page_table, lengths, refs, n_new, page_rows: int, stream=None, check_status: bool = False):

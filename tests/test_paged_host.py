@@ -147,12 +147,11 @@ def test_binding_refuses(lib):
     with pytest.raises(ValueError):
         paged._row_strides(pools[..., ::2])
     table = torch.zeros(3, 5, dtype=torch.int32)
-    c = fa.FaCache()
-    paged._table(c, table[:, :4], table.device)
-    assert (c.S, c.max_pages, c.table_stride) == (3, 4, 5)
+    assert paged._table(table[:, :4], table.device)[:3] == (3, 4, 5)
+    assert paged._table(table[:1, :4], table.device)[:3] == (1, 4, 4)
     for bad in (table.long(), table[0], table[:, ::2]):
         with pytest.raises(ValueError):
-            paged._table(c, bad, table.device)
+            paged._table(bad, table.device)
     for bad in (table[0].long(), table[0][:4], table[0][::2]):
         with pytest.raises(ValueError):
             paged._ints("lengths", bad, (5,), table.device)
