@@ -53,9 +53,8 @@ struct Mma {
   // of keys, 2 pieces)
   static constexpr int kPitch = D * 2 + 16;
   static constexpr int kStageBytes = 2 * kRows * kPitch;  // K and V rows of a warp
-  // Bytes in flight an SM: (stages - 1) of blocks x warps x 64 d.  Shared
-  // memory holds 228 KB an SM, and 8 to 16 warps keep the issue slots fed.
-  static constexpr int kBlocks = D == 32 ? 4 : D == 64 ? 3 : D == 256 ? 1 : 2;  // an SM
+  // Bytes in flight an SM: (stages - 1) of blocks x warps x 64 d.
+  static constexpr int kBlocks = blocks_an_sm(true, D);
   static constexpr int kStages = D == 32 || D == 96 ? 4 : 3;
   // the place in a row of the piece that lane q multiplies in step c, in pieces
   __host__ __device__ static constexpr int k_piece(int c, int q) {
@@ -86,17 +85,27 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, int NH>
+// kAlone: a cluster an item, joined here; else a block a run.
+template <int D, int NH, bool kAlone>
 __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(const __grid_constant__ DecodeParams a) {
   using M = Mma<D>;
   constexpr int kTile = M::kTile, kStages = M::kStages, VW = M::kVW;
   constexpr int kHeads = 8 * NH;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 ml[kWarps][kHeads];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
+  __shared__ float2 part_ml[kHeads];  // kAlone: this block's part, with o in part_o
+  float4* part_o = reinterpret_cast<float4*>(smem);  // over the ring, which is read by then
   Place<kTile> at;
   int64_t end;
-  if (!run_of(a, &at, &end)) return;
+  bool some;
+  if constexpr (kAlone) {
+    some = share_of_item(a, &at, &end);
+    if (!some && threadIdx.x < kHeads) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
+    some = run_of(a, &at, &end);
+    if (!some) return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * M::kStageBytes;
   float* exchange = reinterpret_cast<float*>(smem + M::kRing);
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   float m[NH], l[NH];                 // of heads g, g + 8; l of this lane's keys alone
   int begin = at.t;                   // tile at which the item (or this block's part of it) began
   int stage = 0;
-  bool first = true, last = false;    // item of the run
+  bool first = true, last = !some;    // item of the run
 
   for (bool fresh = true; !last; fresh = false) {
     Place<kTile> next = at;
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
 
     if (at.t + 1 == at.tiles || last) {
       // ---- the item ends here, or goes on in the next block's run
-      const bool whole = begin == 0 && at.t + 1 == at.tiles;
+      const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
       const int slot = 2 * blockIdx.x + (first ? 0 : 1);
@@ -289,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             if (whole) {
               o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
               store4<__nv_bfloat16>(a.O + at.s * a.os + (int64_t)(h0 + 8 * u + head) * a.oh, c * VW + col, o);
+            } else if (kAlone) {
+              part_o[((8 * u + head) * D + c * VW + col) / 4] = o;
             } else {
               *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * kHeads + 8 * u + head) * D + c * VW + col) = o;
             }
@@ -297,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
         if (mine && col == 0) {
           if (whole)
             a.L[(int64_t)at.s * a.H + h0 + 8 * u + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
+          else if (kAlone)
+            part_ml[8 * u + head] = make_float2(top, sum);
           else
             a.part_ml[(int64_t)slot * kHeads + 8 * u + head] = make_float2(top, sum);
         }
@@ -304,20 +317,15 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     }
     at = next;
   }
+  if (kAlone && a.cluster > 1) join_cluster<__nv_bfloat16, D>(a, part_o, part_ml);
 }
 
 template <int D, int NH>
-cudaError_t launch_mma(const Cut& k, DecodeParams a, cudaStream_t s) {
-  using M = Mma<D>;
-  static std::atomic<int> known[64];
-  int resident = 0;
-  cudaError_t e = resident_blocks((const void*)decode_mma_kernel<D, NH>, M::kSmem, known, &resident);
-  if (e != cudaSuccess) return e;
-  const int blocks = blocks_of(k, resident, &a);
-  decode_mma_kernel<D, NH><<<blocks, kThreads, M::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<__nv_bfloat16, D, M::kTile>(k, a, blocks, s);
+cudaError_t launch_mma(const Cut& k, const DecodeParams& a, cudaStream_t s) {
+  static std::atomic<int> known[64], known_alone[64];
+  return launch_decode<__nv_bfloat16, D, Mma<D>::kTile>(k, a, decode_mma_kernel<D, NH, false>,
+                                                        decode_mma_kernel<D, NH, true>, Mma<D>::kSmem, known,
+                                                        known_alone, s);
 }
 
 template <int D>
@@ -354,7 +362,7 @@ extern "C" {
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H) {
   if (fa::check_heads(c, H) != FA_OK) return 0;
   const fa::Cut k = fa::cut_of(*c, H);
-  if (k.most_tiles <= 1) return 0;
+  if (k.cluster > 0 || k.most_tiles <= 1) return 0;  // no parts, or none in global memory
   return (size_t)k.parts() * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
 }
 

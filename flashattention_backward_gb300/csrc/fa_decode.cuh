@@ -9,8 +9,15 @@
 // run: one of an item that began in an earlier run and one of an item that
 // goes on in the next one.  decode_join_kernel adds the parts of an item up, in
 // the order of the runs: no atomics, the same sums each time.
+//
+// Small tables.  Where no item can have more than kClusterTiles tiles for each
+// of a cluster's blocks, and a cluster an item fills no more than the GPU, each
+// item is read by a cluster, whose blocks join their parts through one
+// another's shared memory: no second kernel, no search for the run, no
+// workspace.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -25,6 +32,7 @@ namespace fa {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxRuns = 1280;
+constexpr int kMostBlocks = 16;  // of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -44,11 +52,18 @@ struct DecodeParams {
   int num_pages, max_pages;
   int cap;            // page_rows * max_pages
   int resident;       // blocks that run at a time
+  int cluster;        // blocks an item, if each item has a cluster; else 0
   int64_t table_stride;
   int64_t qs, qh, os, oh;  // byte strides
   int64_t pp, ph, pn;
   float scale2;       // scale * log2(e)
 };
+
+// Blocks an SM holds of the kernel for that type and head dim: what its ring of
+// tiles in shared memory (228 KB an SM) leaves room for.
+constexpr int blocks_an_sm(bool bf16, int d) {
+  return bf16 ? (d == 32 ? 4 : d == 64 ? 3 : d == 256 ? 1 : 2) : (d == 16 ? 4 : d == 32 ? 3 : d == 64 ? 2 : 1);
+}
 
 // ------------------------------------------------------------- sharing out
 __device__ __forceinline__ int rows_of(const DecodeParams& a, int s) {
@@ -333,6 +348,61 @@ __device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, 
   return at->unit < *end;
 }
 
+// With a cluster an item: this block's tiles of its item, the k-th of n equal
+// shares; false if it has none.
+template <int kTile>
+__device__ __forceinline__ bool share_of_item(const DecodeParams& a, Place<kTile>* at, int64_t* end) {
+  const int k = blockIdx.x % a.cluster, n = blockIdx.x / a.cluster;
+  at->s = n / a.items;
+  at->item = n - at->s * a.items;
+  at->rows = rows_of(a, at->s);
+  at->tiles = tiles_of<kTile>(at->rows);
+  at->t = (int)((int64_t)at->tiles * k / a.cluster);
+  at->unit = at->t;
+  *end = (int64_t)at->tiles * (k + 1) / a.cluster;
+  return at->unit < *end;
+}
+
+// Joins the parts of a cluster's blocks: o [heads][D] and ml [heads] in the
+// shared memory of each, m = -inf where a block saw nothing (its o is not
+// read).  Every thread of the cluster calls it.
+template <class T, int D>
+__device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4* o_part, const float2* ml_part) {
+  constexpr int kLanes = D / 4, kMost = kMostBlocks;
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int n = blockIdx.x / a.cluster, s = n / a.items;
+  int kv, heads;
+  const int h0 = item_first_head(a, n - s * a.items, &kv, &heads);
+  cluster.sync();  // the parts are there
+  for (int k = cluster.block_rank() * kThreads + threadIdx.x; k < heads * kLanes; k += a.cluster * kThreads) {
+    const int head = k / kLanes;
+    float2 ml[kMost];
+    float m = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+      ml[r] = r < a.cluster ? cluster.map_shared_rank(ml_part, r)[head] : make_float2(-INFINITY, 0.f);
+      m = fmaxf(m, ml[r].x);
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+      if (ml[r].x == -INFINITY) continue;
+      const float4 v = cluster.map_shared_rank(o_part, r)[k];
+      const float w = ptx::ex2(ml[r].x - m);
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      l = fmaf(w, ml[r].y, l);
+    }
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    store4<T>(a.O + s * a.os + (int64_t)(h0 + head) * a.oh, 4 * (k % kLanes), o);
+    if (k % kLanes == 0) a.L[(int64_t)s * a.H + h0 + head] = none ? INFINITY : (m + log2f(l)) * kLn2;
+  }
+  cluster.sync();  // no block leaves while another reads its part
+}
+
 // ------------------------------------------------------------------- joining
 // Block (r, y): some heads (`together` of them, from y * together) of one item,
 // item r if there are no more items than runs (by_item), else the one that run
@@ -442,6 +512,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 struct Cut {
   int split, item_heads, part_heads;  // items a group is cut into, heads of an item, heads of a part's slots
   int64_t tiles, most_tiles;          // at most: of all items, of one
+  int cluster;                        // blocks an item, or 0: runs
   // units are tiles and kItemCost for every item, and no item has less than one tile
   int64_t units() const { return tiles * (1 + kItemCost); }
   int64_t parts() const { return 2 * (units() < kMaxRuns ? units() : kMaxRuns); }
@@ -449,6 +520,20 @@ struct Cut {
 
 // Rows of a tile.
 inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 256 ? 32 : 64; }
+
+// Each item gets a cluster of as many blocks (1, 2, 4, 8 or 16) as fit the GPU
+// at a time, if that leaves at most kClusterTiles tiles a block.  Beyond that
+// the runs are quicker: they use all SMs, and a block alone on its SM takes
+// 1.1 us a tile (GPU time of 4 sequences of up to 4000 rows, 16 heads on one of
+// d 128: CLUSTERTIMES).
+constexpr int kClusterTiles = 4;
+constexpr int kClusterSms = 148;
+inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
+  const int64_t room = (int64_t)kClusterSms * blocks_an_sm(c.dtype == FA_BF16, c.d);
+  int n = kMostBlocks;
+  while (n > 1 && (items * n > room || n / 2 >= most_tiles)) n /= 2;
+  return items * n <= room && most_tiles <= n * kClusterTiles ? n : 0;
+}
 
 inline Cut cut_of(const fa_cache& c, int H) {
   Cut k;
@@ -462,7 +547,9 @@ inline Cut cut_of(const fa_cache& c, int H) {
   else
     k.part_heads = k.item_heads == 1 ? 1 : k.item_heads <= 4 ? 4 : 8;
   k.most_tiles = ceil_div(cache_rows(c), tile_rows(c));
-  k.tiles = (int64_t)c.S * c.H_kv * k.split * k.most_tiles;
+  const int64_t items = (int64_t)c.S * c.H_kv * k.split;
+  k.tiles = items * k.most_tiles;
+  k.cluster = cluster_of(c, items, k.most_tiles);
   return k;
 }
 
@@ -507,12 +594,44 @@ inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int
   *blocks = known[dev].load(std::memory_order_acquire);
   if (*blocks > 0) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // clusters of 16 blocks
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a_sm, kernel, kThreads, smem);
   if (e != cudaSuccess) return e;
   *blocks = a_sm * sm_count();
   if (*blocks < 1) return cudaErrorInvalidConfiguration;
   known[dev].store(*blocks, std::memory_order_release);
   return cudaSuccess;
+}
+
+// Launches `alone` with a cluster an item, or `kernel` with a block a run and the join.
+template <class T, int D, int kTile>
+cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodeParams), void (*alone)(DecodeParams),
+                          int smem, std::atomic<int>* known, std::atomic<int>* known_alone, cudaStream_t s) {
+  int resident = 0;
+  a.cluster = k.cluster;
+  cudaError_t e = resident_blocks(k.cluster > 0 ? (const void*)alone : (const void*)kernel, smem,
+                                  k.cluster > 0 ? known_alone : known, &resident);
+  if (e != cudaSuccess) return e;
+  if (k.cluster > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.S * a.items * k.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, alone, a);
+  }
+  const int blocks = blocks_of(k, resident, &a);
+  kernel<<<blocks, kThreads, smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || k.most_tiles <= 1) return e;
+  return launch_join<T, D, kTile>(k, a, blocks, s);
 }
 
 cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);

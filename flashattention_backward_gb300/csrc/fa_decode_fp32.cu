@@ -31,8 +31,7 @@ struct Simt {
   static constexpr int kPitch = D * 4 + 16;        // rows start on different banks
   static constexpr int kStageBytes = 2 * kRows * kPitch;
   static constexpr int kStages = D == 16 ? 4 : 3;
-  // blocks an SM: what shared memory holds (a ring is 40 to 203 KB)
-  static constexpr int kBlocks = D == 16 ? 4 : D == 32 ? 3 : D == 64 ? 2 : 1;
+  static constexpr int kBlocks = blocks_an_sm(false, D);
   static constexpr int kLanes = D == 96 ? 8 : kPieces < 32 ? kPieces : 32;  // of a row of V
   static constexpr int kCols = kPieces / kLanes;   // pieces a lane holds
   static constexpr int kGroups = 32 / kLanes;      // rows of V a warp takes at a time
@@ -51,7 +50,8 @@ __device__ __forceinline__ float dot4(float4 q, float4 k, float s) {
   return fmaf(q.w, k.w, fmaf(q.z, k.z, fmaf(q.y, k.y, fmaf(q.x, k.x, s))));
 }
 
-template <int D, int HR>
+// kAlone: a cluster an item, joined here; else a block a run.
+template <int D, int HR, bool kAlone>
 __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     decode_simt_kernel(const __grid_constant__ DecodeParams a) {
   using M = Simt<D, HR>;
@@ -59,10 +59,19 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 ml[kWarps][HR];
   __shared__ __align__(16) float factors[kWarps][HR];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
+  __shared__ float2 part_ml[HR];  // kAlone: this block's part, with o in part_o
+  float4* part_o = reinterpret_cast<float4*>(smem);  // over the ring, which is read by then
   Place<kTile> at;
   int64_t end;
-  if (!run_of(a, &at, &end)) return;
+  bool some;
+  if constexpr (kAlone) {
+    some = share_of_item(a, &at, &end);
+    if (!some && threadIdx.x < HR) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
+    some = run_of(a, &at, &end);
+    if (!some) return;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const uint8_t* ring = smem + warp * kStages * M::kStageBytes;
   float* qs = reinterpret_cast<float*>(smem + M::kQ);
@@ -76,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
   float m[M::kOwn], l[M::kOwn];
   int begin = at.t;
   int stage = 0;
-  bool first = true, last = false;
+  bool first = true, last = !some;
 
   for (bool fresh = true; !last; fresh = false) {
     Place<kTile> next = at;
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
 
     if (at.t + 1 == at.tiles || last) {
       // ---- the item ends here, or goes on in the next block's run
-      const bool whole = begin == 0 && at.t + 1 == at.tiles;
+      const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
       const int slot = 2 * blockIdx.x + (first ? 0 : 1);
@@ -263,6 +272,9 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
             o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             store4<float>(a.O + at.s * a.os + (int64_t)(h0 + head) * a.oh, 4 * piece, o);
             if (piece == 0) a.L[(int64_t)at.s * a.H + h0 + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
+          } else if (kAlone) {
+            part_o[head * M::kPieces + piece] = o;
+            if (piece == 0) part_ml[head] = make_float2(top, sum);
           } else {
             const int64_t p = (int64_t)slot * HR + head;
             *reinterpret_cast<float4*>(a.part_o + p * D + 4 * piece) = o;
@@ -273,20 +285,15 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     }
     at = next;
   }
+  if (kAlone && a.cluster > 1) join_cluster<float, D>(a, part_o, part_ml);
 }
 
 template <int D, int HR>
-cudaError_t launch_simt(const Cut& k, DecodeParams a, cudaStream_t s) {
+cudaError_t launch_simt(const Cut& k, const DecodeParams& a, cudaStream_t s) {
   using M = Simt<D, HR>;
-  static std::atomic<int> known[64];
-  int resident = 0;
-  cudaError_t e = resident_blocks((const void*)decode_simt_kernel<D, HR>, M::kSmem, known, &resident);
-  if (e != cudaSuccess) return e;
-  const int blocks = blocks_of(k, resident, &a);
-  decode_simt_kernel<D, HR><<<blocks, kThreads, M::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<float, D, M::kTile>(k, a, blocks, s);
+  static std::atomic<int> known[64], known_alone[64];
+  return launch_decode<float, D, M::kTile>(k, a, decode_simt_kernel<D, HR, false>, decode_simt_kernel<D, HR, true>,
+                                           M::kSmem, known, known_alone, s);
 }
 
 template <int D>

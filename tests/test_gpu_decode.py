@@ -35,11 +35,13 @@ def _lib():
     assert fa.get_device_status() == 0
 
 
-def make(S, H, Hk, d, page, lengths, dtype=torch.bfloat16, seed=0, rows_first=False, spare=2, junk=True, q_std=1.0):
-    """A cache with pages in random order; what no row reads is NaN."""
+def make(S, H, Hk, d, page, lengths, dtype=torch.bfloat16, seed=0, rows_first=False, spare=2, junk=True, q_std=1.0, wide=0):
+    """A cache with pages in random order; what no row reads is NaN.  wide: more columns of the table.  How the work is
+    shared out goes by the rows that the table could hold: an item of a narrow one is read by a cluster of blocks, those
+    of a wide one by equal runs of all of them and a second kernel."""
     gen = torch.Generator().manual_seed(seed)
     held = [-(-n // page) for n in lengths]
-    pages, columns = sum(held) + spare, max(held + [1]) + 1
+    pages, columns = sum(held) + spare, max(held + [1]) + 1 + wide
     order = torch.randperm(pages, generator=gen)
     table = torch.full((S, columns), -1, dtype=torch.int32)
     shape = (pages, page, Hk, d) if rows_first else (pages, Hk, page, d)
@@ -100,16 +102,18 @@ BF16_DIMS, FP32_DIMS = (32, 64, 96, 128, 256), (16, 32, 64, 96, 128, 256)
 
 @pytest.mark.parametrize("d", BF16_DIMS)
 @pytest.mark.parametrize("H,Hk", [(4, 4), (6, 2), (16, 2), (12, 1), (16, 1), (40, 2)])
-def test_head_layouts_bf16(d, H, Hk):
+@pytest.mark.parametrize("wide", [0, 3000])
+def test_head_layouts_bf16(d, H, Hk, wide):
     lengths = [0, 1, 15, 16, 17, 63, 64, 65, 300]
-    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, seed=d + H))
+    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, seed=d + H, wide=wide))
 
 
 @pytest.mark.parametrize("d", FP32_DIMS)
 @pytest.mark.parametrize("H,Hk", [(3, 3), (6, 2), (9, 1), (16, 2)])
-def test_head_layouts_fp32(d, H, Hk):
+@pytest.mark.parametrize("wide", [0, 3000])
+def test_head_layouts_fp32(d, H, Hk, wide):
     lengths = [0, 1, 15, 16, 17, 63, 64, 65, 300]
-    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, torch.float32, seed=d + H))
+    run_and_check(make(len(lengths), H, Hk, d, 16, lengths, torch.float32, seed=d + H, wide=wide))
 
 
 @pytest.mark.parametrize("page", [1, 2, 3, 7, 13, 16, 48, 64, 100, 256, 1000])
@@ -123,8 +127,9 @@ def test_page_sizes(page, rows_first):
 @pytest.mark.parametrize("n", [1, 64, 65, 2048, 4000, 32768])
 @pytest.mark.parametrize("H,Hk,d,dtype", [(8, 1, 128, torch.bfloat16), (2, 2, 64, torch.bfloat16),
                                           (2, 1, 256, torch.bfloat16), (2, 1, 96, torch.float32)])
-def test_one_sequence_over_the_whole_gpu(n, H, Hk, d, dtype):
-    run_and_check(make(1, H, Hk, d, 64, [n], dtype, seed=n))
+@pytest.mark.parametrize("wide", [0, 600])
+def test_one_sequence_over_the_whole_gpu(n, H, Hk, d, dtype, wide):
+    run_and_check(make(1, H, Hk, d, 64, [n], dtype, seed=n, wide=wide))
 
 
 def test_many_short_and_one_long():
@@ -157,8 +162,19 @@ def test_enough_rows_for_small_runs(d, dtype, Hk, S, n):
         check((o[one], L[one]), q[one], kp, vp, table, lengths[one], d ** -0.5)
 
 
-def test_all_empty():
-    run_and_check(make(3, 4, 2, 64, 16, [0, 0, 0]))
+@pytest.mark.parametrize("wide", [0, 3000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_all_empty(wide, dtype):
+    run_and_check(make(3, 4, 2, 64, 16, [0, 0, 0], dtype, wide=wide))
+
+
+@pytest.mark.parametrize("S,n", [(1, 4000), (9, 1000), (18, 500), (36, 250), (74, 250), (148, 250), (300, 250), (700, 60)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_clusters_of_every_size(S, n, dtype):
+    """As many blocks an item as the GPU holds at a time: 16, 8, 4, 2, 1, or more
+    items than that, with full and partly empty shares."""
+    lengths = [max(0, n - 7 * (i % 50)) for i in range(S)]
+    run_and_check(make(S, 4, 1, 128, 64, lengths, dtype, seed=S))
 
 
 def test_peaked_scores():
@@ -182,7 +198,7 @@ def test_scale(scale):
 
 
 def test_strided_queries_and_given_outputs():
-    q, kp, vp, table, lengths = make(5, 8, 2, 64, 16, [100, 0, 7, 64, 1000], seed=9)
+    q, kp, vp, table, lengths = make(5, 8, 2, 64, 16, [100, 0, 7, 64, 1000], seed=9, wide=3000)
     fused = torch.randn(5, 12, 64, device=DEV).to(torch.bfloat16)  # queries, keys and values of one projection
     view = fused[:, 2:10, None, :]
     o_all = torch.full((5, 10, 1, 64), 7.0, device=DEV, dtype=torch.bfloat16)
@@ -217,9 +233,10 @@ def test_offsets_beyond_32_bits():
     check(got, q, *small, torch.tensor([[0, 1, 2, 3]], dtype=torch.int32), lengths, d ** -0.5)
 
 
+@pytest.mark.parametrize("wide", [0, 3000])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_bad_pages_and_lengths_are_not_followed(dtype):
-    q, kp, vp, table, lengths = make(4, 4, 2, 64, 16, [100, 50, 300, 20], dtype, seed=12)
+def test_bad_pages_and_lengths_are_not_followed(dtype, wide):
+    q, kp, vp, table, lengths = make(4, 4, 2, 64, 16, [100, 50, 300, 20], dtype, seed=12, wide=wide)
     table[0, 2], table[2, 5] = 1 << 20, -7
     got = fa.attention_decode(q, kp, vp, table, lengths)
     assert fa.get_device_status() == fa.FA_ERR_PAGES
@@ -234,16 +251,18 @@ def test_bad_pages_and_lengths_are_not_followed(dtype):
     assert fa.get_device_status() == 0
 
 
-def test_same_call_same_bits():
-    args = make(7, 8, 2, 128, 16, [4000, 1, 900, 0, 77, 3333, 512], seed=13)
+@pytest.mark.parametrize("wide", [0, 3000])
+def test_same_call_same_bits(wide):
+    args = make(7, 8, 2, 128, 16, [4000, 1, 900, 0, 77, 3333, 512], seed=13, wide=wide)
     a = fa.attention_decode(*args)
     for _ in range(5):
         b = fa.attention_decode(*args)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_two_streams_at_once():
-    args = [make(4, 8, 2, 128, 16, [4000, 100, 1700, 64], seed=20 + i) for i in range(2)]
+@pytest.mark.parametrize("wide", [0, 3000])
+def test_two_streams_at_once(wide):
+    args = [make(4, 8, 2, 128, 16, [4000, 100, 1700, 64], seed=20 + i, wide=wide) for i in range(2)]
     want = [fa.attention_decode(*a) for a in args]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -257,9 +276,10 @@ def test_two_streams_at_once():
     assert fa.get_device_status() == 0
 
 
-def test_graph_follows_lengths_that_change():
+@pytest.mark.parametrize("wide", [0, 3000])
+def test_graph_follows_lengths_that_change(wide):
     """A captured call reads lengths and table at each replay; two graphs replayed at once have workspaces of their own."""
-    q, kp, vp, table, lengths = make(3, 8, 2, 64, 16, [2000, 900, 50], seed=30, junk=False)
+    q, kp, vp, table, lengths = make(3, 8, 2, 64, 16, [2000, 900, 50], seed=30, junk=False, wide=wide)
     pairs = []
     torch.cuda.synchronize()
     for _ in range(2):
