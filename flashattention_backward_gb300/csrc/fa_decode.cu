@@ -264,18 +264,6 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
           for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k][8 * u + 2 * q + e].x);
           f[e] = ptx::ex2(ml[warp][8 * u + 2 * q + e].x - base_of(top));
         }
-        // the head and the four columns that this thread adds up
-        const int head = threadIdx.x / (VW / 4), col = threadIdx.x % (VW / 4) * 4;
-        float top = -INFINITY, sum = 0.f;
-        if (head < 8) {
-#pragma unroll
-          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k][8 * u + head].x);
-#pragma unroll
-          for (int k = 0; k < kWarps; ++k) sum += ml[k][8 * u + head].y * ptx::ex2(ml[k][8 * u + head].x - base_of(top));
-        }
-        const bool mine = head < 8 && 8 * u + head < heads;
-        const bool none = sum == 0.f;
-        const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll
         for (int c = 0; c < D / VW; ++c) {
           if (u + c > 0) __syncthreads();
@@ -288,30 +276,36 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
                   make_float4(acc[u][c][x][e] * f[e], acc[u][c][x][2 + e] * f[e], acc[u][c][x + 1][e] * f[e],
                               acc[u][c][x + 1][2 + e] * f[e]);
           __syncthreads();
-          if (mine) {
+          // a thread adds up four columns of a head
+#pragma unroll
+          for (int k0 = 0; k0 < 2 * VW; k0 += kThreads) {
+            const int k = k0 + threadIdx.x, in8 = k / (VW / 4), col = c * VW + k % (VW / 4) * 4, head = 8 * u + in8;
+            if (in8 >= 8 || head >= heads) continue;
+            float top = -INFINITY, sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-              const float4 x = *reinterpret_cast<const float4*>(exchange + (k * 8 + head) * M::kPad + col);
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][head].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              sum += ml[w][head].y * ptx::ex2(ml[w][head].x - base_of(top));
+              const float4 x = *reinterpret_cast<const float4*>(exchange + (w * 8 + in8) * M::kPad + col - c * VW);
               o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             }
             if (whole) {
+              const bool none = sum == 0.f;
+              const float inv = none ? 0.f : 1.f / sum;
               o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-              store4<__nv_bfloat16>(a.O + at.s * a.os + (int64_t)(h0 + 8 * u + head) * a.oh, c * VW + col, o);
+              store4<__nv_bfloat16>(a.O + at.s * a.os + (int64_t)(h0 + head) * a.oh, col, o);
+              if (col == 0) a.L[(int64_t)at.s * a.H + h0 + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
             } else if (kAlone) {
-              part_o[((8 * u + head) * D + c * VW + col) / 4] = o;
+              part_o[(head * D + col) / 4] = o;
+              if (col == 0) part_ml[head] = make_float2(top, sum);
             } else {
-              *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * kHeads + 8 * u + head) * D + c * VW + col) = o;
+              const int64_t p = (int64_t)slot * kHeads + head;
+              *reinterpret_cast<float4*>(a.part_o + p * D + col) = o;
+              if (col == 0) a.part_ml[p] = make_float2(top, sum);
             }
           }
-        }
-        if (mine && col == 0) {
-          if (whole)
-            a.L[(int64_t)at.s * a.H + h0 + 8 * u + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
-          else if (kAlone)
-            part_ml[8 * u + head] = make_float2(top, sum);
-          else
-            a.part_ml[(int64_t)slot * kHeads + 8 * u + head] = make_float2(top, sum);
         }
       }
     }
