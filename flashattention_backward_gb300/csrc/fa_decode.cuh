@@ -411,13 +411,16 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4
 // find that out while the kernel in front still runs.  D / 4 threads hold a row
 // of o; of the block's groups of so many threads, `together` take a head each
 // and the others share its parts, kAhead loads at a time.
-constexpr int kJoinThreads = 256;
+// 128 threads and their 2.2 KB of shared memory fit beside the blocks of the
+// kernel in front, so the join is there when those end: 64 sequences of up to
+// 8192 rows took 153.5 us, with 256 threads 156.4.
+constexpr int kJoinThreads = 128;
 
 template <class T, int D, int kTile, bool kAlone>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
                                                                    int part_heads, int by_item, int heads_together) {
   const int together = kAlone ? 1 : heads_together;
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 8;
   __shared__ float4 os[kGroups][kLanes];
   __shared__ float2 mls[kGroups];
   __shared__ int64_t sums[kJoinThreads / 32];
@@ -523,9 +526,10 @@ inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 25
 
 // Each item gets a cluster of as many blocks (1, 2, 4, 8 or 16) as fit the GPU
 // at a time, if that leaves at most kClusterTiles tiles a block.  Beyond that
-// the runs are quicker: they use all SMs, and a block alone on its SM takes
-// 1.1 us a tile (GPU time of 4 sequences of up to 4000 rows, 16 heads on one of
-// d 128: CLUSTERTIMES).
+// the runs are quicker, which use all SMs: a block alone on its SM takes 1.1 us a
+// tile.  GPU time of 4 sequences of up to 4000 rows, 16 heads on one of d 128:
+// 12.6 us with 8 blocks of 8 tiles, 9.5 with 16 of 4, 8.6 in runs; but the runs'
+// second launch and workspace cost the caller's thread 7 us.
 constexpr int kClusterTiles = 4;
 constexpr int kClusterSms = 148;
 inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
