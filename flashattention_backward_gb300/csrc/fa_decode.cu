@@ -7,7 +7,7 @@
 // and o add up with the factors 2^(m_i - m).
 //
 // Every row of the cache is read once for the group of query heads that share
-// it, 2 d elements a row against 4 d multiply-adds a query head: with 8 heads a
+// it, 2 d elements a row against 4 d flops a query head: with 8 heads a
 // group that is 8 flops a byte in bf16, far below what the tensor cores need
 // to be the limit.  HBM is, so the design is about loads: all SMs have an
 // equal share of the rows, whatever the lengths, and each keeps about 100 KB
@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     if (!some) return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int piece = (kAlone ? blockIdx.x / a.cluster : blockIdx.x) % a.split;
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * M::kStageBytes;
   float* exchange = reinterpret_cast<float*>(smem + M::kRing);
-  Loader<kTile, M::kRows, M::kPieces, M::kPitch, kStages> load(a, at, end, ring);
+  Loader<kTile, M::kRows, M::kPieces, M::kPitch, kStages> load(a, at, end, ring, piece);
 
   uint32_t qf[NH][D / 32][4];
   float acc[NH][D / VW][VW / 16][4];  // O^T, unnormalised
@@ -125,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
     const uint32_t seen = load.next(stage);
 
     if (fresh || at.t == 0) {
-      int kv, heads;
-      const int h0 = item_first_head(a, at.item, &kv, &heads);
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
       const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
@@ -241,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
       const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
-      const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+      const int slot = (2 * (blockIdx.x / a.split) + (first ? 0 : 1)) * a.split + piece;
       first = false;
-      int kv, heads;
-      const int h0 = item_first_head(a, at.item, &kv, &heads);
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
       __syncthreads();  // ml and the exchange buffer have been read
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
@@ -332,7 +333,7 @@ fa_status check_heads(const fa_cache* c, int32_t H) {
   const fa_status st = check_cache(c);
   if (st != FA_OK) return st;
   if (H < 1 || H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
-  if ((int64_t)c->S * H > (1 << 24)) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)c->S * H > (1 << 24) || H / c->H_kv > kMostHeads) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -393,8 +394,8 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
   a.H = H;
   a.group = H / c->H_kv;
   a.split = k.split;
-  a.item_heads = k.item_heads;
-  a.items = c->H_kv * k.split;
+  a.piece_heads = k.piece_heads;
+  a.items = c->H_kv;
   a.num_pages = c->num_pages;
   a.max_pages = c->max_pages;
   a.cap = (int)fa::cache_rows(*c);

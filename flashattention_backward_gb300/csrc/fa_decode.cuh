@@ -1,14 +1,18 @@
 // Shared by the kernels of fa_decode (fa_decode.cu, bf16, and
 // fa_decode_fp32.cu): how the work is shared out, and the joining of parts.
 //
-// Work.  An item is one sequence, one key-value head and some of its query
-// heads; a tile is kTile rows of an item.  All tiles of all items in order are
+// Work.  An item is one sequence and one key-value head; a tile is kTile rows of
+// an item.  All tiles of all items in order are
 // cut into runs, one for each block.  A block finds its run from the lengths
 // itself: the host knows none of them.  A run may end inside an item.  What a
 // block has then goes to the workspace as (m, l, o), at most two such parts a
 // run: one of an item that began in an earlier run and one of an item that
 // goes on in the next one.  decode_join_kernel adds the parts of an item up, in
 // the order of the runs: no atomics, the same sums each time.
+//
+// Query heads.  Up to 16 (8 in fp32) share one reading of the cache.  Larger
+// groups are cut evenly, and as many blocks take each run, side by side, so
+// that all but the first find its rows in L2.
 //
 // Small tables.  Where no item can have more than kClusterTiles tiles for each
 // of a cluster's blocks, and a cluster an item fills no more than the GPU, each
@@ -33,6 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxRuns = 1280;
 constexpr int kMostBlocks = 16;  // of a cluster
+constexpr int kMostHeads = 512;  // query heads that share a key-value head
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -42,13 +47,13 @@ struct DecodeParams {
   float* L;
   const int32_t *table, *lengths;
   int32_t* status;
-  float2* part_ml;    // [2 runs][heads of an item]
-  float* part_o;      // [2 runs][heads of an item][d]
+  float2* part_ml;    // [2 runs][split][heads of a piece, rounded up]
+  float* part_o;      // the same, [d]
   FastDiv page_rows;
   int S, H, group;    // group: query heads that share a key-value head
-  int split;          // items a group is cut into
-  int item_heads;     // query heads of an item (the last of a group may have fewer)
-  int items;          // of a sequence: H_kv * split
+  int split;          // blocks that take a run: pieces a group of query heads is cut into
+  int piece_heads;    // query heads of a piece (the last of a group may have fewer)
+  int items;          // of a sequence: H_kv
   int num_pages, max_pages;
   int cap;            // page_rows * max_pages
   int resident;       // blocks that run at a time
@@ -223,12 +228,11 @@ struct Place {
   }
 };
 
-// The query heads of an item: the first one, and how many.
-__device__ __forceinline__ int item_first_head(const DecodeParams& a, int item, int* kv, int* heads) {
-  *kv = item / a.split;
-  const int part = item - *kv * a.split;
-  *heads = min(a.item_heads, a.group - part * a.item_heads);
-  return *kv * a.group + part * a.item_heads;
+// The piece of an item's query heads that this block takes, the first of them,
+// and how many.
+__device__ __forceinline__ int first_head(const DecodeParams& a, int item, int piece, int* heads) {
+  *heads = min(a.piece_heads, a.group - piece * a.piece_heads);
+  return item * a.group + piece * a.piece_heads;
 }
 
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
@@ -264,6 +268,7 @@ struct Loader {
   Place<kTile> at;      // the tile that is copied next
   const int64_t end;    // of the run
   const uint32_t ring;  // of this warp
+  const int piece;      // of the query heads
   uint64_t queue = 0;   // which rows of the tiles in flight are there, the oldest in the low 16 bits
   // The row that this lane looks up in that tile: its page is asked for one
   // tile ahead of the copies that need it.
@@ -271,8 +276,8 @@ struct Loader {
   bool in = false;
   int64_t off = 0;
 
-  __device__ __forceinline__ Loader(const DecodeParams& p, const Place<kTile>& first, int64_t e, uint32_t r)
-      : a(p), at(first), end(e), ring(r) {
+  __device__ __forceinline__ Loader(const DecodeParams& p, const Place<kTile>& first, int64_t e, uint32_t r, int h)
+      : a(p), at(first), end(e), ring(r), piece(h) {
     look_up();
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) produce(i);
@@ -284,10 +289,10 @@ struct Loader {
     const uint32_t col = a.page_rows.div((uint32_t)j, &r);
     in = j < at.rows;
     page = in ? __ldg(a.table + at.s * a.table_stride + col) : -1;
-    off = (int64_t)(at.item / a.split) * a.ph + (int64_t)r * a.pn;
+    off = at.item * a.ph + (int64_t)r * a.pn;
     if (at.t == 0) {  // a new item: its queries into L1
-      int kv, heads;
-      const char* row = a.Q + at.s * a.qs + (int64_t)item_first_head(a, at.item, &kv, &heads) * a.qh;
+      int heads;
+      const char* row = a.Q + at.s * a.qs + (int64_t)first_head(a, at.item, piece, &heads) * a.qh;
       constexpr int kLines = (kPieces * 16 + 127) / 128;
       for (int k = lane; k < heads * kLines; k += 32) prefetch_l1(row + (k / kLines) * a.qh + (k % kLines) * 128);
     }
@@ -339,20 +344,21 @@ __device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, 
   __shared__ int64_t sums[kWarps];
   Units<kTile, kThreads> units(a, sums);
   const Share share = units.share();
-  if ((int)blockIdx.x >= share.runs()) return false;
-  const int64_t x = share.first(blockIdx.x);
-  *end = share.first(blockIdx.x + 1);
+  const int run = blockIdx.x / a.split;
+  if (run >= share.runs()) return false;
+  const int64_t x = share.first(run);
+  *end = share.first(run + 1);
   int64_t base;
   const int s = units.find(x, 0, &base);
   at->set(a, s, base, x);
   return at->unit < *end;
 }
 
-// With a cluster an item: this block's tiles of its item, the k-th of n equal
+// With a cluster an item (and piece of its heads): this block's tiles of its item, the k-th of n equal
 // shares; false if it has none.
 template <int kTile>
 __device__ __forceinline__ bool share_of_item(const DecodeParams& a, Place<kTile>* at, int64_t* end) {
-  const int k = blockIdx.x % a.cluster, n = blockIdx.x / a.cluster;
+  const int k = blockIdx.x % a.cluster, n = blockIdx.x / a.cluster / a.split;
   at->s = n / a.items;
   at->item = n - at->s * a.items;
   at->rows = rows_of(a, at->s);
@@ -371,9 +377,9 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4
   constexpr int kLanes = D / 4, kMost = kMostBlocks;
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
-  const int n = blockIdx.x / a.cluster, s = n / a.items;
-  int kv, heads;
-  const int h0 = item_first_head(a, n - s * a.items, &kv, &heads);
+  const int n = blockIdx.x / a.cluster / a.split, s = n / a.items;
+  int heads;
+  const int h0 = first_head(a, n - s * a.items, blockIdx.x / a.cluster % a.split, &heads);
   cluster.sync();  // the parts are there
   for (int k = cluster.block_rank() * kThreads + threadIdx.x; k < heads * kLanes; k += a.cluster * kThreads) {
     const int head = k / kLanes;
@@ -404,32 +410,36 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4
 }
 
 // ------------------------------------------------------------------- joining
-// Block (r, y): some heads (`together` of them, from y * together) of one item,
-// item r if there are no more items than runs (by_item), else the one that run
-// r ends inside of if it also begins there: every item of several parts has
-// one such run.  Which parts it has follows from the lengths, so the blocks can
-// find that out while the kernel in front still runs.  D / 4 threads hold a row
-// of o; of the block's groups of so many threads, `together` take a head each
-// and the others share its parts, kAhead loads at a time.
+// Block (r, y): some query heads and columns of one item, item r if there are no
+// more items than runs (by_item), else the one that run r ends inside of if it
+// also begins there: every item of several parts has one such run.  Which parts
+// it has follows from the lengths, so the blocks can find that out while the
+// kernel in front still runs.  `lanes` threads hold a slice of a row of o; of
+// the block's groups of so many threads, `together` take a head each and the
+// others share its parts, kAhead loads at a time.
 // 128 threads and their 2.2 KB of shared memory fit beside the blocks of the
 // kernel in front, so the join is there when those end: 64 sequences of up to
 // 8192 rows took 153.5 us, with 256 threads 156.4.
 constexpr int kJoinThreads = 128;
+struct JoinShape {
+  int by_item, part_heads;
+  int together;  // heads a block takes
+  int slices;    // blocks that a head's columns are cut into; 1 if together > 1
+};
 
-template <class T, int D, int kTile, bool kAlone>
+template <class T, int D, int kTile>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
-                                                                   int part_heads, int by_item, int heads_together) {
-  const int together = kAlone ? 1 : heads_together;
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 8;
-  __shared__ float4 os[kGroups][kLanes];
-  __shared__ float2 mls[kGroups];
+                                                                   const JoinShape j) {
+  constexpr int kAhead = 8;
+  __shared__ float4 os[kJoinThreads];
+  __shared__ float2 mls[kJoinThreads / (D / 16)];  // a group has D / 16 threads at least
   __shared__ int64_t sums[kJoinThreads / 32];
   int s = 0, item = 0, run = 0, slot = 0, following = 0;
   {
     Units<kTile, kJoinThreads> units(a, sums);
     const Share share = units.share();
     int64_t base = 0;
-    if (by_item) {
+    if (j.by_item) {
       s = blockIdx.x / a.items;
       item = blockIdx.x - s * a.items;
       units.find(-1, s, &base);
@@ -440,25 +450,26 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     }
     const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
     run = share.run_of(begin + kItemCost);
-    if (by_item || run == (int)blockIdx.x) following = share.run_of(begin + kItemCost + tiles - 1) - run;
+    if (j.by_item || run == (int)blockIdx.x) following = share.run_of(begin + kItemCost + tiles - 1) - run;
     // a run that holds tiles before the item has it as its second part
     slot = share.first(run) < begin ? 1 : 0;
   }
-  int kv, heads;
-  const int h0 = item_first_head(a, item, &kv, &heads), head0 = blockIdx.y * together;
-  const bool some = following > 0 && head0 < heads;
+  const int head0 = blockIdx.y / j.slices * j.together;  // of the item's query heads
+  const int lanes = D / 4 / j.slices, groups = kJoinThreads / lanes;
+  const int grp = threadIdx.x / lanes, x = threadIdx.x - grp * lanes;
+  const int col = 4 * (blockIdx.y % j.slices * lanes + x);
+  const int sharing = groups / j.together, take = j.together * sharing;  // groups that share a head's parts, and all
   // What comes after this kernel on its stream waits for this kernel alone, so
   // it may not end before the one in front, even if it has nothing to join:
   // block (0, 0) waits in any case.
-  if (some || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!some) return;
-  const int grp = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
-  const int sharing = kGroups / together;  // groups that share a head's parts
-  if (grp < together * sharing) {
-    const int head = min(head0 + grp % together, heads - 1);
+  if (following > 0 || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (following == 0) return;
+  if (grp < take) {
+    const int h = min(head0 + grp % j.together, a.group - 1), piece = h / a.piece_heads;
+    const int head = h - piece * a.piece_heads;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
-    for (int k0 = grp / together; k0 <= following; k0 += sharing * kAhead) {
+    for (int k0 = grp / j.together; k0 <= following; k0 += sharing * kAhead) {
       float2 ml[kAhead];
       float4 v[kAhead];
 #pragma unroll
@@ -467,9 +478,9 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         ml[e] = make_float2(-INFINITY, 0.f);
         v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k > following) continue;
-        const int64_t p = (int64_t)(2 * (run + k) + (k == 0 ? slot : 0)) * part_heads + head;
+        const int64_t p = ((int64_t)(2 * (run + k) + (k == 0 ? slot : 0)) * a.split + piece) * j.part_heads + head;
         ml[e] = a.part_ml[p];
-        v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + 4 * x);
+        v[e] = *reinterpret_cast<const float4*>(a.part_o + p * D + col);
       }
       float top = m;
 #pragma unroll
@@ -485,40 +496,42 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       }
       m = top;
     }
-    os[grp][x] = o;
+    os[threadIdx.x] = o;
     if (x == 0) mls[grp] = make_float2(m, l);
   }
   __syncthreads();
-  if (grp >= together || head0 + grp >= heads) return;
+  if (grp >= j.together || head0 + grp >= a.group) return;
   float m = -INFINITY;
 #pragma unroll 8
-  for (int k = grp; k < together * sharing; k += together) m = fmaxf(m, mls[k].x);
+  for (int k = grp; k < take; k += j.together) m = fmaxf(m, mls[k].x);
   const float base = base_of(m);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
 #pragma unroll 8
-  for (int k = grp; k < together * sharing; k += together) {
-    const float4 v = os[k][x];
-    const float w = ptx::ex2(mls[k].x - base);
+  for (int k = grp; k < take; k += j.together) {
+    const float4 v = os[k * lanes + x];
+    const float2 ml = mls[k];
+    const float w = ptx::ex2(ml.x - base);
     o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-    l = fmaf(w, mls[k].y, l);
+    l = fmaf(w, ml.y, l);
   }
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
   o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  store4<T>(a.O + s * a.os + (int64_t)(h0 + head0 + grp) * a.oh, 4 * x, o);
-  if (x == 0) a.L[(int64_t)s * a.H + h0 + head0 + grp] = none ? INFINITY : (m + log2f(l)) * kLn2;
+  const int64_t h = (int64_t)item * a.group + head0 + grp;
+  store4<T>(a.O + s * a.os + h * a.oh, col, o);
+  if (col == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ----------------------------------------------------------------- launching
 // How a problem is cut: what the workspace's size and the launch go by.
 struct Cut {
-  int split, item_heads, part_heads;  // items a group is cut into, heads of an item, heads of a part's slots
+  int split, piece_heads, part_heads;  // pieces of a group, heads of a piece, the same rounded up
   int64_t tiles, most_tiles;          // at most: of all items, of one
   int cluster;                        // blocks an item, or 0: runs
   // units are tiles and kItemCost for every item, and no item has less than one tile
   int64_t units() const { return tiles * (1 + kItemCost); }
-  int64_t parts() const { return 2 * (units() < kMaxRuns ? units() : kMaxRuns); }
+  int64_t parts() const { return 2 * (units() * split < kMaxRuns ? units() * split : kMaxRuns); }
 };
 
 // Rows of a tile.
@@ -542,41 +555,39 @@ inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
 inline Cut cut_of(const fa_cache& c, int H) {
   Cut k;
   const int group = H / c.H_kv;
-  // up to 16 query heads (8 in fp32) share one reading of the cache; larger
-  // groups are cut evenly, and read it again (from L2 where it holds an item)
   k.split = (int)ceil_div(group, c.dtype == FA_BF16 ? 16 : 8);
-  k.item_heads = (int)ceil_div(group, k.split);
+  k.piece_heads = (int)ceil_div(group, k.split);
   if (c.dtype == FA_BF16)
-    k.part_heads = k.item_heads <= 8 ? 8 : 16;
+    k.part_heads = k.piece_heads <= 8 ? 8 : 16;
   else
-    k.part_heads = k.item_heads == 1 ? 1 : k.item_heads <= 4 ? 4 : 8;
+    k.part_heads = k.piece_heads == 1 ? 1 : k.piece_heads <= 4 ? 4 : 8;
   k.most_tiles = ceil_div(cache_rows(c), tile_rows(c));
-  const int64_t items = (int64_t)c.S * c.H_kv * k.split;
-  k.tiles = items * k.most_tiles;
-  k.cluster = cluster_of(c, items, k.most_tiles);
+  k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
+  k.cluster = cluster_of(c, (int64_t)c.S * c.H_kv * k.split, k.most_tiles);
   return k;
 }
 
-// The blocks of a launch: every run that the lengths can lead to.  Sets a->resident.
-inline int blocks_of(const Cut& k, int resident, DecodeParams* a) {
+// The runs that the lengths can lead to at most.  Sets a->resident.
+inline int runs_of(const Cut& k, int resident, DecodeParams* a) {
   if (resident > kMaxRuns / (1 + kSmallRuns)) resident = kMaxRuns / (1 + kSmallRuns);
+  resident /= k.split;  // at most kMostHeads / 8 = 64: some are left
   a->resident = resident;
   if (k.units() >= (int64_t)resident * kMinUnits) return resident * (1 + kSmallRuns);
   return (int)(k.units() < resident ? k.units() : resident);
 }
 
 template <class T, int D, int kTile>
-cudaError_t launch_join(const Cut& k, const DecodeParams& a, int blocks, cudaStream_t s) {
+cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int64_t items = (int64_t)a.S * a.items;
-  const int by_item = items <= blocks;
-  const int64_t x = by_item ? items : blocks;
-  // one head a block while that leaves few blocks: the parts are then read by
-  // all of its groups, which counts for few items of many parts
-  int together = 1;
-  while (x * ceil_div(a.item_heads, together) > 1024 && together < a.item_heads && 2 * together <= kJoinThreads / (D / 4))
-    together *= 2;
-  cfg.gridDim = dim3((unsigned)x, (unsigned)ceil_div(a.item_heads, together));
+  JoinShape j = {items <= runs, k.part_heads, 1, 1};
+  const int64_t x = j.by_item ? items : runs;
+  // few items of many parts: a head and then a slice of its columns a block, so
+  // that more threads read parts; many: several heads a block
+  while (x * a.group * j.slices < 304 && j.slices < 4) j.slices *= 2;
+  while (x * ceil_div(a.group, j.together) > 1024 && j.together < a.group && 2 * j.together <= kJoinThreads / (D / 4))
+    j.together *= 2;
+  cfg.gridDim = dim3((unsigned)x, (unsigned)(ceil_div(a.group, j.together) * j.slices));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   // its blocks may be there before the kernel in front ends, and wait for that themselves
@@ -585,8 +596,7 @@ cudaError_t launch_join(const Cut& k, const DecodeParams& a, int blocks, cudaStr
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, together == 1 ? decode_join_kernel<T, D, kTile, true> : decode_join_kernel<T, D, kTile, false>,
-                            a, k.part_heads, by_item, together);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, kTile>, a, j);
 }
 
 // How many blocks of a kernel the device holds at a time; raises the kernel's
@@ -619,7 +629,7 @@ cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodePar
   if (e != cudaSuccess) return e;
   if (k.cluster > 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.S * a.items * k.cluster));
+    cfg.gridDim = dim3((unsigned)(a.S * a.items * a.split * k.cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -631,11 +641,11 @@ cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodePar
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, alone, a);
   }
-  const int blocks = blocks_of(k, resident, &a);
-  kernel<<<blocks, kThreads, smem, s>>>(a);
+  const int runs = runs_of(k, resident, &a);
+  kernel<<<runs * a.split, kThreads, smem, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<T, D, kTile>(k, a, blocks, s);
+  return launch_join<T, D, kTile>(k, a, runs, s);
 }
 
 cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);

@@ -3,7 +3,7 @@
 // are those of fa_decode.cu; how the work is shared out and joined is in
 // fa_decode.cuh.
 //
-// 4 d multiply-adds a row of the cache for each of the query heads that share
+// 4 d flops a row of the cache for each of the query heads that share
 // it, against 8 d bytes: 4 flops a byte with 8 heads, a third of what the FMA
 // units could do while HBM sends it.  So here too the loads are what counts, but
 // the operands' way through shared memory has to stay short:
@@ -73,11 +73,12 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     if (!some) return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int piece = (kAlone ? blockIdx.x / a.cluster : blockIdx.x) % a.split;
   const uint8_t* ring = smem + warp * kStages * M::kStageBytes;
   float* qs = reinterpret_cast<float*>(smem + M::kQ);
   float* ps = reinterpret_cast<float*>(smem + M::kP) + warp * M::kRows * HR;
   float* exchange = reinterpret_cast<float*>(smem + M::kExchange);
-  Loader<kTile, M::kRows, M::kPieces, M::kPitch, kStages> load(a, at, end, ptx::smem_addr(ring));
+  Loader<kTile, M::kRows, M::kPieces, M::kPitch, kStages> load(a, at, end, ptx::smem_addr(ring), piece);
 
   const int x0 = lane % M::kLanes, row0 = lane / M::kLanes;  // of V: first piece and row
   const int h_own = HR == 8 ? 2 * q : HR == 4 ? q : 0;       // first head this lane has the scores of
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     const uint32_t seen = load.next(stage);
 
     if (fresh || at.t == 0) {
-      int kv, heads;
-      const int h0 = item_first_head(a, at.item, &kv, &heads);
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
       const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
       // the item before has been through a barrier since it read its queries
       for (int k = threadIdx.x; k < HR * M::kPieces; k += kThreads) {
@@ -218,10 +219,10 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
       const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
-      const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+      const int slot = (2 * (blockIdx.x / a.split) + (first ? 0 : 1)) * a.split + piece;
       first = false;
-      int kv, heads;
-      const int h0 = item_first_head(a, at.item, &kv, &heads);
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
       __syncthreads();  // ml, the exchange buffer and the queries have been read
 #pragma unroll
       for (int u = 0; u < M::kOwn; ++u) {

@@ -295,7 +295,7 @@ typedef struct {
  * Q, O are [S, H, d] with element strides (q_stride_s, q_stride_h) and
  * (o_stride_s, o_stride_h), 16-byte aligned with byte strides multiples of
  * 16; O may not overlap Q.  L is a dense [S, H] float32 array.  H is a
- * multiple of H_kv, S * H <= 2^24, scale > 0.
+ * multiple of H_kv and at most 512 H_kv, S * H <= 2^24, scale > 0.
  * The rows of all sequences are shared out evenly over the GPU, and a
  * sequence that several thread blocks read is joined from their partial
  * results, which pass through `workspace` (16-byte aligned,
