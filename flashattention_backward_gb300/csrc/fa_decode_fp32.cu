@@ -8,12 +8,12 @@
 // units could do while HBM sends it.  So here too the loads are what counts, but
 // the operands' way through shared memory has to stay short:
 //
-//  scores  Lane (g, q) takes keys g and g + 8 and a quarter of their columns, for
-//          all heads of the item: a piece of Q from shared memory serves two
-//          keys, a piece of K all heads.  The quarters are added up by halves:
-//          lanes exchange the heads that the other is to have, so that lane q ends
-//          with the full scores of heads 2q and 2q + 1 (one head with 4 heads an
-//          item) and takes their exponentials alone.
+//  scores  Lane (g, q) takes a slice of the columns of several keys (an eighth of
+//          four keys with 8 heads, a quarter of two with fewer), for all heads: a
+//          piece of Q from shared memory serves all its keys, a piece of K all
+//          heads.  The slices are added up by halves: lanes exchange the heads
+//          that the other is to have, so that lane q ends with the full scores of
+//          a head or two and takes their exponentials alone.
 //  output  A lane holds 4 columns (or a few times 4) of all heads, and a warp's
 //          lanes take whole rows of V; the weights of a row, all heads in one or
 //          two 16-byte pieces of shared memory, are the same for all of them.
@@ -32,10 +32,16 @@ struct Simt {
   static constexpr int kStageBytes = 2 * kRows * kPitch;
   static constexpr int kStages = D == 16 ? 4 : 3;
   static constexpr int kBlocks = blocks_an_sm(false, D);
-  static constexpr int kLanes = D == 96 ? 8 : kPieces < 32 ? kPieces : 32;  // of a row of V
+  // Lanes that share a key's columns, and keys a lane has at a time: with 8
+  // heads eight lanes, so that a piece of Q serves four keys
+  static constexpr int kSlices = HR == 8 && kRows == 16 && kPieces % 8 == 0 ? 8 : 4;
+  static constexpr int kKeys = kRows * kSlices / 32;
+  // Lanes of a row of V: with 8 heads a lane has at least two pieces, so that
+  // the weights of a row serve both
+  static constexpr int kLanes = D == 96 ? 8 : D == 256 ? 32 : HR == 8 && D >= 32 ? kPieces / 2 : kPieces;
   static constexpr int kCols = kPieces / kLanes;   // pieces a lane holds
   static constexpr int kGroups = 32 / kLanes;      // rows of V a warp takes at a time
-  static constexpr int kOwn = HR == 8 ? 2 : 1;     // heads a lane has the scores of
+  static constexpr int kOwn = HR > kSlices ? HR / kSlices : 1;  // heads a lane has the scores of
   static constexpr int kChunk = HR == 1 ? 1 : D == 256 ? 2 : 4;  // heads exchanged at a time
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQ = kRing;                             // [HR][D]
@@ -55,7 +61,8 @@ template <int D, int HR, bool kAlone>
 __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     decode_simt_kernel(const __grid_constant__ DecodeParams a) {
   using M = Simt<D, HR>;
-  constexpr int kTile = M::kTile, kStages = M::kStages, kKeys = M::kRows / 8;
+  constexpr int kTile = M::kTile, kStages = M::kStages, kKeys = M::kKeys, kSlices = M::kSlices;
+  constexpr int kKeyStep = 32 / kSlices;  // keys side by side
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 ml[kWarps][HR];
   __shared__ __align__(16) float factors[kWarps][HR];
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
     some = run_of(a, &at, &end);
     if (!some) return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / kSlices, q = lane % kSlices;
   const int piece = (kAlone ? blockIdx.x / a.cluster : blockIdx.x) % a.split;
   const uint8_t* ring = smem + warp * kStages * M::kStageBytes;
   float* qs = reinterpret_cast<float*>(smem + M::kQ);
@@ -81,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
   Loader<kTile, M::kRows, M::kPieces, M::kPitch, kStages> load(a, at, end, ptx::smem_addr(ring), piece);
 
   const int x0 = lane % M::kLanes, row0 = lane / M::kLanes;  // of V: first piece and row
-  const int h_own = HR == 8 ? 2 * q : HR == 4 ? q : 0;       // first head this lane has the scores of
+  const int h_own = HR == 1 ? 0 : M::kOwn * q;               // first head this lane has the scores of
   float4 acc[HR][M::kCols];   // o, unnormalised, of this lane's rows
   float m[M::kOwn], l[M::kOwn];
   int begin = at.t;
@@ -118,12 +125,13 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
       const uint8_t* ks = ring + stage * M::kStageBytes;
       float s[HR][kKeys] = {};
 #pragma unroll
-      for (int c = 0; c < M::kPieces / 4; ++c) {
-        // pieces two apart: the 8 lanes of an access's quarter (2 keys) take 8 different groups of banks
-        const int piece = M::kPieces == 4 ? q : 8 * (c / 2) + 2 * q + c % 2;
+      for (int c = 0; c < M::kPieces / kSlices; ++c) {
+        // the 8 lanes of an access's quarter take 8 different groups of banks: 8 pieces of a key, or of 2
+        // keys, whose rows are a piece more than a multiple of 8 apart, 4 pieces two apart
+        const int piece = kSlices == 8 ? 8 * c + q : M::kPieces == 4 ? q : 8 * (c / 2) + 2 * q + c % 2;
         float4 k[kKeys];
 #pragma unroll
-        for (int e = 0; e < kKeys; ++e) k[e] = *reinterpret_cast<const float4*>(ks + (g + 8 * e) * M::kPitch + piece * 16);
+        for (int e = 0; e < kKeys; ++e) k[e] = *reinterpret_cast<const float4*>(ks + (g + kKeyStep * e) * M::kPitch + piece * 16);
 #pragma unroll
         for (int h = 0; h < HR; ++h) {
           const float4 x = *reinterpret_cast<const float4*>(qs + h * D + piece * 4);
@@ -131,26 +139,29 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
           for (int e = 0; e < kKeys; ++e) s[h][e] = dot4(x, k[e], s[h][e]);
         }
       }
-      // the quarters added up: lane q keeps heads h_own ... of its keys
+      // the slices added up by halves: lane q keeps heads h_own ... of its keys
       float x[M::kOwn][kKeys];
 #pragma unroll
       for (int e = 0; e < kKeys; ++e) {
         if constexpr (HR == 1) {
           float y = s[0][e];
-          y += __shfl_xor_sync(0xffffffffu, y, 1);
-          x[0][e] = y + __shfl_xor_sync(0xffffffffu, y, 2);
+#pragma unroll
+          for (int o = 1; o < kSlices; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+          x[0][e] = y;
         } else {
-          float half[HR / 2];
+          float part[HR];
 #pragma unroll
-          for (int h = 0; h < HR / 2; ++h) {
-            const float give = q & 2 ? s[h][e] : s[h + HR / 2][e], keep = q & 2 ? s[h + HR / 2][e] : s[h][e];
-            half[h] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-          }
+          for (int h = 0; h < HR; ++h) part[h] = s[h][e];
 #pragma unroll
-          for (int h = 0; h < HR / 4; ++h) {
-            const float give = q & 1 ? half[h] : half[h + HR / 4], keep = q & 1 ? half[h + HR / 4] : half[h];
-            x[h][e] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-          }
+          for (int o = kSlices / 2, n = HR / 2; o > 0; o >>= 1, n >>= 1)
+#pragma unroll
+            for (int h = 0; h < HR / 2; ++h)
+              if (h < n) {
+                const float give = q & o ? part[h] : part[h + n], keep = q & o ? part[h + n] : part[h];
+                part[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              }
+#pragma unroll
+          for (int u = 0; u < M::kOwn; ++u) x[u][e] = part[u];
         }
       }
       bool moved = false;
@@ -159,11 +170,11 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
         float top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < kKeys; ++e) {
-          x[u][e] = (seen >> (g + 8 * e)) & 1 ? x[u][e] * a.scale2 : -INFINITY;
+          x[u][e] = (seen >> (g + kKeyStep * e)) & 1 ? x[u][e] * a.scale2 : -INFINITY;
           top = fmaxf(top, x[u][e]);
         }
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = kSlices; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float now = fmaxf(m[u], top), base = base_of(now), alpha = ptx::ex2(m[u] - base);
         moved |= now != m[u];
         m[u] = now;
@@ -172,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
         for (int e = 0; e < kKeys; ++e) {
           x[u][e] = ptx::ex2(x[u][e] - base);
           l[u] += x[u][e];
-          if (HR > 1 || q == 0) ps[(g + 8 * e) * HR + h_own + u] = x[u][e];
+          if (HR > 1 || q == 0) ps[(g + kKeyStep * e) * HR + h_own + u] = x[u][e];
         }
         if (g == 0 && (HR > 1 || q == 0)) factors[warp][h_own + u] = alpha;
       }
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
 #pragma unroll
       for (int u = 0; u < M::kOwn; ++u) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], o);
+        for (int o = kSlices; o < 32; o <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], o);
         if (g == 0 && (HR > 1 || q == 0)) ml[warp][h_own + u] = make_float2(m[u], l[u]);
       }
       __syncthreads();
