@@ -583,9 +583,12 @@ cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStrea
   JoinShape j = {items <= runs, k.part_heads, 1, 1};
   const int64_t x = j.by_item ? items : runs;
   // few items of many parts: a head and then a slice of its columns a block, so
-  // that more threads read parts; many: several heads a block
+  // that more threads read parts; many of few: several heads a block, as long as
+  // a head's parts are still read in one go
+  constexpr int kMost = kJoinThreads / (D / 4);
   while (x * a.group * j.slices < 304 && j.slices < 4) j.slices *= 2;
-  while (x * ceil_div(a.group, j.together) > 1024 && j.together < a.group && 2 * j.together <= kJoinThreads / (D / 4))
+  while (x * ceil_div(a.group, j.together) > 304 && j.together < a.group && 2 * j.together <= kMost &&
+         kMost / (2 * j.together) * 8 >= runs / x + 2)
     j.together *= 2;
   cfg.gridDim = dim3((unsigned)x, (unsigned)(ceil_div(a.group, j.together) * j.slices));
   cfg.blockDim = dim3(kJoinThreads);
