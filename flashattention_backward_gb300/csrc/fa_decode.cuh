@@ -105,24 +105,46 @@ constexpr double kBigShare = 0.9;
 constexpr int kSmallRuns = 1;
 constexpr int kMinUnits = 64;  // of a resident block, for there to be small runs
 
-struct Share {
-  int64_t big_units, small_units;  // units of all items: in big and in small runs
-  int big, small;                  // runs
-  __device__ __forceinline__ Share(int64_t total, int resident) {
-    big = (int)(total < resident ? total : resident);
-    const bool tail = total >= (int64_t)resident * kMinUnits;
-    big_units = tail ? (int64_t)((double)total * kBigShare) : total;
-    small_units = total - big_units;
-    small = tail ? resident * kSmallRuns : 0;
+// x / n, as one of 32 bits where that does (a division of 64 bits takes several
+// times as long, and stands in front of all loads).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t n) {
+  return (uint64_t)(x | n) >> 32 ? x / n : (int64_t)((uint32_t)x / (uint32_t)n);
+}
+
+// `units` units in `runs` runs as equal as can be: the first `longer` of them
+// have one more than `each`.
+struct Cuts {
+  int64_t units, each;
+  int runs, longer;
+  __device__ __forceinline__ Cuts(int64_t u, int r) : units(u), each(r > 0 ? divide(u, r) : 0), runs(r) {
+    longer = (int)(u - each * r);
   }
-  __device__ __forceinline__ int runs() const { return big + small; }
+  __device__ __forceinline__ int64_t first(int w) const { return each * w + min(w, longer); }
+  // the run that holds unit x
+  __device__ __forceinline__ int run_of(int64_t x) const {
+    const int64_t in_longer = (each + 1) * longer;
+    return x < in_longer ? (int)divide(x, each + 1) : longer + (int)divide(x - in_longer, each);
+  }
+};
+
+struct Share {
+  Cuts big, small;  // units of all items: in big and in small runs
+  static __device__ __forceinline__ bool tail(int64_t total, int resident) {
+    return total >= (int64_t)resident * kMinUnits;
+  }
+  static __device__ __forceinline__ int64_t of_big(int64_t total, int resident) {
+    return tail(total, resident) ? total - (int64_t)((float)total * (float)(1 - kBigShare)) : total;
+  }
+  __device__ __forceinline__ Share(int64_t total, int resident)
+      : big(of_big(total, resident), (int)(total < resident ? total : resident)),
+        small(total - big.units, tail(total, resident) ? resident * kSmallRuns : 0) {}
+  __device__ __forceinline__ int runs() const { return big.runs + small.runs; }
   __device__ __forceinline__ int64_t first(int w) const {
-    return w <= big ? big_units * w / big : big_units + small_units * (w - big) / small;
+    return w <= big.runs ? big.first(w) : big.units + small.first(w - big.runs);
   }
   // the run that holds unit x: the largest w with first(w) <= x
   __device__ __forceinline__ int run_of(int64_t x) const {
-    return x < big_units ? (int)(((x + 1) * big - 1) / big_units)
-                         : big + (int)(((x - big_units + 1) * small - 1) / small_units);
+    return x < big.units ? big.run_of(x) : big.runs + small.run_of(x - big.units);
   }
 };
 
@@ -209,7 +231,7 @@ struct Place {
     s = seq;
     rows = rows_of(a, s);
     tiles = tiles_of<kTile>(rows);
-    item = (int)((x - base) / (kItemCost + tiles));
+    item = (int)divide(x - base, kItemCost + tiles);
     const int64_t begin = base + (int64_t)item * (kItemCost + tiles);
     t = max((int)(x - begin) - kItemCost, 0);
     unit = begin + kItemCost + t;
@@ -446,7 +468,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     } else if ((int)blockIdx.x < share.runs()) {
       const int64_t x = share.first(blockIdx.x + 1) - 1;
       s = units.find(x, 0, &base);
-      item = (int)((x - base) / (kItemCost + tiles_of<kTile>(rows_of(a, s))));
+      item = (int)divide(x - base, kItemCost + tiles_of<kTile>(rows_of(a, s)));
     }
     const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
     run = share.run_of(begin + kItemCost);
