@@ -369,7 +369,7 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
   const fa_status st = fa::check_heads(c, H);
   if (st != FA_OK) return st;
   const int es = fa::elem_size(c->dtype);
-  if (!(scale > 0.f) || !isfinite(scale) || O == Q || !fa::aligned16(Q) || !fa::aligned16(K_pages) || !fa::aligned16(V_pages) ||
+  if (!(scale > 0.f) || !isfinite(scale * fa::kLog2e) || O == Q || !fa::aligned16(Q) || !fa::aligned16(K_pages) || !fa::aligned16(V_pages) ||
       !fa::aligned16(O) || !fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(L) ||
       !fa::good_stride(q_stride_s, c->d, es, false) || !fa::good_stride(q_stride_h, c->d, es, false) ||
       !fa::good_stride(o_stride_s, c->d, es, true) || !fa::good_stride(o_stride_h, c->d, es, true))

@@ -346,3 +346,75 @@ def test_a_generation_together(captured):
     grow([0 if s not in gone else 13 for s in range(S)])
     for _ in range(4):
         token(list(range(S)))
+
+
+def test_refusals():
+    kp, vp = pools(9, 2, 16, 64, torch.bfloat16)
+    table, start = ints([[3, 1], [0, 8]]), ints([0, 0])
+    k = torch.zeros(2, 2, 3, 64, dtype=torch.bfloat16, device=DEV)
+    before = kp.clone()
+    for args in ((k[:1], k[:1], kp, vp, table, start), (k, k[:, :, :2], kp, vp, table, start),
+                 (k.float(), k.float(), kp, vp, table, start), (k, k.transpose(1, 2).contiguous().transpose(1, 2), kp, vp, table, start),
+                 (k[..., :32], k[..., :32], kp, vp, table, start), (k, k, kp, vp, table, start.long()),
+                 (k, k, kp, vp, table, start[:1]), (k, k, kp, vp, table[0], start), (k, k, kp, vp, table, start, start[:1]),
+                 (k.cpu(), k.cpu(), kp, vp, table, start)):
+        with pytest.raises(ValueError):
+            fa.cache_append(*args)
+    fa.cache_append(k[:, :, :0], k[:, :, :0], kp, vp, table, start)  # no rows: nothing to do
+    for moves in (ints([0, 1, 2]), ints([[0, 1]]), ints([[0, 1, 2]]).long(), ints([[0, 1, 2]]).cpu()):
+        with pytest.raises(ValueError):
+            fa.cache_copy_pages(kp, vp, moves)
+    with pytest.raises(ValueError):
+        fa.cache_copy_pages(kp, vp, ints([[0, 1, 2]]), ints([1, 2]))
+    fa.cache_copy_pages(kp, vp, torch.empty(0, 3, dtype=torch.int32, device=DEV))
+    assert torch.equal(kp, before)
+    c = Cache(9, 4, 3, 5)
+    one = ints([1, 0, 0])
+    for call in (lambda: fa.pages_extend(c.table, c.lengths, c.refs, one[:2], 4),
+                 lambda: fa.pages_extend(c.table, c.lengths.long(), c.refs, one, 4),
+                 lambda: fa.pages_extend(c.table.long(), c.lengths, c.refs, one, 4),
+                 lambda: fa.pages_extend(c.table, c.lengths, c.refs.cpu(), one, 4),
+                 lambda: fa.pages_fork(c.table, c.lengths, c.refs, one, one[:2], 4),
+                 lambda: fa.pages_fork(c.table, c.lengths, c.refs, one.long(), one, 4),
+                 lambda: fa.pages_free(c.table, c.lengths, c.refs, one[None], 4),
+                 lambda: fa.pages_compact(c.table, c.lengths, c.refs, 4, out=(c.table[:2], c.refs)),
+                 lambda: fa.pages_compact(c.table, c.lengths, c.refs, 4, out=(c.table, c.refs[:2]))):
+        with pytest.raises(ValueError):
+            call()
+    for rows in (0, -1):
+        with pytest.raises(fa.FaError):
+            fa.pages_extend(c.table, c.lengths, c.refs, one, rows)
+    with pytest.raises(fa.FaError):
+        fa.pages_extend(c.table, c.lengths, c.refs, ints([99, 0, 0]), 4, check_status=True)
+    assert fa.pages_fork(c.table, c.lengths, c.refs, one[:0], one[:0], 4).shape == (0, 3)
+    fa.pages_free(c.table, c.lengths, c.refs, one[:0], 4)
+    c.same()
+    assert fa.get_device_status() == 0
+
+
+def test_calls_on_another_stream():
+    """A stream given by the caller, while the current one is another."""
+    stream = torch.cuda.Stream()
+    c = Cache(40, 4, 4, 6)
+    kp, vp = pools(40, 2, 4, 64, torch.bfloat16)
+    k = torch.randn(4, 2, 9, 64, device=DEV).to(torch.bfloat16)
+    n = ints([9, 3, 0, 0])
+    src, dst = ints([0, 1]), ints([2, 3])
+    torch.cuda.synchronize()
+    start = fa.pages_extend(*c.args(), n, 4, stream=stream)
+    fa.cache_append(k, k, kp, vp, c.table, start, n, stream=stream)
+    moves = fa.pages_fork(*c.args(), src, dst, 4, stream=stream)
+    fa.cache_copy_pages(kp, vp, moves, stream=stream)
+    fa.pages_free(*c.args(), src, 4, stream=stream)
+    again, count = fa.pages_compact(*c.args(), 4, stream=stream)
+    fa.cache_copy_pages(kp, vp, again, count, stream=stream.cuda_stream)
+    stream.synchronize()
+    assert fa.get_device_status(stream) == 0
+    c.m.extend([9, 3, 0, 0])
+    c.m.fork([0, 1], [2, 3])
+    c.m.free([0, 1])
+    c.m.compact()
+    c.same()
+    for s, n in ((2, 9), (3, 3)):
+        for j in range(n):
+            assert torch.equal(kp[c.m.table[s][j // 4], :, j % 4], k[s - 2, :, j])

@@ -313,3 +313,37 @@ def test_agrees_with_the_forward_over_the_same_rows():
     # the forward rounds its weights to bf16 (2^-8 of each, at most 2^-8 of max |v| in the sum) and its output
     assert (o.float() - o2.float()).abs().max() <= 2 * 2.0 ** -8 * v.float().abs().max()
     assert (L.reshape(S, H) - L2.reshape(S, H)).abs().max() <= 1e-3
+
+
+def test_refusals():
+    q, kp, vp, table, lengths = make(3, 8, 2, 64, 16, [100, 7, 64], seed=40, wide=3000)
+    good = dict(q=q, k_pages=kp, v_pages=vp, page_table=table, lengths=lengths)
+    fa.attention_decode(**good)
+    o, L = torch.empty_like(q), torch.empty(3, 8, 1, device=DEV)
+    for bad in (dict(q=q[:2]), dict(q=q[:, :, 0]), dict(q=q.expand(-1, -1, 2, -1)), dict(q=q[..., :32]), dict(q=q.float()),
+                dict(q=q.cpu()), dict(q=q.detach().requires_grad_()), dict(v_pages=vp.float()), dict(v_pages=vp[:-1]),
+                dict(v_pages=vp.transpose(1, 2).contiguous().transpose(1, 2)), dict(k_pages=kp.cpu()),
+                dict(page_table=table.long()), dict(page_table=table.t()), dict(page_table=table.cpu()),
+                dict(lengths=lengths.long()), dict(lengths=lengths[:2]), dict(lengths=lengths.cpu()),
+                dict(out=(o.float(), L)), dict(out=(o, L[:, :, 0])), dict(out=(o, L.half())),
+                dict(workspace=torch.empty(1 << 20, 2, device=DEV)[:, 0])):
+        with pytest.raises(ValueError):
+            fa.attention_decode(**{**good, **bad})
+    small = torch.empty(fa.fa_decode_workspace_bytes(fa.cache_for(kp, vp, table), 8) - 1, dtype=torch.uint8, device=DEV)
+    for bad in (dict(q=q[:, :7]), dict(scale=0.0), dict(scale=float("nan")), dict(workspace=small), dict(out=(q, L))):
+        with pytest.raises(fa.FaError) as err:
+            fa.attention_decode(**{**good, **bad})
+        assert err.value.code == fa.FA_ERR_INVALID_ARG
+    with pytest.raises(fa.FaError) as err:  # more than 512 query heads a key-value head
+        fa.attention_decode(torch.empty(3, 1026, 1, 64, dtype=torch.bfloat16, device=DEV), kp, vp, table, lengths)
+    assert err.value.code == fa.FA_ERR_UNSUPPORTED
+    with torch.no_grad():
+        fa.attention_decode(**{**good, "q": q.detach().requires_grad_()})
+    assert fa.get_device_status() == 0
+
+
+def test_largest_group_of_heads():
+    """512 query heads on one key-value head, in pieces of 16 (8 in fp32)."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for wide in (0, 3000):
+            run_and_check(make(2, 512, 1, 32, 16, [300, 65], dtype, seed=41, wide=wide))

@@ -74,7 +74,7 @@ def test_pools_are_checked(lib, kw, code):
 def test_pointers_and_sizes_are_checked(lib):
     c = ctypes.byref(_cache())
     ok = [c, 4, 0.125, BAD, 256, 64, BAD, BAD, BAD, BAD, 2 * BAD, 256, 64, BAD, BAD, 1 << 40, None]
-    for i, x in [(1, 0), (1, 3), (1, -2), (2, 0.0), (2, float("nan")), (2, float("inf")), (2, -1.0), (3, 0), (3, BAD + 8),
+    for i, x in [(1, 0), (1, 3), (1, -2), (2, 0.0), (2, float("nan")), (2, float("inf")), (2, 3e38), (2, -1.0), (3, 0), (3, BAD + 8),
                  (4, 4), (5, -64), (6, BAD + 2), (7, 0), (8, 0), (8, BAD + 2), (9, 0), (10, BAD + 4), (10, BAD), (11, 60), (12, 0),
                  (13, 0)]:
         args = list(ok)
