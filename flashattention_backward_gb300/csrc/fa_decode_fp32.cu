@@ -17,6 +17,12 @@
 //  output  A lane holds 4 columns (or a few times 4) of all heads, and a warp's
 //          lanes take whole rows of V; the weights of a row, all heads in one or
 //          two 16-byte pieces of shared memory, are the same for all of them.
+//
+// Measured at 32 sequences of 8192 rows, as a share of the 6.8 TB/s of a copy: 95 %
+// with one query head a key head (d 32 to 256), 86 to 92 % with four; with eight,
+// 87 % at d 64, 82 % at d 128, 76 % at d 96, and 56 % at d 256, whose tiles have 8 rows
+// a warp: there the one warp of each scheduler waits for its own FMAs and
+// shared-memory reads.
 
 #include "fa_decode.cuh"
 
