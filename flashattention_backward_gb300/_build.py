@@ -2,7 +2,9 @@
 
 Each CUDA translation unit compiles in its own nvcc process (in parallel),
 then the objects link into one shared library with the CUDA runtime linked
-statically, so the library only needs the driver at run time.
+statically, so the library only needs the driver at run time.  The PyTorch
+binding of the paged-cache calls (csrc/fa_torch.cpp) is a second, small library
+beside it, compiled by the host compiler against the installed PyTorch.
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_simt.cu", "fa_bwd_sm103.cu", "fa_bwd_sm103_count.cu", "fa_bwd_d256_sm103.cu",
            "fa_fwd_sm103.cu", "fa_noalloc.cu", "fa_host.cu", "fa_tma.cu", "fa_decode.cu", "fa_decode_fp32.cu", "fa_cache.cu", "fa_pages.cu"]
+TORCH_SOURCE = "fa_torch.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3",
@@ -30,6 +34,37 @@ NVCC_FLAGS = ARCH + [
     "-Xptxas",
     "-warn-spills",
 ]
+
+
+def torch_binding_path() -> str:
+    """The binding for this Python and PyTorch: its name says which, so that
+    another version does not load it."""
+    import torch
+
+    return os.path.join(OUT_DIR, f"_fa_torch_{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def build_torch_binding() -> tuple[str, str]:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    out = torch_binding_path()
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-O2", "-std=c++17", os.path.join(CSRC, TORCH_SOURCE),
+           "-o", tmp, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{os.path.join(root, 'include')}", f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}",
+            f"-I{sysconfig.get_paths()['include']}", f"-I{cuda_include()}"]
+    lib = os.path.join(root, "lib")
+    cmd += [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {TORCH_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out, r.stderr
+
+
+def cuda_include() -> str:
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
 
 
 def nvcc_path() -> str:
@@ -49,14 +84,14 @@ def _stale(lib: str, deps: list[str]) -> bool:
 def _deps() -> list[str]:
     out = [os.path.join(PKG, "..", "include", "fa.h")]
     for f in os.listdir(CSRC):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.endswith((".cu", ".cuh", ".h", ".cpp")):
             out.append(os.path.join(CSRC, f))
     return out
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile (if stale) and return the path of libfa.so."""
-    if not force and not _stale(LIB, _deps()):
+    if not force and not _stale(LIB, _deps()) and not _stale(torch_binding_path(), _deps()):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = nvcc_path()
@@ -70,8 +105,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_torch_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose:
         for _, log in results:
             if log.strip():

@@ -347,3 +347,30 @@ def test_largest_group_of_heads():
     for dtype in (torch.bfloat16, torch.float32):
         for wide in (0, 3000):
             run_and_check(make(2, 512, 1, 32, 16, [300, 65], dtype, seed=41, wide=wide))
+
+
+def test_strides_of_dimensions_of_one():
+    """PyTorch leaves the stride of a dimension of one element open; the descriptor holds a packed one."""
+    def strides(shape, st, table=None):
+        t = torch.zeros(1 << 16, dtype=torch.bfloat16, device=DEV).as_strided(shape, st)
+        c = fa.cache_for(t, t, table)
+        return c.stride_page, c.stride_h, c.stride_n, c.table_stride
+
+    assert strides((1, 1, 1, 64), (3, 5, 7, 1))[:3] == (64, 64, 64)
+    assert strides((2, 1, 16, 64), (1024, 1, 64, 1))[:3] == (1024, 1024, 64)
+    assert strides((5, 3, 16, 64), (16 * 3 * 64, 64, 3 * 64, 1))[:3] == (16 * 3 * 64, 64, 3 * 64)
+    table = torch.zeros(3, 5, dtype=torch.int32, device=DEV)
+    c = fa.cache_for(*[torch.zeros(2, 1, 16, 64, device=DEV)] * 2, table[:, :4])
+    assert (c.S, c.max_pages, c.table_stride, c.dtype) == (3, 4, 5, fa.FA_FP32)
+    c = fa.cache_for(*[torch.zeros(2, 1, 16, 64, device=DEV)] * 2, table[:1, :4])
+    assert (c.S, c.max_pages, c.table_stride) == (1, 4, 4)
+    with pytest.raises(ValueError):
+        strides((2, 2, 4, 64), (1024, 512, 128, 2))
+
+
+def test_grouped_single_page_strides():
+    """Single sequences, heads, pages and rows, in storages that leave their strides open."""
+    for shape in ((1, 1, 1), (1, 4, 1), (1, 4, 4), (3, 4, 1)):
+        S, H, Hk = shape
+        for page, n in ((1, 1), (16, 16), (64, 5)):
+            run_and_check(make(S, H, Hk, 64, page, [n] * S, seed=50, spare=0, rows_first=True))

@@ -134,39 +134,34 @@ def test_division_by_multiplication():
 
 def test_binding_refuses(lib):
     pools = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):  # CPU tensors: no CPU path exists
+    with pytest.raises(ValueError, match="CUDA"):  # CPU tensors: no CPU path exists
         fa.cache_for(pools, pools)
-    with pytest.raises(TypeError):
-        fa.cache_for(pools.half(), pools.half())
-    with pytest.raises(ValueError):
-        fa.cache_for(pools, pools.float())
-    with pytest.raises(ValueError):
-        fa.cache_for(pools, pools[:3])
-    with pytest.raises(ValueError):
-        fa.cache_for(pools[0], pools[0])
-    with pytest.raises(ValueError):
-        paged._row_strides(pools[..., ::2])
+    for bad in ((pools.half(), pools.half()), (pools, None), ("pools", pools)):
+        with pytest.raises(TypeError):
+            fa.cache_for(*bad)
+    for bad in ((pools, pools.float()), (pools, pools[:3]), (pools[0], pools[0])):
+        with pytest.raises(ValueError):
+            fa.cache_for(*bad)
     table = torch.zeros(3, 5, dtype=torch.int32)
-    assert paged._table(table[:, :4], table.device)[:3] == (3, 4, 5)
-    assert paged._table(table[:1, :4], table.device)[:3] == (1, 4, 4)
-    for bad in (table.long(), table[0], table[:, ::2]):
+    refs = torch.zeros(9, dtype=torch.int32)
+    for call in (lambda: fa.attention_decode(torch.zeros(3, 2, 1, 64), pools, pools, table, table[:, 0]),
+                 lambda: fa.cache_append(pools, pools, pools, pools, table, refs),
+                 lambda: fa.cache_copy_pages(pools, pools, table[:, :3]),
+                 lambda: fa.pages_extend(table, table[:, 0], refs, table[:, 0], 16),
+                 lambda: fa.pages_fork(table, table[:, 0], refs, refs, refs, 16),
+                 lambda: fa.pages_free(table, table[:, 0], refs, refs, 16),
+                 lambda: fa.pages_compact(table, table[:, 0], refs, 16)):
         with pytest.raises(ValueError):
-            paged._table(bad, table.device)
-    for bad in (table[0].long(), table[0][:4], table[0][::2]):
-        with pytest.raises(ValueError):
-            paged._ints("lengths", bad, (5,), table.device)
-    with pytest.raises(ValueError):
-        fa.pages_extend(table, table[:, 0], torch.zeros(9, dtype=torch.int32), table[:, 0], 16)
+            call()
+    with pytest.raises(TypeError):
+        fa.pages_extend(table, table[:, 0], None, table[:, 0], 16)
 
 
-def test_strides_of_dimensions_of_one():
-    t = torch.zeros(1, 1, 1, 64)
-    assert paged._row_strides(t.as_strided((1, 1, 1, 64), (3, 5, 7, 1))) == (64, 64, 64)
-    assert paged._row_strides(torch.zeros(2, 1, 16, 64).as_strided((2, 1, 16, 64), (1024, 1, 64, 1))) == (1024, 1024, 64)
-    s = paged._row_strides(torch.zeros(5, 16, 3, 64).permute(0, 2, 1, 3))
-    assert s == (16 * 3 * 64, 64, 3 * 64)
-    q = torch.zeros(5, 12, 64)[:, 2:10, None, :]
-    assert paged._row_strides(q)[:2] == (768, 64)
+def test_missing_binding_fails_loudly(lib, monkeypatch):
+    monkeypatch.setattr(paged, "_EXT", None)
+    monkeypatch.setattr(_build, "torch_binding_path", lambda: "/nonexistent/_fa_torch.so")
+    with pytest.raises(RuntimeError, match="build"):
+        fa.pages_free(*[torch.zeros(1, dtype=torch.int32)] * 4, 16)
 
 
 def test_oracle_is_a_softmax():
