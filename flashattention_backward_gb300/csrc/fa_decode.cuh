@@ -559,19 +559,24 @@ struct Cut {
 // Rows of a tile.
 inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 256 ? 32 : 64; }
 
-// Each item gets a cluster of as many blocks (1, 2, 4, 8 or 16) as fit the GPU
+// Each item gets a cluster of as many blocks (1, 2, 4, 8 or 16) as the GPU holds
 // at a time, if that leaves at most kClusterTiles tiles a block.  Beyond that
 // the runs are quicker, which use all SMs: a block alone on its SM takes 1.1 us a
-// tile.  GPU time of 4 sequences of up to 4000 rows, 16 heads on one of d 128:
-// 12.6 us with 8 blocks of 8 tiles, 9.5 with 16 of 4, 8.6 in runs; but the runs'
-// second launch and workspace cost the caller's thread 7 us.
-constexpr int kClusterTiles = 4;
-constexpr int kClusterSms = 148;
+// tile.  4 sequences of up to 4000 rows, 16 heads on one of d 128, took 8.3 us in
+// runs, 9.1 with 16 blocks of 4 tiles and 12.6 with 8 of 8; 8 of 512, 32 heads on 8,
+// 10.2 in runs and 7.7 with 4 blocks of 2 tiles.
+constexpr int kClusterTiles = 2;
 inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
-  const int64_t room = (int64_t)kClusterSms * blocks_an_sm(c.dtype == FA_BF16, c.d);
-  int n = kMostBlocks;
-  while (n > 1 && (items * n > room || n / 2 >= most_tiles)) n /= 2;
-  return items * n <= room && most_tiles <= n * kClusterTiles ? n : 0;
+  // clusters that the GPU holds of each size, for each block an SM: a cluster stays inside a GPC
+  struct {
+    int blocks, fit;
+  } sizes[] = {{kMostBlocks, 7}, {8, 15}, {4, 36}, {2, 76}, {1, 152}};
+  const int an_sm = blocks_an_sm(c.dtype == FA_BF16, c.d);
+  for (const auto& z : sizes) {
+    if (items > (int64_t)z.fit * an_sm || z.blocks / 2 >= most_tiles) continue;  // too many, or blocks without a tile
+    return most_tiles <= (int64_t)z.blocks * kClusterTiles ? z.blocks : 0;
+  }
+  return 0;
 }
 
 inline Cut cut_of(const fa_cache& c, int H) {

@@ -168,7 +168,7 @@ def test_all_empty(wide, dtype):
     run_and_check(make(3, 4, 2, 64, 16, [0, 0, 0], dtype, wide=wide))
 
 
-@pytest.mark.parametrize("S,n", [(1, 4000), (9, 1000), (18, 500), (36, 250), (74, 250), (148, 250), (300, 250), (700, 60)])
+@pytest.mark.parametrize("S,n", [(1, 1900), (7, 1000), (18, 500), (36, 250), (74, 180), (148, 100), (300, 60), (700, 60)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_clusters_of_every_size(S, n, dtype):
     """As many blocks an item as the GPU holds at a time: 16, 8, 4, 2, 1, or more
