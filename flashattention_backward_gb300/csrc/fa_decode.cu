@@ -34,14 +34,12 @@ namespace {
 //                those that make a lane's share of B a run of 16 bytes of a key,
 //                two steps' worth, and the same columns of Q are A's.
 //  O^T += V^T P^T  A = 16 columns x 16 keys, B = 16 keys x 8 heads: S's
-//                accumulators are P^T's operand as they stand.  A's pairs of
-//                keys come from two rows: lane (g, q) reads columns 64 c + 8 g
-//                ... + 7 of keys 2q, 2q + 1, 2q + 8, 2q + 9, and byte permutes pair
-//                them.  Column 64 c + 8 g + 2 i + r is row g + 8 r of product i.
+//                accumulators are P^T's operand as they stand, and ldmatrix turns
+//                V round.
 //
 // A warp copies its own 16 rows (cp.async into a ring of its own) and waits for
-// them alone: no block barrier in the loop, no transposition, conflict-free
-// 16-byte shared-memory reads.  tcgen05 would want 64 or 128 rows of A where
+// them alone: no block barrier in the loop, conflict-free 16-byte
+// shared-memory reads.  tcgen05 would want 64 or 128 rows of A where
 // there are 1 to 16 query heads, and a barrier a tile, for a product that is
 // not the limit.
 //
@@ -52,11 +50,11 @@ template <int D>
 struct Mma {
   static constexpr int kRows = 16;             // of a tile, a warp
   static constexpr int kTile = kWarps * kRows;
-  static constexpr int kVW = D % 64 ? 32 : 64; // columns of V in a block: 8 or 16 bytes a lane
+  static constexpr int kVW = D % 64 ? 32 : 64; // columns of O that are exchanged at a time
   static constexpr int kPieces = D / 8;        // of 16 bytes in a row
   // 16 bytes between rows: the 8 lanes of an access's quarter then take 8
-  // different groups of 4 banks, of K (2 keys x 4 pieces, 2 apart) as of V (4 pairs
-  // of keys, 2 pieces)
+  // different groups of 4 banks, of K (2 keys x 4 pieces, 2 apart) as of V (8 keys,
+  // one piece)
   static constexpr int kPitch = D * 2 + 16;
   static constexpr int kStageBytes = 2 * kRows * kPitch;  // K and V rows of a warp
   // Bytes in flight an SM: (stages - 1) of blocks x warps x 64 d.
@@ -77,10 +75,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(at));
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -213,26 +211,16 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             }
         }
       }
-      constexpr int kLaneV = VW / 4, kWords = VW / 16;
-      const uint32_t v_at = ring + stage * M::kStageBytes + M::kStageBytes / 2 + 2 * q * M::kPitch + g * kLaneV;
+      // V^T's operand: four 8 x 8 pieces of V (keys 0 - 7 and 8 - 15, columns 0 - 7
+      // and 8 - 15 of a step), turned round on their way; lane 8 n + r names row r of piece n
+      const uint32_t v_at = ring + stage * M::kStageBytes + M::kStageBytes / 2 +
+                            ((lane & 7) + (lane >> 4) * 8) * M::kPitch + ((lane >> 3) & 1) * 16;
 #pragma unroll
       for (int c = 0; c < D / VW; ++c) {
-        uint32_t w[4][kWords];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t from = v_at + ((r & 1) + (r >> 1) * 8) * M::kPitch + c * VW * 2;
-          if constexpr (VW == 64) {
-            const uint4 x = lds16(from);
-            w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
-          } else {
-            const uint2 x = lds8(from);
-            w[r][0] = x.x, w[r][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kWords; ++e) {
-          const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5410), a1 = __byte_perm(w[0][e], w[1][e], 0x7632);
-          const uint32_t a2 = __byte_perm(w[2][e], w[3][e], 0x5410), a3 = __byte_perm(w[2][e], w[3][e], 0x7632);
+        for (int e = 0; e < VW / 16; ++e) {
+          uint32_t a0, a1, a2, a3;
+          ldmatrix_trans(v_at + (c * VW + e * 16) * 2, a0, a1, a2, a3);
 #pragma unroll
           for (int u = 0; u < NH; ++u) {
             mma16816(acc[u][c][e], a0, a1, a2, a3, hi[u][0], hi[u][1]);
@@ -274,14 +262,14 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
 #pragma unroll
         for (int c = 0; c < D / VW; ++c) {
           if (u + c > 0) __syncthreads();
-          float* mine_at = exchange + ((warp * 8 + 2 * q) * M::kPad + g * (VW / 8));
+          float* mine_at = exchange + (warp * 8 + 2 * q) * M::kPad + g;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int x = 0; x < VW / 16; x += 2)
-              *reinterpret_cast<float4*>(mine_at + e * M::kPad + 2 * x) =
-                  make_float4(acc[u][c][x][e] * f[e], acc[u][c][x][2 + e] * f[e], acc[u][c][x + 1][e] * f[e],
-                              acc[u][c][x + 1][2 + e] * f[e]);
+            for (int x = 0; x < VW / 16; ++x) {
+              mine_at[e * M::kPad + 16 * x] = acc[u][c][x][e] * f[e];
+              mine_at[e * M::kPad + 16 * x + 8] = acc[u][c][x][2 + e] * f[e];
+            }
           __syncthreads();
           // a thread adds up four columns of a head
 #pragma unroll
