@@ -54,6 +54,7 @@ struct AppendParams {
 };
 
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams a) {
+  after_stream();
   int64_t from[kUnroll], to[kUnroll];
   bool on[kUnroll];
 #pragma unroll
@@ -117,6 +118,7 @@ struct CopyParams {
 // do not overlap another's, so loads and stores of one iteration need no
 // order; K and V pools are different buffers.
 __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams a) {
+  after_stream();
   int n = a.max_moves;
   if (a.count) {
     const int given = __ldg(a.count);
@@ -207,8 +209,7 @@ fa_status fa_cache_append(const fa_cache* c, int32_t rows, const void* K, const 
   a.ph = c->stride_h * es;
   a.pn = c->stride_n * es;
   const unsigned blocks = (unsigned)fa::ceil_div(total, a.block_rows);
-  fa::cache_append_kernel<<<blocks, fa::kThreads, 0, (cudaStream_t)stream>>>(a);
-  return fa::status_of(cudaGetLastError());
+  return fa::status_of(fa::launch_early(fa::cache_append_kernel, dim3(blocks), fa::kThreads, 0, (cudaStream_t)stream, 1, a));
 }
 
 fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_t* moves, const int32_t* count,
@@ -243,8 +244,8 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
   a.pn = c->stride_n * es;
   const int64_t work = (int64_t)max_moves * a.chunks;
   const int64_t resident = (int64_t)sms * 8;
-  fa::cache_copy_kernel<<<(unsigned)(work < resident ? work : resident), fa::kThreads, 0, (cudaStream_t)stream>>>(a);
-  return fa::status_of(cudaGetLastError());
+  const dim3 grid((unsigned)(work < resident ? work : resident));
+  return fa::status_of(fa::launch_early(fa::cache_copy_kernel, grid, fa::kThreads, 0, (cudaStream_t)stream, 1, a));
 }
 
 }  // extern "C"

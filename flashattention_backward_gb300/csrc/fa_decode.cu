@@ -102,11 +102,12 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
   Place<kTile> at;
   int64_t end;
   bool some;
+  after_stream();
   if constexpr (kAlone) {
     some = share_of_item(a, &at, &end);
     if (!some && threadIdx.x < kHeads) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
   } else {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may line up
+    next_may_start();  // the join
     some = run_of(a, &at, &end);
     if (!some) return;
   }

@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   // What comes after this kernel on its stream waits for this kernel alone, so
   // it may not end before the one in front, even if it has nothing to join:
   // block (0, 0) waits in any case.
-  if (following > 0 || (blockIdx.x == 0 && blockIdx.y == 0)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (following > 0 || (blockIdx.x == 0 && blockIdx.y == 0)) after_stream();
   if (following == 0) return;
   if (grp < take) {
     const int h = min(head0 + grp % j.together, a.group - 1), piece = h / a.piece_heads;
@@ -605,7 +605,6 @@ inline int runs_of(const Cut& k, int resident, DecodeParams* a) {
 
 template <class T, int D, int kTile>
 cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
   const int64_t items = (int64_t)a.S * a.items;
   JoinShape j = {items <= runs, k.part_heads, 1, 1};
   const int64_t x = j.by_item ? items : runs;
@@ -617,16 +616,8 @@ cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStrea
   while (x * ceil_div(a.group, j.together) > 304 && j.together < a.group && 2 * j.together <= kMost &&
          kMost / (2 * j.together) * 8 >= runs / x + 2)
     j.together *= 2;
-  cfg.gridDim = dim3((unsigned)x, (unsigned)(ceil_div(a.group, j.together) * j.slices));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  // its blocks may be there before the kernel in front ends, and wait for that themselves
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, kTile>, a, j);
+  const dim3 grid((unsigned)x, (unsigned)(ceil_div(a.group, j.together) * j.slices));
+  return launch_early(decode_join_kernel<T, D, kTile>, grid, kJoinThreads, 0, s, 1, a, j);
 }
 
 // How many blocks of a kernel the device holds at a time; raises the kernel's
@@ -657,23 +648,9 @@ cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodePar
   cudaError_t e = resident_blocks(k.cluster > 0 ? (const void*)alone : (const void*)kernel, smem,
                                   k.cluster > 0 ? known_alone : known, &resident);
   if (e != cudaSuccess) return e;
-  if (k.cluster > 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.S * a.items * a.split * k.cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = a.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, alone, a);
-  }
+  if (k.cluster > 0) return launch_early(alone, dim3((unsigned)(a.S * a.items * a.split * k.cluster)), kThreads, smem, s, k.cluster, a);
   const int runs = runs_of(k, resident, &a);
-  kernel<<<runs * a.split, kThreads, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(kernel, dim3((unsigned)(runs * a.split)), kThreads, smem, s, 1, a);
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
   return launch_join<T, D, kTile>(k, a, runs, s);
 }

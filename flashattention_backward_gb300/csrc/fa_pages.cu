@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g
   // [S]: pages wanted by the sequences before; many of them are kept in `start`,
   // whose values are only known at the end
   int* first_of = g.S <= kThreads ? first_of_few : start;
+  after_stream();
   if (threadIdx.x == 0) wanted = 0;
   __syncthreads();
   bool bad = false;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_extend_kernel(const Pages g
 // whether it is a destination.
 constexpr int kForkBlocks = 8;
 
-__global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     pages_fork_kernel(const Pages g, int pairs, const int32_t* src, const int32_t* dst, int32_t* table,
                       int32_t* lengths, int32_t* refs, int32_t* moves) {
   namespace cg = cooperative_groups;
@@ -193,6 +194,7 @@ __global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kThreads, 
   const cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31;
   const int first = blockIdx.x * kWarps + (threadIdx.x >> 5), step = kForkBlocks * kWarps;  // this warp's pairs
+  after_stream();
   for (int w = threadIdx.x; w < (g.S + 15) / 16; w += kThreads) marks[w] = 0;
   if (threadIdx.x == 0) any_bad = 0;
   cluster.sync();
@@ -283,6 +285,7 @@ __global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kThreads, 
 __global__ void __launch_bounds__(128) pages_free_kernel(const Pages g, const int32_t* list, int32_t* table,
                                                          int32_t* lengths, int32_t* refs) {
   __shared__ int rows;
+  after_stream();
   const int s = list[blockIdx.x];
   if (s < 0 || s >= g.S) {
     if (s != -1 && threadIdx.x == 0) report_pages(g.status);
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages 
                                                                     int32_t* refs_out, int32_t* moves,
                                                                     int32_t* n_moves) {
   __shared__ int sums[kWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_stream();
+  next_may_start();  // pages_rename_kernel
   const auto used = [&](int p) { return refs[p] > 0; };
   int mine = 0, n;
   for (int p = threadIdx.x; p < g.num_pages; p += kThreads) mine += used(p);
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const 
   const int held = g.pages(min(max(n, 0), g.rows));
   // the kernel in front writes no table: entries may be read ahead of it
   int ahead = threadIdx.x < held ? table[row + threadIdx.x] : -1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_stream();
   const int count = *n_moves;
   for (int c = threadIdx.x; c < g.max_pages; c += blockDim.x) {
     int p = -1;
@@ -410,8 +414,8 @@ fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengt
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
-  fa::pages_extend_kernel<<<1, fa::kThreads, 0, (cudaStream_t)stream>>>(g, page_table, lengths, refs, n_new, start);
-  return fa::status_of(cudaGetLastError());
+  return fa::status_of(fa::launch_early(fa::pages_extend_kernel, dim3(1), fa::kThreads, 0, (cudaStream_t)stream, 1, g,
+                                        page_table, lengths, refs, n_new, start));
 }
 
 fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, const int32_t* dst, int32_t* page_table,
@@ -425,9 +429,9 @@ fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, co
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
-  fa::pages_fork_kernel<<<fa::kForkBlocks, fa::kThreads, (c->S + 15) / 16 * 4, (cudaStream_t)stream>>>(
-      g, pairs, src, dst, page_table, lengths, refs, moves);
-  return fa::status_of(cudaGetLastError());
+  return fa::status_of(fa::launch_early(fa::pages_fork_kernel, dim3(fa::kForkBlocks), fa::kThreads,
+                                        (c->S + 15) / 16 * 4, (cudaStream_t)stream, fa::kForkBlocks, g, pairs, src, dst,
+                                        page_table, lengths, refs, moves));
 }
 
 fa_status fa_pages_free(const fa_cache* c, int32_t count, const int32_t* sequences, int32_t* page_table,
@@ -441,8 +445,8 @@ fa_status fa_pages_free(const fa_cache* c, int32_t count, const int32_t* sequenc
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
   if (count == 0) return FA_OK;
-  fa::pages_free_kernel<<<count, 128, 0, (cudaStream_t)stream>>>(g, sequences, page_table, lengths, refs);
-  return fa::status_of(cudaGetLastError());
+  return fa::status_of(fa::launch_early(fa::pages_free_kernel, dim3((unsigned)count), 128, 0, (cudaStream_t)stream, 1, g,
+                                        sequences, page_table, lengths, refs));
 }
 
 fa_status fa_pages_compact(const fa_cache* c, const int32_t* page_table, const int32_t* lengths, const int32_t* refs,
@@ -456,22 +460,11 @@ fa_status fa_pages_compact(const fa_cache* c, const int32_t* page_table, const i
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;
   const cudaStream_t s = (cudaStream_t)stream;
-  fa::pages_compact_kernel<<<1, fa::kThreads, 0, s>>>(g, refs, refs_out, moves, n_moves);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      fa::launch_early(fa::pages_compact_kernel, dim3(1), fa::kThreads, 0, s, 1, g, refs, refs_out, moves, n_moves);
   if (e != cudaSuccess) return FA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)c->S);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  // its blocks may be there before the kernel in front ends, and wait for that themselves
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa::pages_rename_kernel, g, page_table, lengths, (const int32_t*)refs_out,
-                         (const int32_t*)moves, (const int32_t*)n_moves, table_out);
-  return fa::status_of(e);
+  return fa::status_of(fa::launch_early(fa::pages_rename_kernel, dim3((unsigned)c->S), 128, 0, s, 1, g, page_table,
+                                        lengths, refs_out, moves, n_moves, table_out));
 }
 
 }  // extern "C"

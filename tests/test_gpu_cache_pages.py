@@ -418,3 +418,61 @@ def test_calls_on_another_stream():
     for s, n in ((2, 9), (3, 3)):
         for j in range(n):
             assert torch.equal(kp[c.m.table[s][j // 4], :, j % 4], k[s - 2, :, j])
+
+
+def test_a_step_captured_between_other_work():
+    """Copies, kernels of PyTorch's own and another stream's work in front of, between and behind the calls of a captured
+    step: the calls' blocks may line up early, but must not look at anything before it is there."""
+    S, H, Hk, d, page = 4, 8, 2, 64, 16
+    c = Cache(64, page, S, 12)
+    kp, vp = pools(64, Hk, page, d, torch.bfloat16)
+    src = [torch.randn(S, n, 1, d, device=DEV).to(torch.bfloat16) for n in (Hk, Hk, H)]
+    k, v, q = (torch.zeros_like(t) for t in src)
+    plan, one = ints([1, 1, 0, 1]), ints([0] * S)
+    big = torch.zeros(1 << 24, device=DEV)
+    host = torch.zeros(S, dtype=torch.int32).pin_memory()
+    c.extend([30, 15, 0, 1])
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.add_(1)                # something slow, and then what the step reads
+            one.copy_(plan)
+            k.copy_(src[0])
+            v.copy_(src[1])
+        torch.cuda.current_stream().wait_stream(side)
+        q.copy_(src[2])
+        start = fa.pages_extend(*c.args(), one, page)
+        big.mul_(2)
+        fa.cache_append(k, v, kp, vp, c.table, start, one)
+        got = fa.attention_decode(q, kp, vp, c.table, c.lengths)
+        out = got[0] * 2
+        host.copy_(start, non_blocking=True)
+        return got[0], got[1], out
+
+    with torch.cuda.stream(main):
+        step()
+        torch.cuda.synchronize()
+        c.m.extend([1, 1, 0, 1])
+        with torch.cuda.graph(graph, stream=main):
+            got = step()
+    torch.cuda.synchronize()
+    for i in range(20):
+        for t in src:
+            t.normal_()
+        plan.copy_(ints([1, i % 2, i // 3 % 2, 1]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.get_device_status() == 0
+        want = c.m.extend([1, i % 2, i // 3 % 2, 1])
+        c.same()
+        assert host.tolist() == want
+        check(got[:2], src[2], kp, vp, c.table, c.lengths, d ** -0.5)
+        assert torch.equal(got[2], got[0] * 2)
+        for s in range(S):
+            n = c.m.lengths[s] - 1
+            if want[s] == n:
+                assert torch.equal(kp[c.m.table[s][n // page], :, n % page], src[0][s, :, 0])
