@@ -16,7 +16,7 @@
 // How the work is shared out and joined is in fa_decode.cuh.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 64 sequences of up
-// to 8192 rows, 32 heads on 8 of d 128, 987 MB: 152 us, 96 %.  4 of 8192, 16 heads
+// to 8192 rows, 32 heads on 8 of d 128, 987 MB: 152 to 155 us, 94 to 96 %.  4 of 8192, 16 heads
 // of d 256, 537 MB: 91 us, 87 %.  32 of up to 2048, 32 heads of d 64, 235 MB: 44 us,
 // 78 %; one of 32768, 8 heads of d 128, 134 MB: 28 us, 71 %: the start of a call,
 // the last tiles and the join take about 8 us beside the loads.
