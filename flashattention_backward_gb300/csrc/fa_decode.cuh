@@ -392,8 +392,10 @@ __device__ __forceinline__ bool share_of_item(const DecodeParams& a, Place<kTile
 }
 
 // Joins the parts of a cluster's blocks: o [heads][D] and ml [heads] in the
-// shared memory of each, m = -inf where a block saw nothing (its o is not
-// read).  Every thread of the cluster calls it.
+// shared memory of each, l = kNoPart of a block without tiles, whose o is not
+// read.  m alone does not tell: it is -inf too where all scores are NaN, and
+// that has to come out.  Every thread of the cluster calls it.
+constexpr float kNoPart = -1.f;
 template <class T, int D>
 __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4* o_part, const float2* ml_part) {
   constexpr int kLanes = D / 4, kMost = kMostBlocks;
@@ -409,16 +411,17 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4
     float m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < kMost; ++r) {
-      ml[r] = r < a.cluster ? cluster.map_shared_rank(ml_part, r)[head] : make_float2(-INFINITY, 0.f);
+      ml[r] = r < a.cluster ? cluster.map_shared_rank(ml_part, r)[head] : make_float2(-INFINITY, kNoPart);
       m = fmaxf(m, ml[r].x);
     }
+    const float base = base_of(m);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll
     for (int r = 0; r < kMost; ++r) {
-      if (ml[r].x == -INFINITY) continue;
+      if (ml[r].y == kNoPart) continue;
       const float4 v = cluster.map_shared_rank(o_part, r)[k];
-      const float w = ptx::ex2(ml[r].x - m);
+      const float w = ptx::ex2(ml[r].x - base);
       o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
       l = fmaf(w, ml[r].y, l);
     }

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
   after_stream();
   if constexpr (kAlone) {
     some = share_of_item(a, &at, &end);
-    if (!some && threadIdx.x < HR) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    if (!some && threadIdx.x < HR) part_ml[threadIdx.x] = make_float2(-INFINITY, kNoPart);
   } else {
     next_may_start();  // the join
     some = run_of(a, &at, &end);

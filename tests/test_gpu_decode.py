@@ -192,6 +192,26 @@ def test_rising_scores():
     run_and_check((q, kp, vp, table, lengths))
 
 
+@pytest.mark.parametrize("wide", [0, 3000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_reaches_its_heads_alone(wide, dtype):
+    """A NaN in a query makes every score of its head NaN, one in a key a score of
+    each head that reads it, however the rows are shared out; the other heads
+    and an empty sequence with a NaN query know nothing of it."""
+    args = make(3, 4, 2, 64, 16, [200, 0, 130], dtype, seed=31, wide=wide)
+    clean = fa.attention_decode(*args)
+    q, kp, vp, table, lengths = args
+    q[0, 1, 0, 5] = float("nan")
+    q[1, 2, 0, 0] = float("nan")
+    kp[table[2, 100 // 16].item(), 1, 100 % 16, 63] = float("nan")  # key head 1: query heads 2, 3
+    o, L = fa.attention_decode(*args)
+    assert fa.get_device_status() == 0
+    hit = torch.zeros(3, 4, dtype=torch.bool, device=DEV)
+    hit[0, 1] = hit[2, 2] = hit[2, 3] = True
+    assert o[hit].isnan().all() and L[hit].isnan().all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(L[~hit], clean[1][~hit])
+
+
 @pytest.mark.parametrize("scale", [1e-3, 1.0])
 def test_scale(scale):
     run_and_check(make(3, 4, 2, 64, 16, [100, 7, 64], seed=8), scale)
