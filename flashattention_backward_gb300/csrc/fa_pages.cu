@@ -341,8 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const Pages 
 }
 
 // Table entries after a compaction: one block a sequence.  The moves are in
-// rising order of their sources, which lie behind all pages that stay.  An
-// entry that names no page in use is damaged and becomes -1.
+// rising order of their sources and of their destinations, and the sources lie
+// behind all pages that stay.  An entry that names no page in use is damaged and
+// becomes -1: also one that names a destination, which was free and is in use now.
 __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const int32_t* table,
                                                            const int32_t* lengths, const int32_t* refs_out,
                                                            const int32_t* moves, const int32_t* n_moves,
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const 
   // the kernel in front writes no table: entries may be read ahead of it
   int ahead = threadIdx.x < held ? table[row + threadIdx.x] : -1;
   after_stream();
-  const int count = *n_moves;
+  const int count = *n_moves, source0 = count > 0 ? moves[0] : g.num_pages;
   for (int c = threadIdx.x; c < g.max_pages; c += blockDim.x) {
     int p = -1;
     if (c < held) {
@@ -362,7 +363,9 @@ __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const 
       if (p < 0 || p >= g.num_pages) {
         p = -1;
       } else {
-        // the first move whose source is at or behind p, eight ways at a time
+        // the first move whose source (or destination, of a page before all
+        // sources) is at or behind p, eight ways at a time
+        const int32_t* key = moves + (p < source0);
         int lo = 0, hi = count;
         while (lo < hi) {
           const int step = (hi - lo + 7) / 8;
@@ -370,13 +373,13 @@ __global__ void __launch_bounds__(128) pages_rename_kernel(const Pages g, const 
 #pragma unroll
           for (int k = 1; k < 8; ++k) {
             const int at = lo + k * step - 1;
-            if (at < hi && moves[3 * (int64_t)at] < p) below = k;
+            if (at < hi && key[3 * (int64_t)at] < p) below = k;
           }
           if (below < 7) hi = min(hi, lo + (below + 1) * step - 1);
           lo += below * step;
         }
-        if (lo < count && moves[3 * (int64_t)lo] == p)
-          p = moves[3 * (int64_t)lo + 1];
+        if (lo < count && key[3 * (int64_t)lo] == p)
+          p = p < source0 ? -1 : moves[3 * (int64_t)lo + 1];
         else if (refs_out[p] <= 0)
           p = -1;
       }

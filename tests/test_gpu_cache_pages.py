@@ -151,6 +151,21 @@ def test_damaged_tables_are_not_followed():
     assert fa.get_device_status() == 0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_drops_entries_of_free_pages(in_place):
+    """A damaged entry that names a free page, which the compaction gives to
+    another sequence: it becomes -1, it does not come to share that page."""
+    c = Cache(10, 4, 3, 5)
+    c.extend([9, 4, 8])   # pages 0 1 2, 3 and 4 5
+    c.free([1])           # page 3 is free: page 5 will go there
+    c.table[0, 1] = 3
+    out = (c.table, c.refs) if in_place else (torch.empty_like(c.full)[:, :5], torch.empty_like(c.refs))
+    moves, count = fa.pages_compact(*c.args(), 4, out=out)
+    assert fa.get_device_status() == fa.FA_ERR_PAGES
+    assert count.item() == 1 and moves[0].tolist() == [5, 3, 4]
+    assert out[0].tolist() == [[0, -1, 2, -1, -1], [-1] * 5, [4, 3, -1, -1, -1]]
+
+
 def test_compact_into_copies_leaves_the_old_ones():
     c = Cache(50, 4, 6, 7)
     c.extend([20, 3, 9, 28, 0, 1])
