@@ -67,10 +67,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
     if (!on[u]) continue;
     const uint32_t sh = a.rows.div(row, &i);
     const uint32_t s = a.heads.div(sh, &h);
-    const int64_t start = __ldg(a.start + s);
+    const int64_t start = a.start[s];
     int count = (int)a.rows.d;
     if (a.counts) {
-      const int given = __ldg(a.counts + s);
+      const int given = a.counts[s];
       if ((given < 0 || given > count) && c == 0 && i == 0 && h == 0) report_pages(a.status);
       count = min(max(given, 0), count);
     }
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
     const int64_t pos = start + i;
     const int64_t col = pos < (int64_t(1) << 31) ? (int64_t)a.page_rows.div((uint32_t)pos) : a.max_pages;
     int page = -1;
-    if (col < a.max_pages) page = __ldg(a.table + s * a.table_stride + col);
+    if (col < a.max_pages) page = a.table[s * a.table_stride + col];
     if (page < 0 || page >= a.num_pages) {
       on[u] = false;
       if (c == 0) report_pages(a.status);
@@ -121,15 +121,15 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams a
   after_stream();
   int n = a.max_moves;
   if (a.count) {
-    const int given = __ldg(a.count);
+    const int given = *a.count;
     if ((given < 0 || given > n) && blockIdx.x == 0 && threadIdx.x == 0) report_pages(a.status);
     n = min(max(given, 0), n);
   }
   const int64_t total = (int64_t)n * a.chunks;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int m = (int)(w / a.chunks), chunk = (int)(w - (int64_t)m * a.chunks);
-    const int src = __ldg(a.moves + 3 * (int64_t)m), dst = __ldg(a.moves + 3 * (int64_t)m + 1);
-    const int rows = __ldg(a.moves + 3 * (int64_t)m + 2);
+    const int32_t* move = a.moves + 3 * (int64_t)m;
+    const int src = move[0], dst = move[1], rows = move[2];
     if (src == -1) continue;
     if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || rows < 0 || rows > (int)a.page_rows.d) {
       if (threadIdx.x == 0) report_pages(a.status);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
         const bool on = g + 8 * u < heads;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(row + (g + 8 * u) * a.qh + M::k_piece(c, q) * 16))
+          const uint4 x = on ? *reinterpret_cast<const uint4*>(row + (g + 8 * u) * a.qh + M::k_piece(c, q) * 16)
                              : make_uint4(0, 0, 0, 0);
           qf[u][c][0] = x.x, qf[u][c][1] = x.y, qf[u][c][2] = x.z, qf[u][c][3] = x.w;
         }

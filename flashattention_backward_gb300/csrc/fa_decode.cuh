@@ -72,7 +72,7 @@ constexpr int blocks_an_sm(bool bf16, int d) {
 
 // ------------------------------------------------------------- sharing out
 __device__ __forceinline__ int rows_of(const DecodeParams& a, int s) {
-  const int n = __ldg(a.lengths + s);
+  const int n = a.lengths[s];
   if (n < 0 || n > a.cap) report_pages(a.status);
   return min(max(n, 0), a.cap);
 }
@@ -310,7 +310,7 @@ struct Loader {
     uint32_t r;
     const uint32_t col = a.page_rows.div((uint32_t)j, &r);
     in = j < at.rows;
-    page = in ? __ldg(a.table + at.s * a.table_stride + col) : -1;
+    page = in ? a.table[at.s * a.table_stride + col] : -1;
     off = at.item * a.ph + (int64_t)r * a.pn;
     if (at.t == 0) {  // a new item: its queries into L1
       int heads;

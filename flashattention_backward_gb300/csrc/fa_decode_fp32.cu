@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, Simt<D, HR>::kBlocks)
       for (int k = threadIdx.x; k < HR * M::kPieces; k += kThreads) {
         const int h = k / M::kPieces, piece = k % M::kPieces;
         reinterpret_cast<float4*>(qs)[k] =
-            h < heads ? __ldg(reinterpret_cast<const float4*>(row + h * a.qh + piece * 16)) : make_float4(0, 0, 0, 0);
+            h < heads ? *reinterpret_cast<const float4*>(row + h * a.qh + piece * 16) : make_float4(0, 0, 0, 0);
       }
       __syncthreads();
 #pragma unroll

@@ -75,6 +75,10 @@ int sm_count();
 // d 128, took 30.9 us a call and takes 28.5, one row appended to 64 sequences 5.7 and
 // 3.3, five calls of a fork 25.6 and 14.4.  At least one block of every kernel has to
 // wait: what comes next on the stream waits for this kernel alone.
+// What work in front may have written is read with plain loads, never with
+// __ldg or through const __restrict__: a load on the non-coherent path promises
+// that its data does not change while the kernel runs, and these kernels run
+// from before that work has ended; nor does after_stream() hold such a load back.
 template <class... P, class... A>
 inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
                                 A... args) {
