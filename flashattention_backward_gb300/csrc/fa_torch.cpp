@@ -14,12 +14,14 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <optional>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -58,8 +60,8 @@ const Tensor& tensor(PyObject* o, const char* name) {
 struct Stream {
   void* raw;
   bool given;
-  c10::DeviceIndex device;
-  Stream(const at::Device& d, PyObject* o) : given(o != Py_None), device(d.index()) {
+  at::Device device;
+  Stream(const at::Device& d, PyObject* o) : given(o != Py_None), device(d) {
     const auto current = c10::cuda::current_device();
     TORCH_CHECK_VALUE(d.index() == current, "the tensors are on ", d, ", the current device is cuda:", (int)current);
     if (given) {
@@ -69,12 +71,32 @@ struct Stream {
       raw = c10::cuda::getCurrentCUDAStream(current).stream();
     }
   }
-  // A tensor of this call on a stream of the caller's: its memory may not be
-  // handed out again before that stream is done with it.
+  c10::cuda::CUDAStream stream() const {
+    return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), device.index());
+  }
+  // A tensor of the caller's, used on a stream that it gave: its memory may not
+  // be handed out again before that stream is done with it.
   void lend(const Tensor& t) const {
-    if (given && t.defined() && t.numel() > 0)
-      c10::cuda::CUDACachingAllocator::recordStream(
-          t.storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), device));
+    if (given) record(t, stream());
+  }
+  // A new tensor.  The allocator hands out memory that was freed while work of
+  // the stream it was freed on was still using it, for that stream alone: so it
+  // is asked for memory of the stream that the call runs on.
+  Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    const c10::cuda::OptionalCUDAStreamGuard guard(given ? std::optional<c10::Stream>(stream().unwrap()) : std::nullopt);
+    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  }
+  // A new tensor for the caller, who may use it on the current stream and then
+  // let it go.
+  Tensor result(at::IntArrayRef shape, at::ScalarType type) const {
+    Tensor t = empty(shape, type);
+    if (given) record(t, c10::cuda::getCurrentCUDAStream(device.index()));
+    return t;
+  }
+
+ private:
+  static void record(const Tensor& t, const c10::cuda::CUDAStream& s) {
+    if (t.defined() && t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), s);
   }
 };
 
@@ -171,12 +193,6 @@ Pages::Pages(PyObject* page_table, PyObject* len, PyObject* ref, PyObject* page_
   refs = ints(ref, "refs", {c.num_pages}, device);
 }
 
-Tensor new_ints(at::IntArrayRef shape, const at::Device& device, const Stream& stream) {
-  Tensor t = at::empty(shape, at::TensorOptions().dtype(at::kInt).device(device));
-  stream.lend(t);
-  return t;
-}
-
 // The library's call, without the interpreter's lock: a full launch queue
 // makes it wait.
 template <class F, class... A>
@@ -236,8 +252,8 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const RowStrides qs(q);
   Tensor o, L, workspace;
   if (a[7] == Py_None) {
-    o = at::empty(q.sizes(), at::TensorOptions().dtype(cache.type).device(cache.device));
-    L = at::empty(q.sizes().slice(0, 3), at::TensorOptions().dtype(at::kFloat).device(cache.device));
+    o = stream.result(q.sizes(), cache.type);
+    L = stream.result(q.sizes().slice(0, 3), at::kFloat);
   } else {
     TORCH_CHECK_TYPE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 2, "out must be a tuple (o, L)");
     o = tensor(PyTuple_GET_ITEM(a[7], 0), "out[0]");
@@ -247,6 +263,8 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(L.sizes() == q.sizes().slice(0, 3) && L.scalar_type() == at::kFloat &&
                           L.device() == cache.device && L.is_contiguous(),
                       "out[1] must be a contiguous float32 tensor of shape ", q.sizes().slice(0, 3));
+    stream.lend(o);
+    stream.lend(L);
   }
   size_t bytes = g_fa.workspace_bytes(&c, heads);
   if (a[6] != Py_None) {
@@ -254,12 +272,10 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(workspace.device() == cache.device && workspace.is_contiguous(),
                       "workspace must be a contiguous tensor on ", cache.device);
     bytes = workspace.nbytes();
+    stream.lend(workspace);
   } else if (bytes > 0) {
-    workspace = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(cache.device));
+    workspace = stream.empty({(int64_t)bytes}, at::kByte);
   }
-  stream.lend(o);
-  stream.lend(L);
-  stream.lend(workspace);
   const RowStrides os(o);
   call("fa_decode", g_fa.decode, &c, heads, (float)scale, (const void*)q.data_ptr(), qs.s0, qs.s1,
        (const void*)cache.k, (const void*)cache.v, cache.table, lengths, o.data_ptr(), os.s0, os.s1,
@@ -309,7 +325,7 @@ PyObject* extend(PyObject* const* a, Py_ssize_t n) {
   Pages p(a[0], a[1], a[2], a[4]);
   const Stream stream(p.device, a[5]);
   const int32_t* n_new = ints(a[3], "n_new", {p.c.S}, p.device);
-  Tensor start = new_ints({p.c.S}, p.device, stream);
+  Tensor start = stream.result({p.c.S}, at::kInt);
   call("fa_pages_extend", g_fa.extend, &p.c, p.table, p.lengths, p.refs, n_new, static_cast<int32_t*>(start.data_ptr()),
        stream.raw);
   return THPVariable_Wrap(start);
@@ -324,7 +340,7 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(list.dim() == 1, "src must be a 1-D tensor");
   const int64_t pairs = list.size(0);
   const int32_t *src = ints(a[3], "src", {pairs}, p.device), *dst = ints(a[4], "dst", {pairs}, p.device);
-  Tensor moves = new_ints({pairs, 3}, p.device, stream);
+  Tensor moves = stream.result({pairs, 3}, at::kInt);
   if (pairs > 0)
     call("fa_pages_fork", g_fa.fork, &p.c, as_int32(pairs, "the number of pairs"), src, dst, p.table, p.lengths, p.refs,
          static_cast<int32_t*>(moves.data_ptr()), stream.raw);
@@ -359,7 +375,7 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
     table_out = static_cast<int32_t*>(t.data_ptr());
     refs_out = ints(PyTuple_GET_ITEM(a[4], 1), "out[1]", {p.c.num_pages}, p.device);
   }
-  Tensor moves = new_ints({p.c.num_pages / 2, 3}, p.device, stream), count = new_ints({1}, p.device, stream);
+  Tensor moves = stream.result({p.c.num_pages / 2, 3}, at::kInt), count = stream.result({1}, at::kInt);
   call("fa_pages_compact", g_fa.compact, &p.c, (const int32_t*)p.table, (const int32_t*)p.lengths,
        (const int32_t*)p.refs, table_out, refs_out, static_cast<int32_t*>(moves.data_ptr()),
        static_cast<int32_t*>(count.data_ptr()), stream.raw);

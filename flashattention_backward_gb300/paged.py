@@ -23,6 +23,10 @@ range, too few free pages) is never followed; it is recorded in the device
 status word, which :func:`get_device_status` reads and ``check_status=True``
 raises as :class:`FaError`.
 
+A call runs on the current stream, or on ``stream``, whose work is in order
+with the call's; what it allocates is memory of that stream.  Its results may
+be used on the current stream too, once that has waited for the other.
+
 No call here has a gradient.
 """
 
