@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int a = src[i], held = g.pages(lengths[a]);
       for (int c = lane; c < held; c += 32) {
         const int p = table[a * g.table_stride + c];
-        bad |= p < 0 || p >= g.num_pages;
+        // nor may it name a free page, which could be handed out below
+        bad |= p < 0 || p >= g.num_pages || refs[p] <= 0;
       }
     }
     if (bad) atomicOr(cluster.map_shared_rank(&any_bad, 0), 1);

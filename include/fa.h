@@ -355,8 +355,9 @@ fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengt
  * free one; moves[i] = (old page, new page, rows in it) for
  * fa_cache_copy_pages, or (-1, -1, -1).  src may repeat.  All or nothing:
  * with an index out of range, a dst that is not empty, comes twice or is also
- * a src, a damaged table row or too few free pages, nothing changes, all
- * moves are -1 and FA_ERR_PAGES is recorded.  1 <= pairs <= S <= 65536. */
+ * a src, a damaged table row (of a src: an entry among its pages that names
+ * none, or a free one) or too few free pages, nothing changes, all moves are
+ * -1 and FA_ERR_PAGES is recorded.  1 <= pairs <= S <= 65536. */
 fa_status fa_pages_fork(const fa_cache* c, int32_t pairs, const int32_t* src, const int32_t* dst, int32_t* page_table,
                         int32_t* lengths, int32_t* refs, int32_t* moves, void* stream);
 
