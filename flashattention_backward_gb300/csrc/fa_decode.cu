@@ -45,7 +45,8 @@ namespace {
 //
 // P is multiplied as the sum of two bf16 numbers (p rounded, and what is left
 // rounded): the second product costs nothing beside the loads, and leaves the
-// rounding of the output as the only one to fewer than 16 bits.
+// rounding of the output as the only one to fewer than 16 bits.  What is left
+// may be 0 or below it, which makes NaN of an infinity in V: infinite_values().
 template <int D>
 struct Mma {
   static constexpr int kRows = 16;             // of a tile, a warp
@@ -87,6 +88,66 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Puts the infinities of V where its rows gave NaN, although the weights are
+// none: in the sums that this thread has just stored at `dst`, heads `pitch`
+// bytes apart (bf16, or fp32 where they are a part), over tiles first ... last
+// of an item.  The weights are positive, so a column is infinite if its
+// infinities are of one sign and it holds no NaN.  Each thread by itself, and
+// never in ordinary use: 64 sequences of up to 8192 rows, 32 heads on 8 of d 128,
+// take 1.9 ms with an infinity in every page, 4.0 ms with nothing else in V, and
+// 0.15 ms without.
+template <int D, int NH>
+__device__ __noinline__ void infinite_values(const DecodeParams& a, int s, int item, int rows, int first, int last,
+                                             int heads, char* dst, int64_t pitch, bool part) {
+  constexpr int VW = Mma<D>::kVW, kAhead = 4;
+  const int end = min(rows, (last + 1) * Mma<D>::kTile);
+#pragma unroll 1
+  for (int i = 0; i < NH * (D / VW); ++i)
+#pragma unroll 1
+    for (int k = threadIdx.x; k < 2 * VW; k += kThreads) {  // four columns of a head, as they were stored
+      const int head = 8 * (i / (D / VW)) + k / (VW / 4), col = i % (D / VW) * VW + k % (VW / 4) * 4;
+      if (head >= heads) continue;
+      float* as_part = reinterpret_cast<float*>(dst + head * pitch) + col;
+      __nv_bfloat16* as_bf16 = reinterpret_cast<__nv_bfloat16*>(dst + head * pitch) + col;
+      uint32_t lost = 0;  // a bit a column: NaN here, and infinities above, below and NaN in its rows
+#pragma unroll
+      for (int x = 0; x < 4; ++x) lost |= isnan(part ? as_part[x] : __bfloat162float(as_bf16[x])) ? 1u << x : 0;
+      if (!lost) continue;
+      uint32_t above = 0, below = 0, none = 0;
+#pragma unroll 1
+      for (int j = first * Mma<D>::kTile; j < end; j += kAhead) {
+        uint2 v[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          uint32_t r;
+          const uint32_t c = a.page_rows.div((uint32_t)(j + e), &r);
+          const int page = j + e < end ? a.table[s * a.table_stride + c] : -1;
+          v[e] = make_uint2(0, 0);
+          if (page >= 0 && page < a.num_pages)
+            v[e] = *reinterpret_cast<const uint2*>(a.V + page * a.pp + item * a.ph + (int64_t)r * a.pn + 2 * col);
+        }
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t bits = (x < 2 ? v[e].x : v[e].y) >> (x % 2 * 16) & 0xffffu;
+            above |= bits == 0x7f80u ? 1u << x : 0;
+            below |= bits == 0xff80u ? 1u << x : 0;
+            none |= (bits & 0x7fffu) > 0x7f80u ? 1u << x : 0;
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (!((lost & ~none & (above ^ below)) >> x & 1)) continue;
+        const float inf = above >> x & 1 ? INFINITY : -INFINITY;
+        if (part)
+          as_part[x] = inf;
+        else
+          as_bf16[x] = __float2bfloat16(inf);
+      }
+    }
 }
 
 // kAlone: a cluster an item, joined here; else a block a run.
@@ -249,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
         if (q == 0) ml[warp][g + 8 * u] = make_float2(m[u], l[u]);
       }
       __syncthreads();
+      bool odd = false;  // NaN in a sum of this thread's, with weights that are none
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
         // this warp's factor of heads 2q, 2q + 1
@@ -287,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
               const float4 x = *reinterpret_cast<const float4*>(exchange + (w * 8 + in8) * M::kPad + col - c * VW);
               o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
             }
+            odd |= isnan((o.x + o.y) + (o.z + o.w)) && !isnan(sum);
             if (whole) {
               const bool none = sum == 0.f;
               const float inv = none ? 0.f : 1.f / sum;
@@ -303,6 +366,12 @@ __global__ void __launch_bounds__(kThreads, Mma<D>::kBlocks) decode_mma_kernel(c
             }
           }
         }
+      }
+      if (odd) {
+        char* dst = whole    ? a.O + at.s * a.os + h0 * a.oh
+                    : kAlone ? reinterpret_cast<char*>(part_o)
+                             : reinterpret_cast<char*>(a.part_o + (int64_t)slot * kHeads * D);
+        infinite_values<D, NH>(a, at.s, at.item, at.rows, begin, at.t, heads, dst, whole ? a.oh : D * 4, !whole);
       }
     }
     at = next;

@@ -290,8 +290,11 @@ typedef struct {
  * Rows behind n are not read.  A row on a page out of range counts as not
  * visible, a negative length as 0 and one beyond page_rows * max_pages as
  * that (FA_ERR_PAGES in each case).  In bf16 the weights are multiplied as
- * the sum of two bf16 numbers, so that O is rounded once, to bf16; an infinite
- * value in a visible row of V gives NaN.
+ * the sum of two bf16 numbers, so that O is rounded once, to bf16.  An infinite
+ * value in a visible row of V comes out as it is; as NaN where both signs meet,
+ * and possibly where its weight is below 2^-126 of the largest.  Sums are taken
+ * in fp32 before they are divided by the sum of the weights: |V| up to the
+ * largest float32 / (2 n) cannot overflow them.
  * Q, O are [S, H, d] with element strides (q_stride_s, q_stride_h) and
  * (o_stride_s, o_stride_h), 16-byte aligned with byte strides multiples of
  * 16; O may not overlap Q.  L is a dense [S, H] float32 array.  H is a
