@@ -55,6 +55,12 @@ const Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// No call here has a gradient, so none may be asked for one.
+void no_gradient(const char* call, const Tensor& t) {
+  TORCH_CHECK_VALUE(!(t.requires_grad() && at::GradMode::is_enabled()), call,
+                    " has no gradient: call it under torch.no_grad()");
+}
+
 // The stream to launch on, after checking that `device` is the current one.
 // given: an address as a Python int, or None for the current stream.
 struct Stream {
@@ -233,14 +239,15 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
 PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   want(n, 9);
   const Tensor& q = tensor(a[0], "q");
+  no_gradient("attention_decode", q);
+  no_gradient("attention_decode", tensor(a[1], "k_pages"));
+  no_gradient("attention_decode", tensor(a[2], "v_pages"));
   Cache cache(a[1], a[2], a[3]);
   const fa_cache& c = cache.c;
   TORCH_CHECK_VALUE(q.dim() == 4 && q.size(0) == c.S && q.size(2) == 1 && q.size(3) == c.d, "q must be a [", c.S,
                     ", heads, 1, ", c.d, "] tensor");
   TORCH_CHECK_VALUE(q.scalar_type() == cache.type && q.device() == cache.device,
                     "q must have the dtype and device of the pools");
-  TORCH_CHECK_VALUE(!(q.requires_grad() && at::GradMode::is_enabled()),
-                    "attention_decode has no gradient: call it under torch.no_grad()");
   const Stream stream(cache.device, a[8]);
   const int32_t* lengths = ints(a[4], "lengths", {c.S}, cache.device);
   const int32_t heads = as_int32(q.size(1), "the number of heads");
@@ -258,6 +265,8 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_TYPE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 2, "out must be a tuple (o, L)");
     o = tensor(PyTuple_GET_ITEM(a[7], 0), "out[0]");
     L = tensor(PyTuple_GET_ITEM(a[7], 1), "out[1]");
+    no_gradient("attention_decode", o);
+    no_gradient("attention_decode", L);
     TORCH_CHECK_VALUE(o.sizes() == q.sizes() && o.scalar_type() == cache.type && o.device() == cache.device,
                       "out[0] must have the shape, dtype and device of q");
     TORCH_CHECK_VALUE(L.sizes() == q.sizes().slice(0, 3) && L.scalar_type() == at::kFloat &&
@@ -287,6 +296,10 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
 PyObject* append(PyObject* const* a, Py_ssize_t n) {
   want(n, 8);
   const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  no_gradient("cache_append", k);
+  no_gradient("cache_append", v);
+  no_gradient("cache_append", tensor(a[2], "k_pages"));
+  no_gradient("cache_append", tensor(a[3], "v_pages"));
   Cache cache(a[2], a[3], a[4]);
   const fa_cache& c = cache.c;
   TORCH_CHECK_VALUE(k.dim() == 4 && k.size(0) == c.S && k.size(1) == c.H_kv && k.size(3) == c.d && v.sizes() == k.sizes(),
@@ -308,6 +321,8 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
 // k_pages, v_pages, moves, count, stream
 PyObject* copy(PyObject* const* a, Py_ssize_t n) {
   want(n, 5);
+  no_gradient("cache_copy_pages", tensor(a[0], "k_pages"));
+  no_gradient("cache_copy_pages", tensor(a[1], "v_pages"));
   Cache cache(a[0], a[1], Py_None);
   const Tensor& moves = tensor(a[2], "moves");
   TORCH_CHECK_VALUE(moves.dim() == 2, "moves must be an [n, 3] tensor");

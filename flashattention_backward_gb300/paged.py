@@ -27,7 +27,8 @@ A call runs on the current stream, or on ``stream``, whose work is in order
 with the call's; what it allocates is memory of that stream.  Its results may
 be used on the current stream too, once that has waited for the other.
 
-No call here has a gradient.
+No call here has a gradient; one whose tensors need one is refused unless
+gradients are switched off (``torch.no_grad()``).
 """
 
 from __future__ import annotations
