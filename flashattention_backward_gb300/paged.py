@@ -95,7 +95,8 @@ def _binding():
         lib = _pkg.load_library()
         path = _build.torch_binding_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"the PyTorch binding was not found at {path}: run __graft_entry__.build() first")
+            raise RuntimeError(f"the PyTorch binding was not found at {path}: run __graft_entry__.build(), which says why "
+                               "where it cannot be compiled")
         spec = importlib.util.spec_from_file_location("_fa_torch", path)
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
