@@ -136,7 +136,11 @@ def attention_decode(q, k_pages, v_pages, page_table, lengths, scale: Optional[f
     ``out`` may pass (o, L) to write to; ``workspace`` a uint8 tensor of
     :func:`fa_decode_workspace_bytes`, otherwise one is allocated for the
     call.  Calls that may run at the same time, replays of captured graphs
-    among them, need a workspace each."""
+    among them, need a workspace each.
+
+    The same call gives the same bits.  The order of its sums goes by the
+    lengths, the heads, the dtype and the shapes of pools and table, so a table
+    with more columns may give other last bits."""
     got = (_EXT or _binding()).decode(q, k_pages, v_pages, page_table, lengths, scale, workspace,
                                       None if out is None else tuple(out), _raw(stream))
     if check_status:

@@ -305,8 +305,9 @@ typedef struct {
  * fa_decode_workspace_bytes(c, H) bytes, whose contents before the call do
  * not matter; 0 bytes: may be NULL).  Calls that may run at the same time
  * need a workspace each, also when they are replayed from graphs.
- * Results are bitwise reproducible for the same S, H and lengths on the same
- * kind of GPU.  As with every call that keeps a status word, the first one on
+ * Results are bitwise reproducible for the same H, lengths and dtype, d, H_kv,
+ * S, page_rows and max_pages of the cache on the same kind of GPU: the order of
+ * the sums goes by these, and one more column of the table may change it.  As with every call that keeps a status word, the first one on
  * a device belongs before any stream capture. */
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H);
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
