@@ -414,7 +414,7 @@ fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengt
   const fa_status st = fa::check_pages(c);
   if (st != FA_OK) return st;
   if (!fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(refs) || !fa::aligned4(n_new) ||
-      !fa::aligned4(start))
+      !fa::aligned4(start) || start == lengths || start == n_new)
     return FA_ERR_INVALID_ARG;
   fa::Pages g;
   if (!fa::geometry(*c, &g)) return FA_ERR_CUDA;

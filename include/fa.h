@@ -350,7 +350,9 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
  * += n_new[s], and the pages that takes enter the table with refs = 1.  All
  * or nothing: when there are too few free pages, a sequence would pass the
  * table, or a length or n_new is out of range, nothing changes, every
- * start[s] is -1 and FA_ERR_PAGES is recorded. */
+ * start[s] is -1 and FA_ERR_PAGES is recorded.  (Where free pages were too few,
+ * table entries behind a sequence's pages may become -1, and counts below 0 are
+ * 0 then.)  start may be neither lengths nor n_new. */
 fa_status fa_pages_extend(const fa_cache* c, int32_t* page_table, int32_t* lengths, int32_t* refs,
                           const int32_t* n_new, int32_t* start, void* stream);
 
