@@ -8,7 +8,7 @@
 // four of V before its first store, 128 bytes in flight a thread.
 //
 // Measured: prompts of up to 4000 rows for 4 sequences, 16 heads of d 128, 163 MB
-// read and written: 28 us, 5.9 TB/s (87 % of a copy's rate; 25.7 to 27.2 us in ncu).
+// read and written: 27 to 28 us, 5.9 TB/s (87 % of a copy's rate; 25.7 to 27.2 us in ncu).
 // 2048 pages of 16 rows, 8 heads of d 128, 268 MB: 37 to 40 us, 6.8 to 7.2 TB/s
 // (ncu).  One row each for 64 sequences: 3.4 us, the launch and three dependent loads.
 

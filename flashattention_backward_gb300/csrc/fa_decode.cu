@@ -17,8 +17,8 @@
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 64 sequences of up
 // to 8192 rows, 32 heads on 8 of d 128, 987 MB: 152 to 155 us, 94 to 96 %.  4 of 8192, 16 heads
-// of d 256, 537 MB: 91 us, 87 %.  32 of up to 2048, 32 heads of d 64, 235 MB: 44 us,
-// 78 %; one of 32768, 8 heads of d 128, 134 MB: 28 us, 71 %: the start of a call,
+// of d 256, 537 MB: 90 to 92 us, 85 to 87 %.  32 of up to 2048, 32 heads of d 64, 235 MB: 44 to
+// 45 us, 77 %; one of 32768, 8 heads of d 128, 134 MB: 28 us, 70 %: the start of a call,
 // the last tiles and the join take about 8 us beside the loads.
 
 #include "fa_decode.cuh"
@@ -39,9 +39,12 @@ namespace {
 //
 // A warp copies its own 16 rows (cp.async into a ring of its own) and waits for
 // them alone: no block barrier in the loop, conflict-free 16-byte
-// shared-memory reads.  tcgen05 would want 64 or 128 rows of A where
-// there are 1 to 16 query heads, and a barrier a tile, for a product that is
-// not the limit.
+// shared-memory reads.  tcgen05 could take the keys as the 64 or 128 rows of A
+// and the heads as B's columns in both products, at the price of a barrier a
+// tile and of the weights' way through tensor memory, for products that are not
+// the limit up to 16 heads.  Above 16 they are part of it: 32 heads a key head
+// reach 42 % of a copy's rate at d 32, 53 to 64 % at d 64 to 256 (32 sequences of 8192
+// rows), against 80 to 90 % with 16.
 //
 // P is multiplied as the sum of two bf16 numbers (p rounded, and what is left
 // rounded): the second product costs nothing beside the loads, and leaves the

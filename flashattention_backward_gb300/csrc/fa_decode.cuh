@@ -100,7 +100,12 @@ constexpr int kItemCost = 1;
 // rows (100 units a resident block) took 164.1 us with equal runs, 158.7 with
 // these, 157.9 to 159.7 with two or three times as many small ones; 32 of up to
 // 2048 (33 units) took 44.9 and, with small runs, 47 to 50: a block's start
-// costs as much as two tiles.  Hence kMinUnits.
+// costs as much as two tiles.  Hence kMinUnits.  With 24 instead, on one
+// GPU: 82.4 -> 78.3 us (64 sequences of up to 4608 rows, 8 key heads of d 128: 48 units a
+// resident block), 75.5 -> 73.9 (of up to 3584: 45), 92.9 -> 90.5 (4 of 8192, 16 heads of
+// d 256: 54), 106.6 -> 103.2 (16 of up to 4000: 64), 54.6 -> 49.7 (16 of up to 2048: 28), but
+// 43.4 -> 44.2 (64 of up to 2048, d 128: 24) and 50.5 -> 51.0 (32 of 1024, 32 heads of d 64: 38,
+// items of 16 tiles): a lower border would suit long items, and 64 is on the safe side.
 constexpr double kBigShare = 0.9;
 constexpr int kSmallRuns = 1;
 constexpr int kMinUnits = 64;  // of a resident block, for there to be small runs
@@ -443,8 +448,10 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& a, const float4
 // the block's groups of so many threads, `together` take a head each and the
 // others share its parts, kAhead loads at a time.
 // 128 threads and their 2.2 KB of shared memory fit beside the blocks of the
-// kernel in front, so the join is there when those end: 64 sequences of up to
-// 8192 rows took 153.5 us, with 256 threads 156.4.
+// kernel in front, so the join is there when those end.  With 256 threads, on the
+// same GPU: 32 sequences of 1024 rows, 32 heads of d 64, 55.4 us instead of 50.5; of
+// 4096 173.3 instead of 165.4; 64 of up to 8192, 8 key heads of d 128, 138.8 instead
+// of 136.9; nothing at d 256.
 constexpr int kJoinThreads = 128;
 struct JoinShape {
   int by_item, part_heads;
@@ -570,7 +577,9 @@ inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 25
 // 10.2 in runs and 7.7 with 4 blocks of 2 tiles.
 constexpr int kClusterTiles = 2;
 inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
-  // clusters that the GPU holds of each size, for each block an SM: a cluster stays inside a GPC
+  // clusters that the GPU holds of each size, for each block an SM, as a GB300 of 152 SMs answers when asked: a cluster
+  // stays inside a GPC.  Written down, because the workspace's size goes by this too, which is asked for without a GPU;
+  // one that holds other numbers of them computes the same, in more or fewer waves.
   struct {
     int blocks, fit;
   } sizes[] = {{kMostBlocks, 7}, {8, 15}, {4, 36}, {2, 76}, {1, 152}};

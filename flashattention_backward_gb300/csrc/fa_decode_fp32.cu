@@ -18,11 +18,12 @@
 //          lanes take whole rows of V; the weights of a row, all heads in one or
 //          two 16-byte pieces of shared memory, are the same for all of them.
 //
-// Measured at 32 sequences of 8192 rows, as a share of the 6.8 TB/s of a copy: 95 %
-// with one query head a key head (d 32 to 256), 86 to 92 % with four; with eight,
-// 87 % at d 64, 82 % at d 128, 76 % at d 96, and 56 % at d 256, whose tiles have 8 rows
-// a warp: there the one warp of each scheduler waits for its own FMAs and
-// shared-memory reads.
+// Measured at 32 sequences of 8192 rows, as a share of the 6.8 TB/s of a copy: 94 to
+// 98 % with one query head a key head (d 32 to 256), 86 to 94 % with four, at d 16 81 and
+// 79 %.  With eight, 87 % at d 64, 82 % at d 128, 76 % at d 32 and 96, 61 % at d 16, whose
+// tiles are 1 KB of K for a warp, and 56 % at d 256, whose tiles have 8 rows a warp
+// and whose SMs one warp a scheduler.  Above eight each piece of the heads reads the
+// tile again: 29 (d 256) to 48 % (d 64) with 16.
 
 #include "fa_decode.cuh"
 

@@ -10,9 +10,10 @@
 // and what bounds the calls is the latency of a handful of dependent passes,
 // not bandwidth.
 //
-// Measured (ncu, cold caches, launch included): extend 7.6 us for 256 sequences
-// and a pool of 2000 pages, fork 11 us for 224 pairs of up to 63 pages, free 5 us for
-// the same, compact 8 us and 7 us for 8192 pages and a table of 64 x 64.
+// Measured (ncu, cold caches, launch included): extend 9.2 to 9.5 us for 256
+// sequences and a pool of 2000 pages, fork 10.4 to 11.0 us for 224 pairs of up to 63 pages,
+// free 6.2 to 6.9 us for the same, compact 9.3 to 9.5 us and 8.4 to 9.1 us for 8192 pages
+// and a table of 64 x 64.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
