@@ -307,8 +307,9 @@ typedef struct {
  * need a workspace each, also when they are replayed from graphs.
  * Results are bitwise reproducible for the same H, lengths and dtype, d, H_kv,
  * S, page_rows and max_pages of the cache on the same kind of GPU: the order of
- * the sums goes by these, and one more column of the table may change it.  As with every call that keeps a status word, the first one on
- * a device belongs before any stream capture. */
+ * the sums goes by these, and one more column of the table may change it.
+ * As with every call that keeps a status word, the first one on a device
+ * belongs before any stream capture. */
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H);
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
                     const void* K_pages, const void* V_pages, const int32_t* page_table, const int32_t* lengths,
