@@ -57,6 +57,12 @@ __all__ = [
     "pages_fork",
     "pages_free",
     "pages_compact",
+    "cache_for_e4m3",
+    "attention_decode_e4m3",
+    "fa_decode_e4m3_workspace_bytes",
+    "cache_append_e4m3",
+    "cache_read_e4m3",
+    "cache_copy_pages_e4m3",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE, FA_ERR_PAGES = range(7)
@@ -463,9 +469,15 @@ def selftest_wait_timeout(limit_ns: int, stream=None) -> None:
 from .paged import (  # noqa: E402
     FaCache,
     attention_decode,
+    attention_decode_e4m3,
     cache_append,
+    cache_append_e4m3,
     cache_copy_pages,
+    cache_copy_pages_e4m3,
     cache_for,
+    cache_for_e4m3,
+    cache_read_e4m3,
+    fa_decode_e4m3_workspace_bytes,
     fa_decode_workspace_bytes,
     pages_compact,
     pages_extend,

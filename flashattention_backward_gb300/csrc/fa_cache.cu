@@ -112,11 +112,16 @@ struct CopyParams {
   int chunks;            // chunks of kBlockPieces in a page
   int pieces;            // H_kv * page_rows * pieces of a row
   int64_t pp, ph, pn;    // byte strides of the pools
+  float *KS, *VS;        // kScales: [num_pages, heads, blocks]
+  FastDiv blocks;
+  int heads, block_rows;
 };
 
 // One block takes chunks of pages, a grid's width apart.  The rows of a triple
 // do not overlap another's, so loads and stores of one iteration need no
-// order; K and V pools are different buffers.
+// order; K and V pools are different buffers.  kScales: pools in 8 bits, whose
+// scales move along, those of a page shared out among its chunks.
+template <bool kScales>
 __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams a) {
   after_stream();
   int n = a.max_moves;
@@ -160,7 +165,59 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyParams a
         *reinterpret_cast<uint4*>(kd + at[u]) = k[u];
         *reinterpret_cast<uint4*>(vd + at[u]) = v[u];
       }
+    if constexpr (kScales) {
+      const int held = (rows + a.block_rows - 1) / a.block_rows;  // blocks of a head that hold rows
+      const int64_t all = (int64_t)a.heads * a.blocks.d, from = src * all, to = dst * all;
+      for (int64_t x = (int64_t)chunk * kThreads + threadIdx.x; x < all; x += (int64_t)a.chunks * kThreads) {
+        uint32_t b;
+        a.blocks.div((uint32_t)x, &b);
+        if ((int)b >= held) continue;
+        const float k = a.KS[from + x], v = a.VS[from + x];
+        a.KS[to + x] = k;
+        a.VS[to + x] = v;
+      }
+    }
   }
+}
+
+// es: bytes of an element of the pools; block_rows > 0: pools in 8 bits.
+fa_status copy_pages(const fa_cache* c, int es, int32_t block_rows, int32_t max_moves, const int32_t* moves,
+                     const int32_t* count, void* K_pages, void* V_pages, float* K_scales, float* V_scales,
+                     void* stream) {
+  if (max_moves < 0 || !aligned16(K_pages) || !aligned16(V_pages) || (max_moves > 0 && !aligned4(moves)) ||
+      (count && !aligned4(count)))
+    return FA_ERR_INVALID_ARG;
+  const int row_pieces = c->d * es / 16;
+  const int64_t pieces = (int64_t)c->H_kv * c->page_rows * row_pieces;
+  if (pieces > (int64_t(1) << 30)) return FA_ERR_UNSUPPORTED;
+  if (max_moves == 0) return FA_OK;
+  CopyParams a;
+  a.status = device_status_word();
+  const int sms = sm_count();
+  if (!a.status || sms < 1) return FA_ERR_CUDA;
+  a.KP = (char*)K_pages;
+  a.VP = (char*)V_pages;
+  a.moves = moves;
+  a.count = count;
+  a.row_pieces = FastDiv(row_pieces);
+  a.page_rows = FastDiv(c->page_rows);
+  a.max_moves = max_moves;
+  a.num_pages = c->num_pages;
+  a.pieces = (int)pieces;
+  a.chunks = (int)ceil_div(pieces, kBlockPieces);
+  a.pp = c->stride_page * es;
+  a.ph = c->stride_h * es;
+  a.pn = c->stride_n * es;
+  a.KS = K_scales;
+  a.VS = V_scales;
+  a.blocks = FastDiv(block_rows > 0 ? c->page_rows / block_rows : 1);
+  a.heads = c->H_kv;
+  a.block_rows = block_rows;
+  const int64_t work = (int64_t)max_moves * a.chunks;
+  const int64_t resident = (int64_t)sms * 8;
+  const dim3 grid((unsigned)(work < resident ? work : resident));
+  return status_of(launch_early(block_rows > 0 ? cache_copy_kernel<true> : cache_copy_kernel<false>, grid, kThreads, 0,
+                                (cudaStream_t)stream, 1, a));
 }
 
 }  // namespace
@@ -217,35 +274,18 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
   fa::NvtxRange range("fa_cache_copy_pages");
   const fa_status st = fa::check_cache(c);
   if (st != FA_OK) return st;
-  if (max_moves < 0 || !fa::aligned16(K_pages) || !fa::aligned16(V_pages) || (max_moves > 0 && !fa::aligned4(moves)) ||
-      (count && !fa::aligned4(count)))
+  return fa::copy_pages(c, fa::elem_size(c->dtype), 0, max_moves, moves, count, K_pages, V_pages, nullptr, nullptr, stream);
+}
+
+fa_status fa_cache_copy_pages_e4m3(const fa_cache* c, int32_t block_rows, int32_t max_moves, const int32_t* moves,
+                                   const int32_t* count, void* K_pages, void* V_pages, float* K_scales,
+                                   float* V_scales, void* stream) {
+  fa::NvtxRange range("fa_cache_copy_pages_e4m3");
+  const fa_status st = fa::check_cache_e4m3(c, block_rows);
+  if (st != FA_OK) return st;
+  if (!fa::aligned4(K_scales) || !fa::aligned4(V_scales) || K_pages == V_pages || K_scales == V_scales)
     return FA_ERR_INVALID_ARG;
-  const int es = fa::elem_size(c->dtype);
-  const int row_pieces = c->d * es / 16;
-  const int64_t pieces = (int64_t)c->H_kv * c->page_rows * row_pieces;
-  if (pieces > (int64_t(1) << 30)) return FA_ERR_UNSUPPORTED;
-  if (max_moves == 0) return FA_OK;
-  fa::CopyParams a;
-  a.status = fa::device_status_word();
-  const int sms = fa::sm_count();
-  if (!a.status || sms < 1) return FA_ERR_CUDA;
-  a.KP = (char*)K_pages;
-  a.VP = (char*)V_pages;
-  a.moves = moves;
-  a.count = count;
-  a.row_pieces = fa::FastDiv(row_pieces);
-  a.page_rows = fa::FastDiv(c->page_rows);
-  a.max_moves = max_moves;
-  a.num_pages = c->num_pages;
-  a.pieces = (int)pieces;
-  a.chunks = (int)fa::ceil_div(pieces, fa::kBlockPieces);
-  a.pp = c->stride_page * es;
-  a.ph = c->stride_h * es;
-  a.pn = c->stride_n * es;
-  const int64_t work = (int64_t)max_moves * a.chunks;
-  const int64_t resident = (int64_t)sms * 8;
-  const dim3 grid((unsigned)(work < resident ? work : resident));
-  return fa::status_of(fa::launch_early(fa::cache_copy_kernel, grid, fa::kThreads, 0, (cudaStream_t)stream, 1, a));
+  return fa::copy_pages(c, 1, block_rows, max_moves, moves, count, K_pages, V_pages, K_scales, V_scales, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,54 @@
+// e4m3 numbers and the scales of a paged cache in 8 bits (fa_cache_e4m3.cu,
+// fa_decode_e4m3.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa_paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+// Two numbers to e4m3, ties to even, `lo` in bits 0-7.  |x| <= 448 and NaN come
+// out as such; anything larger would become 448.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  return pack_e4m3x2(a, b) | pack_e4m3x2(c, d) << 16;
+}
+// The numbers in bits 0-15 and in bits 16-31 as two fp16 each, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_lo(uint32_t x) {
+  uint32_t r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi(uint32_t x) {
+  uint32_t r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float4 e4m3x4_to_float4(uint32_t x) {
+  const float2 a = f16x2_to_float2(e4m3x2_lo(x)), b = f16x2_to_float2(e4m3x2_hi(x));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// The smallest power of two s with t <= 448 s, 2^-126 at least, for the bits of
+// a finite t >= 0.  448 is 1.75 * 2^8: the addition carries into the exponent
+// where t's mantissa is above 1.75.
+__device__ __forceinline__ float scale_for(uint32_t t) {
+  const int e = (int)((t + 0x1fffffu) >> 23) - 8;
+  return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+// 1 / s of a power of two, 2^-126 to 2^126.
+__device__ __forceinline__ float inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
+
+}  // namespace fa

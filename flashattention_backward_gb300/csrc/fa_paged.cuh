@@ -50,17 +50,26 @@ inline bool good_stride(int64_t stride, int d, int es, bool written) {
   return stride >= (written ? d : 0) && stride < (int64_t(1) << 48) && (stride * es) % 16 == 0;
 }
 
-inline fa_status check_cache(const fa_cache* c) {
+// es: bytes of an element of the pools.
+inline fa_status check_pools(const fa_cache* c, int es) {
   const fa_status st = check_pages(c);
   if (st != FA_OK) return st;
   if (c->dtype != FA_BF16 && c->dtype != FA_FP32) return FA_ERR_INVALID_ARG;
   const bool known = c->d == 32 || c->d == 64 || c->d == 96 || c->d == 128 || c->d == 256;
   if (!known && !(c->d == 16 && c->dtype == FA_FP32)) return FA_ERR_UNSUPPORTED;
-  const int es = elem_size(c->dtype);
   if (!good_stride(c->stride_page, c->d, es, true) || !good_stride(c->stride_h, c->d, es, true) ||
       !good_stride(c->stride_n, c->d, es, true))
     return FA_ERR_INVALID_ARG;
   return FA_OK;
+}
+inline fa_status check_cache(const fa_cache* c) {
+  return check_pools(c, c && c->dtype == FA_BF16 ? 2 : 4);
+}
+// Pools in 8 bits with a scale for every block_rows rows.
+inline fa_status check_cache_e4m3(const fa_cache* c, int32_t block_rows) {
+  const fa_status st = check_pools(c, 1);
+  if (st != FA_OK) return st;
+  return block_rows >= 1 && c->page_rows % block_rows == 0 ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
 inline fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }

@@ -23,6 +23,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -41,6 +42,11 @@ struct Entries {
   decltype(&fa_pages_fork) fork;
   decltype(&fa_pages_free) free;
   decltype(&fa_pages_compact) compact;
+  decltype(&fa_decode_e4m3_workspace_bytes) workspace_bytes_e4m3;
+  decltype(&fa_decode_e4m3) decode_e4m3;
+  decltype(&fa_cache_append_e4m3) append_e4m3;
+  decltype(&fa_cache_read_e4m3) read_e4m3;
+  decltype(&fa_cache_copy_pages_e4m3) copy_e4m3;
 } g_fa;
 PyObject* g_error = nullptr;  // FaError(code, what)
 
@@ -59,6 +65,15 @@ const Tensor& tensor(PyObject* o, const char* name) {
 void no_gradient(const char* call, const Tensor& t) {
   TORCH_CHECK_VALUE(!(t.requires_grad() && at::GradMode::is_enabled()), call,
                     " has no gradient: call it under torch.no_grad()");
+}
+
+// k_pages, v_pages, k_scales, v_scales; call: null if it asks for nothing that a gradient could be of.
+void no_gradients(const char* call, PyObject* const* a) {
+  const char* names[4] = {"k_pages", "v_pages", "k_scales", "v_scales"};
+  for (int i = 0; i < 4; ++i) {
+    const Tensor& t = tensor(a[i], names[i]);
+    if (call) no_gradient(call, t);
+  }
 }
 
 // The stream to launch on, after checking that `device` is the current one.
@@ -144,13 +159,18 @@ struct Cache {
   const int32_t* table = nullptr;
   void *k, *v;
   at::ScalarType type;
-  Cache(PyObject* k_pages, PyObject* v_pages, PyObject* page_table) : device(at::kCPU) {
+  Cache(PyObject* k_pages, PyObject* v_pages, PyObject* page_table)
+      : Cache(k_pages, v_pages, page_table, tensor(k_pages, "k_pages").scalar_type()) {
+    TORCH_CHECK_VALUE(tensor(v_pages, "v_pages").scalar_type() == type, "k_pages and v_pages must share the dtype");
+  }
+
+ protected:
+  // rows: the dtype of the rows outside the cache, which is the pools' own unless those hold 8 bits
+  Cache(PyObject* k_pages, PyObject* v_pages, PyObject* page_table, at::ScalarType rows) : device(at::kCPU), type(rows) {
     const Tensor &kt = tensor(k_pages, "k_pages"), &vt = tensor(v_pages, "v_pages");
     TORCH_CHECK_VALUE(kt.dim() == 4 && vt.sizes() == kt.sizes(),
                       "k_pages and v_pages must be [pages, kv_heads, page_rows, d] tensors of one shape");
-    type = kt.scalar_type();
     TORCH_CHECK_TYPE(type == at::kBFloat16 || type == at::kFloat, "unsupported dtype ", type);
-    TORCH_CHECK_VALUE(vt.scalar_type() == type, "k_pages and v_pages must share the dtype");
     device = kt.device();
     TORCH_CHECK_VALUE(device.is_cuda() && vt.device() == device, "the pools must be on one CUDA device");
     const RowStrides s(kt);
@@ -166,6 +186,28 @@ struct Cache {
     k = kt.data_ptr();
     v = vt.data_ptr();
     if (page_table != Py_None) table = set_table(&c, tensor(page_table, "page_table"), device);
+  }
+};
+
+// Two pools in 8 bits with their scales; `rows` is the dtype of the rows outside.
+struct CacheE4m3 : Cache {
+  int32_t block_rows;
+  float *k_scales, *v_scales;
+  CacheE4m3(PyObject* k_pages, PyObject* v_pages, PyObject* ks, PyObject* vs, PyObject* page_table, at::ScalarType rows)
+      : Cache(k_pages, v_pages, page_table, rows) {
+    for (PyObject* p : {k_pages, v_pages})
+      TORCH_CHECK_TYPE(tensor(p, "pools").scalar_type() == at::kFloat8_e4m3fn, "k_pages and v_pages must be float8_e4m3fn");
+    const Tensor &kt = tensor(ks, "k_scales"), &vt = tensor(vs, "v_scales");
+    TORCH_CHECK_VALUE(kt.dim() == 3 && kt.size(0) == c.num_pages && kt.size(1) == c.H_kv && kt.size(2) > 0 &&
+                          c.page_rows % kt.size(2) == 0 && vt.sizes() == kt.sizes(),
+                      "k_scales and v_scales must be [", c.num_pages, ", ", c.H_kv, ", blocks] tensors, with blocks that divide ",
+                      c.page_rows);
+    for (const Tensor* t : {&kt, &vt})
+      TORCH_CHECK_VALUE(t->scalar_type() == at::kFloat && t->is_contiguous() && t->device() == device,
+                        "k_scales and v_scales must be contiguous float32 tensors on ", device);
+    block_rows = c.page_rows / (int32_t)kt.size(2);
+    k_scales = static_cast<float*>(kt.data_ptr());
+    v_scales = static_cast<float*>(vt.data_ptr());
   }
 };
 
@@ -235,38 +277,35 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
   return r;
 }
 
-// q, k_pages, v_pages, page_table, lengths, scale, workspace, out, stream
-PyObject* decode(PyObject* const* a, Py_ssize_t n) {
-  want(n, 9);
-  const Tensor& q = tensor(a[0], "q");
-  no_gradient("attention_decode", q);
-  no_gradient("attention_decode", tensor(a[1], "k_pages"));
-  no_gradient("attention_decode", tensor(a[2], "v_pages"));
-  Cache cache(a[1], a[2], a[3]);
+// The rest of both decode calls.  a: lengths, scale, workspace, out, stream.  bytes(heads) is the
+// workspace's size, launch(...) the library's call.
+template <class Bytes, class Launch>
+PyObject* decode_over(const char* what, const Tensor& q, const Cache& cache, PyObject* const* a, Bytes&& bytes_for,
+                      Launch&& launch) {
   const fa_cache& c = cache.c;
   TORCH_CHECK_VALUE(q.dim() == 4 && q.size(0) == c.S && q.size(2) == 1 && q.size(3) == c.d, "q must be a [", c.S,
                     ", heads, 1, ", c.d, "] tensor");
   TORCH_CHECK_VALUE(q.scalar_type() == cache.type && q.device() == cache.device,
                     "q must have the dtype and device of the pools");
-  const Stream stream(cache.device, a[8]);
-  const int32_t* lengths = ints(a[4], "lengths", {c.S}, cache.device);
+  const Stream stream(cache.device, a[4]);
+  const int32_t* lengths = ints(a[0], "lengths", {c.S}, cache.device);
   const int32_t heads = as_int32(q.size(1), "the number of heads");
   double scale = 1.0 / std::sqrt((double)c.d);
-  if (a[5] != Py_None) {
-    scale = PyFloat_AsDouble(a[5]);
+  if (a[1] != Py_None) {
+    scale = PyFloat_AsDouble(a[1]);
     if (PyErr_Occurred()) throw python_error();
   }
   const RowStrides qs(q);
   Tensor o, L, workspace;
-  if (a[7] == Py_None) {
+  if (a[3] == Py_None) {
     o = stream.result(q.sizes(), cache.type);
     L = stream.result(q.sizes().slice(0, 3), at::kFloat);
   } else {
-    TORCH_CHECK_TYPE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 2, "out must be a tuple (o, L)");
-    o = tensor(PyTuple_GET_ITEM(a[7], 0), "out[0]");
-    L = tensor(PyTuple_GET_ITEM(a[7], 1), "out[1]");
-    no_gradient("attention_decode", o);
-    no_gradient("attention_decode", L);
+    TORCH_CHECK_TYPE(PyTuple_Check(a[3]) && PyTuple_GET_SIZE(a[3]) == 2, "out must be a tuple (o, L)");
+    o = tensor(PyTuple_GET_ITEM(a[3], 0), "out[0]");
+    L = tensor(PyTuple_GET_ITEM(a[3], 1), "out[1]");
+    no_gradient(what, o);
+    no_gradient(what, L);
     TORCH_CHECK_VALUE(o.sizes() == q.sizes() && o.scalar_type() == cache.type && o.device() == cache.device,
                       "out[0] must have the shape, dtype and device of q");
     TORCH_CHECK_VALUE(L.sizes() == q.sizes().slice(0, 3) && L.scalar_type() == at::kFloat &&
@@ -275,9 +314,9 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     stream.lend(o);
     stream.lend(L);
   }
-  size_t bytes = g_fa.workspace_bytes(&c, heads);
-  if (a[6] != Py_None) {
-    workspace = tensor(a[6], "workspace");
+  size_t bytes = bytes_for(heads);
+  if (a[2] != Py_None) {
+    workspace = tensor(a[2], "workspace");
     TORCH_CHECK_VALUE(workspace.device() == cache.device && workspace.is_contiguous(),
                       "workspace must be a contiguous tensor on ", cache.device);
     bytes = workspace.nbytes();
@@ -285,11 +324,45 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   } else if (bytes > 0) {
     workspace = stream.empty({(int64_t)bytes}, at::kByte);
   }
-  const RowStrides os(o);
-  call("fa_decode", g_fa.decode, &c, heads, (float)scale, (const void*)q.data_ptr(), qs.s0, qs.s1,
-       (const void*)cache.k, (const void*)cache.v, cache.table, lengths, o.data_ptr(), os.s0, os.s1,
-       static_cast<float*>(L.data_ptr()), workspace.defined() ? workspace.data_ptr() : nullptr, bytes, stream.raw);
+  launch(heads, (float)scale, qs, lengths, o, RowStrides(o), static_cast<float*>(L.data_ptr()),
+         workspace.defined() ? workspace.data_ptr() : nullptr, bytes, stream.raw);
   return pair(o, L);
+}
+
+// q, k_pages, v_pages, page_table, lengths, scale, workspace, out, stream
+PyObject* decode(PyObject* const* a, Py_ssize_t n) {
+  want(n, 9);
+  const Tensor& q = tensor(a[0], "q");
+  no_gradient("attention_decode", q);
+  no_gradient("attention_decode", tensor(a[1], "k_pages"));
+  no_gradient("attention_decode", tensor(a[2], "v_pages"));
+  const Cache cache(a[1], a[2], a[3]);
+  return decode_over(
+      "attention_decode", q, cache, a + 4, [&](int32_t heads) { return g_fa.workspace_bytes(&cache.c, heads); },
+      [&](int32_t heads, float scale, const RowStrides& qs, const int32_t* lengths, const Tensor& o,
+          const RowStrides& os, float* L, void* workspace, size_t bytes, void* stream) {
+        call("fa_decode", g_fa.decode, &cache.c, heads, scale, (const void*)q.data_ptr(), qs.s0, qs.s1,
+             (const void*)cache.k, (const void*)cache.v, cache.table, lengths, o.data_ptr(), os.s0, os.s1, L, workspace,
+             bytes, stream);
+      });
+}
+
+// q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale, workspace, out, stream
+PyObject* decode_e4m3(PyObject* const* a, Py_ssize_t n) {
+  want(n, 11);
+  const char* what = "attention_decode_e4m3";
+  const Tensor& q = tensor(a[0], "q");
+  no_gradient(what, q);
+  no_gradients(what, a + 1);
+  const CacheE4m3 cache(a[1], a[2], a[3], a[4], a[5], q.scalar_type());
+  return decode_over(
+      what, q, cache, a + 6, [&](int32_t heads) { return g_fa.workspace_bytes_e4m3(&cache.c, heads); },
+      [&](int32_t heads, float scale, const RowStrides& qs, const int32_t* lengths, const Tensor& o,
+          const RowStrides& os, float* L, void* workspace, size_t bytes, void* stream) {
+        call("fa_decode_e4m3", g_fa.decode_e4m3, &cache.c, cache.block_rows, heads, scale, (const void*)q.data_ptr(), qs.s0,
+             qs.s1, (const void*)cache.k, (const void*)cache.v, (const float*)cache.k_scales,
+             (const float*)cache.v_scales, cache.table, lengths, o.data_ptr(), os.s0, os.s1, L, workspace, bytes, stream);
+      });
 }
 
 // k, v, k_pages, v_pages, page_table, start, counts, stream
@@ -315,6 +388,89 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(s == RowStrides(v), "k and v must share their strides");
   call("fa_cache_append", g_fa.append, &c, as_int32(k.size(2), "the number of rows"), (const void*)k.data_ptr(),
        (const void*)v.data_ptr(), s.s0, s.s1, s.s2, cache.k, cache.v, cache.table, start, counts, stream.raw);
+  Py_RETURN_NONE;
+}
+
+// k, v, k_pages, v_pages, k_scales, v_scales, page_table, start, counts, stream
+PyObject* append_e4m3(PyObject* const* a, Py_ssize_t n) {
+  want(n, 10);
+  const char* what = "cache_append_e4m3";
+  const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  no_gradient(what, k);
+  no_gradient(what, v);
+  no_gradients(what, a + 2);
+  const CacheE4m3 cache(a[2], a[3], a[4], a[5], a[6], k.scalar_type());
+  const fa_cache& c = cache.c;
+  TORCH_CHECK_VALUE(k.dim() == 4 && k.size(0) == c.S && k.size(1) == c.H_kv && k.size(3) == c.d && v.sizes() == k.sizes(),
+                    "k and v must be [", c.S, ", ", c.H_kv, ", rows, ", c.d, "] tensors");
+  TORCH_CHECK_VALUE(v.scalar_type() == cache.type && k.device() == cache.device && v.device() == cache.device,
+                    "k and v must share the dtype and be on the device of the pools");
+  const Stream stream(cache.device, a[9]);
+  const int32_t* start = ints(a[7], "start", {c.S}, cache.device);
+  const int32_t* counts = a[8] == Py_None ? nullptr : ints(a[8], "counts", {c.S}, cache.device);
+  if (k.size(2) == 0) Py_RETURN_NONE;
+  const RowStrides s(k);
+  TORCH_CHECK_VALUE(s == RowStrides(v), "k and v must share their strides");
+  call("fa_cache_append_e4m3", g_fa.append_e4m3, &c, cache.block_rows, as_int32(k.size(2), "the number of rows"),
+       (const void*)k.data_ptr(), (const void*)v.data_ptr(), s.s0, s.s1, s.s2, cache.k, cache.v, cache.k_scales,
+       cache.v_scales, cache.table, start, counts, stream.raw);
+  Py_RETURN_NONE;
+}
+
+// k_pages, v_pages, k_scales, v_scales, page_table, rows, start, counts, dtype, out, stream
+PyObject* read_e4m3(PyObject* const* a, Py_ssize_t n) {
+  want(n, 11);
+  const char* what = "cache_read_e4m3";
+  no_gradients(what, a);
+  TORCH_CHECK_TYPE(THPDtype_Check(a[8]), "dtype must be a torch.dtype");
+  const auto type = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+  const CacheE4m3 cache(a[0], a[1], a[2], a[3], a[4], type);
+  const fa_cache& c = cache.c;
+  const long rows = PyLong_AsLong(a[5]);
+  if (rows == -1 && PyErr_Occurred()) throw python_error();
+  TORCH_CHECK_VALUE(rows >= 0, "the number of rows is out of range");
+  const Stream stream(cache.device, a[10]);
+  const int32_t* start = a[6] == Py_None ? nullptr : ints(a[6], "start", {c.S}, cache.device);
+  const int32_t* counts = a[7] == Py_None ? nullptr : ints(a[7], "counts", {c.S}, cache.device);
+  const int64_t shape[4] = {c.S, c.H_kv, as_int32(rows, "the number of rows"), c.d};
+  Tensor x[2];
+  if (a[9] == Py_None) {
+    // the library refuses so many rows, and only then: no memory is asked for that it would not fill
+    if ((int64_t)c.S * c.H_kv * rows >= int64_t(1) << 31) throw Failed{FA_ERR_UNSUPPORTED, "fa_cache_read_e4m3"};
+    for (Tensor& t : x) t = stream.result(shape, type);
+  } else {
+    TORCH_CHECK_TYPE(PyTuple_Check(a[9]) && PyTuple_GET_SIZE(a[9]) == 2, "out must be a tuple (k, v)");
+    for (int i = 0; i < 2; ++i) {
+      x[i] = tensor(PyTuple_GET_ITEM(a[9], i), "out");
+      no_gradient(what, x[i]);
+      TORCH_CHECK_VALUE(x[i].sizes() == at::IntArrayRef(shape) && x[i].scalar_type() == type && x[i].device() == cache.device,
+                        "out must be ", type, " tensors of shape ", at::IntArrayRef(shape), " on ", cache.device);
+      stream.lend(x[i]);
+    }
+  }
+  if (rows > 0) {
+    const RowStrides s(x[0]);
+    TORCH_CHECK_VALUE(s == RowStrides(x[1]), "the tensors of out must share their strides");
+    call("fa_cache_read_e4m3", g_fa.read_e4m3, &c, cache.block_rows, (int32_t)rows, (const void*)cache.k,
+         (const void*)cache.v, (const float*)cache.k_scales, (const float*)cache.v_scales, cache.table, start, counts,
+         x[0].data_ptr(), x[1].data_ptr(), s.s0, s.s1, s.s2, stream.raw);
+  }
+  return pair(x[0], x[1]);
+}
+
+// k_pages, v_pages, k_scales, v_scales, moves, count, stream
+PyObject* copy_e4m3(PyObject* const* a, Py_ssize_t n) {
+  want(n, 7);
+  no_gradients("cache_copy_pages_e4m3", a);
+  // there are no rows outside: the dtype that goes with every head dim
+  const CacheE4m3 cache(a[0], a[1], a[2], a[3], Py_None, at::kFloat);
+  const Tensor& moves = tensor(a[4], "moves");
+  TORCH_CHECK_VALUE(moves.dim() == 2, "moves must be an [n, 3] tensor");
+  const Stream stream(cache.device, a[6]);
+  const int32_t* m = ints(a[4], "moves", {moves.size(0), 3}, cache.device);
+  const int32_t* count = a[5] == Py_None ? nullptr : ints(a[5], "count", {1}, cache.device);
+  call("fa_cache_copy_pages_e4m3", g_fa.copy_e4m3, &cache.c, cache.block_rows, as_int32(moves.size(0), "the number of moves"),
+       m, count, cache.k, cache.v, cache.k_scales, cache.v_scales, stream.raw);
   Py_RETURN_NONE;
 }
 
@@ -407,6 +563,18 @@ PyObject* describe(PyObject* const* a, Py_ssize_t n) {
                        (long long)c.table_stride);
 }
 
+// k_pages, v_pages, k_scales, v_scales, page_table, dtype: the fields of fa_cache, then block_rows
+PyObject* describe_e4m3(PyObject* const* a, Py_ssize_t n) {
+  want(n, 6);
+  no_gradients(nullptr, a);
+  TORCH_CHECK_TYPE(THPDtype_Check(a[5]), "dtype must be a torch.dtype");
+  const CacheE4m3 cache(a[0], a[1], a[2], a[3], a[4], reinterpret_cast<THPDtype*>(a[5])->scalar_type);
+  const fa_cache& c = cache.c;
+  return Py_BuildValue("(iiiiiiiiLLLL)i", c.num_pages, c.page_rows, c.H_kv, c.d, c.dtype, c.S, c.max_pages, c.reserved,
+                       (long long)c.stride_page, (long long)c.stride_h, (long long)c.stride_n,
+                       (long long)c.table_stride, cache.block_rows);
+}
+
 // FaError, then the addresses of the entry points in the order of Entries
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   constexpr Py_ssize_t kEntries = sizeof(Entries) / sizeof(void*);
@@ -426,6 +594,9 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {FA_METHOD("bind", bind),       FA_METHOD("describe", describe), FA_METHOD("decode", decode),
                            FA_METHOD("append", append),   FA_METHOD("copy", copy),         FA_METHOD("extend", extend),
                            FA_METHOD("fork", fork),       FA_METHOD("free", release),      FA_METHOD("compact", compact),
+                           FA_METHOD("decode_e4m3", decode_e4m3), FA_METHOD("append_e4m3", append_e4m3),
+                           FA_METHOD("read_e4m3", read_e4m3), FA_METHOD("copy_e4m3", copy_e4m3),
+                           FA_METHOD("describe_e4m3", describe_e4m3),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, g_methods};
 

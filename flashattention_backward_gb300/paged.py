@@ -17,6 +17,17 @@ a table of -1, lengths of 0 and refs of 0::
     fa.cache_append(k_new, v_new, k_pages, v_pages, table, start, n_new)
     o, L = fa.attention_decode(q, k_pages, v_pages, table, lengths)
 
+The same cache can be held in 8 bits: ``float8_e4m3fn`` pools and, for each, a
+contiguous float32 tensor of scales ``[pages, kv_heads, blocks]``, one for every
+``page_rows / blocks`` rows of a page and head (``blocks = page_rows``: one a
+token, ``blocks = 1``: one a page).  :func:`cache_append_e4m3` quantises rows as
+it writes them and sets the scales, which are powers of two and need no value
+before that; a stored value times its scale is what the others read.  ``q`` and
+the rows outside stay bf16 or fp32, the page calls are the same::
+
+    fa.cache_append_e4m3(k_new, v_new, k_pages, v_pages, k_scales, v_scales, table, start, n_new)
+    o, L = fa.attention_decode_e4m3(q, k_pages, v_pages, k_scales, v_scales, table, lengths)
+
 Nothing here waits for the GPU or reads back from it, so a whole step can be
 captured into a graph.  What is wrong on the device (a page or index out of
 range, too few free pages) is never followed; it is recorded in the device
@@ -46,7 +57,8 @@ from . import _build
 
 # the library's entry points, in the order in which the binding takes them
 _ENTRIES = ("decode_workspace_bytes", "decode", "cache_append", "cache_copy_pages", "pages_extend", "pages_fork",
-            "pages_free", "pages_compact")
+            "pages_free", "pages_compact", "decode_e4m3_workspace_bytes", "decode_e4m3", "cache_append_e4m3",
+            "cache_read_e4m3", "cache_copy_pages_e4m3")
 _i32, _i64, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
 
@@ -80,8 +92,15 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.fa_pages_fork.argtypes = [P, _i32] + [_vp] * 7
     lib.fa_pages_free.argtypes = [P, _i32] + [_vp] * 5
     lib.fa_pages_compact.argtypes = [P] + [_vp] * 8
+    lib.fa_decode_e4m3_workspace_bytes.argtypes = [P, _i32]
+    lib.fa_decode_e4m3_workspace_bytes.restype = _sz
+    lib.fa_decode_e4m3.argtypes = [P, _i32, _i32, ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                   _i64, _vp, _vp, _sz, _vp]
+    lib.fa_cache_append_e4m3.argtypes = [P, _i32, _i32, _vp, _vp, _i64, _i64, _i64] + [_vp] * 8
+    lib.fa_cache_read_e4m3.argtypes = [P, _i32, _i32] + [_vp] * 9 + [_i64, _i64, _i64, _vp]
+    lib.fa_cache_copy_pages_e4m3.argtypes = [P, _i32, _i32] + [_vp] * 7
     for name in ("decode", "cache_append", "cache_copy_pages", "pages_extend", "pages_fork", "pages_free",
-                 "pages_compact"):
+                 "pages_compact", "decode_e4m3", "cache_append_e4m3", "cache_read_e4m3", "cache_copy_pages_e4m3"):
         getattr(lib, "fa_" + name).restype = ctypes.c_int
 
 
@@ -168,6 +187,65 @@ def cache_copy_pages(k_pages, v_pages, moves, count=None, stream=None, check_sta
     (_EXT or _binding()).copy(k_pages, v_pages, moves, count, _raw(stream))
     if check_status:
         _status("fa_cache_copy_pages", stream)
+
+
+def cache_for_e4m3(k_pages, v_pages, k_scales, v_scales, page_table=None, dtype=torch.bfloat16):
+    """Descriptor of two pools in 8 bits and, if given, the page table over
+    them, with the rows that share a scale; ``dtype`` is that of the queries
+    and of the rows outside the cache."""
+    fields, block_rows = _binding().describe_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, dtype)
+    return FaCache(*fields), block_rows
+
+
+def fa_decode_e4m3_workspace_bytes(c: FaCache, heads: int) -> int:
+    return int(_pkg.load_library().fa_decode_e4m3_workspace_bytes(ctypes.byref(c), int(heads)))
+
+
+def attention_decode_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale: Optional[float] = None,
+                          workspace=None, out=None, stream=None, check_status: bool = False):
+    """:func:`attention_decode` over pools in 8 bits: every stored value counts
+    as itself times its block's scale.  ``q``, ``o`` are bf16 or fp32;
+    ``workspace`` has :func:`fa_decode_e4m3_workspace_bytes`."""
+    got = (_EXT or _binding()).decode_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, lengths, scale, workspace,
+                                           None if out is None else tuple(out), _raw(stream))
+    if check_status:
+        _status("fa_decode_e4m3", stream)
+    return got
+
+
+def cache_append_e4m3(k, v, k_pages, v_pages, k_scales, v_scales, page_table, start, counts=None, stream=None,
+                      check_status: bool = False) -> None:
+    """:func:`cache_append` into pools in 8 bits.  The rows (bf16 or fp32) are
+    rounded to the nearest e4m3 number of their block's scale, the smallest
+    power of two that takes the largest finite value to at most 448; what is
+    not finite becomes NaN.  In a block that holds rows before ``start[s]``
+    the scale can only grow, and then those rows are rounded once more.  Rows
+    are written from front to back: those of a touched block behind the new
+    ones hold nothing afterwards."""
+    (_EXT or _binding()).append_e4m3(k, v, k_pages, v_pages, k_scales, v_scales, page_table, start, counts, _raw(stream))
+    if check_status:
+        _status("fa_cache_append_e4m3", stream)
+
+
+def cache_read_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, rows: int, start=None, counts=None,
+                    dtype=torch.bfloat16, out=None, stream=None, check_status: bool = False):
+    """Rows of pools in 8 bits as dense k, v [S, kv_heads, ``rows``, d] of
+    ``dtype``: row i is row ``start[s] + i`` of sequence s (``i`` without
+    ``start``) for i < ``counts[s]`` (all rows without ``counts``) and 0 behind that, as the forward
+    pass over cached tokens takes them.  ``out`` may pass (k, v) to write to."""
+    got = (_EXT or _binding()).read_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, rows, start, counts, dtype,
+                                         None if out is None else tuple(out), _raw(stream))
+    if check_status:
+        _status("fa_cache_read_e4m3", stream)
+    return got
+
+
+def cache_copy_pages_e4m3(k_pages, v_pages, k_scales, v_scales, moves, count=None, stream=None,
+                          check_status: bool = False) -> None:
+    """:func:`cache_copy_pages` for pools in 8 bits: rows and their scales."""
+    (_EXT or _binding()).copy_e4m3(k_pages, v_pages, k_scales, v_scales, moves, count, _raw(stream))
+    if check_status:
+        _status("fa_cache_copy_pages_e4m3", stream)
 
 
 def pages_extend(page_table, lengths, refs, n_new, page_rows: int, stream=None, check_status: bool = False):

@@ -340,6 +340,68 @@ fa_status fa_cache_append(const fa_cache* c, int32_t rows, const void* K, const 
 fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_t* moves, const int32_t* count,
                               void* K_pages, void* V_pages, void* stream);
 
+/* A cache in 8 bits: rows that are quantised as they are written.
+ * ---------------------------------------------------------------
+ * The pools hold e4m3 numbers (4 exponent and 3 mantissa bits, up to 448, no
+ * infinities), a byte each, and two float32 arrays hold a scale, a power of two,
+ * for each block of block_rows rows of a page and head: a stored value times
+ * its block's scale is the value it stands for.  block_rows divides page_rows:
+ * 1 is a scale a row, page_rows one a page and head.  The scales of a pool are dense,
+ * [num_pages, H_kv, page_rows / block_rows]; what stands there before a block's
+ * first row is written does not matter.
+ * fa_cache says the rest: its dtype is that of Q, O and the rows outside the
+ * cache, its strides are those of the e4m3 pools, in elements, which are bytes, and
+ * multiples of 16.  dtype, d and limits as above.  The page calls below are the same
+ * for every kind of cache. */
+
+/* New rows, quantised, into their pages: which go where, and which are dropped,
+ * is as for fa_cache_append, with FA_ERR_PAGES in the same cases.  For each
+ * block that gets rows, with t the largest finite |x| of its new rows,
+ *   need  = the smallest power of two with t <= 448 need, 2^-126 at least
+ *   scale = max(need, the block's scale), if rows of the block stand before
+ *           start[s], else need.
+ * The new rows become x / scale, rounded to the nearest e4m3 number, ties to
+ * even; what is not finite becomes NaN.  Where the scale grows, the rows before
+ * are divided by what it grew by and rounded once more: exact, but for
+ * numbers that end below 2^-6.  Rows of a touched block behind the new ones are
+ * taken to hold nothing.
+ * rows >= 1, S * H_kv * rows < 2^31.  Neither the pools nor the scales of K and
+ * V may be the same memory. */
+fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K, const void* V,
+                               int64_t stride_s, int64_t stride_h, int64_t stride_n, void* K_pages, void* V_pages,
+                               float* K_scales, float* V_scales, const int32_t* page_table, const int32_t* start,
+                               const int32_t* counts, void* stream);
+
+/* Rows read back: K[s, g, i] and V[s, g, i] ([S, H_kv, rows, d] of c->dtype with
+ * element strides (stride_s, stride_h, stride_n), byte strides multiples of 16)
+ * become row start[s] + i of sequence s, for i < counts[s], and 0 for the other
+ * i.  start NULL: 0; counts NULL: all `rows`; counts outside 0 ... rows are
+ * cut to it and a negative start counts as no rows (FA_ERR_PAGES in both cases); a
+ * row whose page is out of range or that lies behind the table is 0 (FA_ERR_PAGES).
+ * rows >= 1, S * H_kv * rows < 2^31.  K and V may not be the same memory. */
+fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K_pages,
+                             const void* V_pages, const float* K_scales, const float* V_scales,
+                             const int32_t* page_table, const int32_t* start, const int32_t* counts, void* K, void* V,
+                             int64_t stride_s, int64_t stride_h, int64_t stride_n, void* stream);
+
+/* fa_cache_copy_pages for pools in 8 bits: the blocks that hold rows copied bring
+ * their scales along. */
+fa_status fa_cache_copy_pages_e4m3(const fa_cache* c, int32_t block_rows, int32_t max_moves, const int32_t* moves,
+                                   const int32_t* count, void* K_pages, void* V_pages, float* K_scales,
+                                   float* V_scales, void* stream);
+
+/* fa_decode over a cache in 8 bits: with k and v the values that the stored ones
+ * stand for, the same formulas, limits and workspace rules, and the same treatment
+ * of lengths, pages and empty sequences.  Scales are positive and finite.
+ * O is rounded once, to dtype; sums, scores and weights are held to 22 bits or
+ * more.  A NaN among the visible rows makes NaN of what it goes into. */
+size_t fa_decode_e4m3_workspace_bytes(const fa_cache* c, int32_t H);
+fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float scale, const void* Q,
+                         int64_t q_stride_s, int64_t q_stride_h, const void* K_pages, const void* V_pages,
+                         const float* K_scales, const float* V_scales, const int32_t* page_table,
+                         const int32_t* lengths, void* O, int64_t o_stride_s, int64_t o_stride_h, float* L,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* The page calls: whole numbers on the device, no host round trip, so that
  * they can stand in a captured graph between the calls above.  A sequence
  * with n rows has ceil(n / page_rows) pages.  Free pages are taken lowest
