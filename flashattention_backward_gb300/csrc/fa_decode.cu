@@ -74,16 +74,6 @@ struct Mma {
   static constexpr int kSmem = kRing + kExchange;
 };
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-               : "r"(at));
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -395,13 +385,9 @@ cudaError_t launch_bf16(const Cut& k, const DecodeParams& a, cudaStream_t s) {
   return k.part_heads == 8 ? launch_mma<D, 1>(k, a, s) : launch_mma<D, 2>(k, a, s);
 }
 
-// H against the cache; the strides of Q and O are checked by the entry point.
-fa_status check_heads(const fa_cache* c, int32_t H) {
+fa_status check(const fa_cache* c, int32_t H) {
   const fa_status st = check_cache(c);
-  if (st != FA_OK) return st;
-  if (H < 1 || H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
-  if ((int64_t)c->S * H > (1 << 24) || H / c->H_kv > kMostHeads) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
+  return st == FA_OK ? check_heads(c, H) : st;
 }
 
 }  // namespace
@@ -422,10 +408,7 @@ cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodePara
 extern "C" {
 
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t H) {
-  if (fa::check_heads(c, H) != FA_OK) return 0;
-  const fa::Cut k = fa::cut_of(*c, H);
-  if (k.cluster > 0 || k.most_tiles <= 1) return 0;  // no parts, or none in global memory
-  return (size_t)k.parts() * k.part_heads * (sizeof(float2) + sizeof(float) * c->d);
+  return fa::check(c, H) == FA_OK ? fa::workspace_of(fa::cut_of(*c, H), c->d) : 0;
 }
 
 fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, int64_t q_stride_s, int64_t q_stride_h,
@@ -433,48 +416,18 @@ fa_status fa_decode(const fa_cache* c, int32_t H, float scale, const void* Q, in
                     void* O, int64_t o_stride_s, int64_t o_stride_h, float* L, void* workspace,
                     size_t workspace_bytes, void* stream) {
   fa::NvtxRange range("fa_decode");
-  const fa_status st = fa::check_heads(c, H);
+  fa_status st = fa::check(c, H);
   if (st != FA_OK) return st;
-  const int es = fa::elem_size(c->dtype);
-  if (!(scale > 0.f) || !isfinite(scale * fa::kLog2e) || O == Q || !fa::aligned16(Q) || !fa::aligned16(K_pages) || !fa::aligned16(V_pages) ||
-      !fa::aligned16(O) || !fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(L) ||
-      !fa::good_stride(q_stride_s, c->d, es, false) || !fa::good_stride(q_stride_h, c->d, es, false) ||
-      !fa::good_stride(o_stride_s, c->d, es, true) || !fa::good_stride(o_stride_h, c->d, es, true))
-    return FA_ERR_INVALID_ARG;
-  const size_t need = fa_decode_workspace_bytes(c, H);
-  if (need > 0 && (!fa::aligned16(workspace) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  const fa::DecodeCall x = {c, H, scale, Q, q_stride_s, q_stride_h, K_pages, V_pages, page_table, lengths,
+                            O, o_stride_s, o_stride_h, L, workspace, workspace_bytes};
   const fa::Cut k = fa::cut_of(*c, H);
+  const size_t need = fa::workspace_of(k, c->d);
+  st = fa::check_call(x, need);
+  if (st != FA_OK) return st;
   fa::DecodeParams a;
   a.status = fa::device_status_word();
   if (!a.status) return FA_ERR_CUDA;
-  a.Q = (const char*)Q;
-  a.K = (const char*)K_pages;
-  a.V = (const char*)V_pages;
-  a.O = (char*)O;
-  a.L = L;
-  a.table = page_table;
-  a.lengths = lengths;
-  a.part_o = (float*)workspace;
-  a.part_ml = (float2*)(a.part_o + (need > 0 ? (size_t)k.parts() * k.part_heads * c->d : 0));
-  a.page_rows = fa::FastDiv(c->page_rows);
-  a.S = c->S;
-  a.H = H;
-  a.group = H / c->H_kv;
-  a.split = k.split;
-  a.piece_heads = k.piece_heads;
-  a.items = c->H_kv;
-  a.num_pages = c->num_pages;
-  a.max_pages = c->max_pages;
-  a.cap = (int)fa::cache_rows(*c);
-  a.table_stride = c->table_stride;
-  a.qs = q_stride_s * es;
-  a.qh = q_stride_h * es;
-  a.os = o_stride_s * es;
-  a.oh = o_stride_h * es;
-  a.pp = c->stride_page * es;
-  a.ph = c->stride_h * es;
-  a.pn = c->stride_n * es;
-  a.scale2 = scale * fa::kLog2e;
+  fa::fill(x, k, need, fa::elem_size(c->dtype), &a);
   const cudaStream_t s = (cudaStream_t)stream;
   return fa::status_of(c->dtype == FA_BF16 ? fa::launch_decode_bf16(*c, k, a, s) : fa::launch_decode_fp32(*c, k, a, s));
 }

@@ -284,6 +284,18 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// ------------------------------------------------------ shared-memory reads
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(at));
+}
+
 // A warp's copies of its rows of each tile, ahead of their use: rows warp *
 // kRows ... of the tile, K then V, kPieces pieces of 16 bytes each, kPitch
 // bytes apart, in a ring of kStages in shared memory.
@@ -576,14 +588,14 @@ inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 25
 // runs, 9.1 with 16 blocks of 4 tiles and 12.6 with 8 of 8; 8 of 512, 32 heads on 8,
 // 10.2 in runs and 7.7 with 4 blocks of 2 tiles.
 constexpr int kClusterTiles = 2;
-inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
+// an_sm: blocks of the kernel that an SM holds.
+inline int cluster_of(int an_sm, int64_t items, int64_t most_tiles) {
   // clusters that the GPU holds of each size, for each block an SM, as a GB300 of 152 SMs answers when asked: a cluster
   // stays inside a GPC.  Written down, because the workspace's size goes by this too, which is asked for without a GPU;
   // one that holds other numbers of them computes the same, in more or fewer waves.
   struct {
     int blocks, fit;
   } sizes[] = {{kMostBlocks, 7}, {8, 15}, {4, 36}, {2, 76}, {1, 152}};
-  const int an_sm = blocks_an_sm(c.dtype == FA_BF16, c.d);
   for (const auto& z : sizes) {
     if (items > (int64_t)z.fit * an_sm || z.blocks / 2 >= most_tiles) continue;  // too many, or blocks without a tile
     return most_tiles <= (int64_t)z.blocks * kClusterTiles ? z.blocks : 0;
@@ -591,19 +603,30 @@ inline int cluster_of(const fa_cache& c, int64_t items, int64_t most_tiles) {
   return 0;
 }
 
-inline Cut cut_of(const fa_cache& c, int H) {
+// A group of query heads in even pieces of at most `most`.
+inline Cut pieces_of(int group, int most) {
   Cut k;
-  const int group = H / c.H_kv;
-  k.split = (int)ceil_div(group, c.dtype == FA_BF16 ? 16 : 8);
+  k.split = (int)ceil_div(group, most);
   k.piece_heads = (int)ceil_div(group, k.split);
-  if (c.dtype == FA_BF16)
-    k.part_heads = k.piece_heads <= 8 ? 8 : 16;
-  else
-    k.part_heads = k.piece_heads == 1 ? 1 : k.piece_heads <= 4 ? 4 : 8;
-  k.most_tiles = ceil_div(cache_rows(c), tile_rows(c));
-  k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
-  k.cluster = cluster_of(c, (int64_t)c.S * c.H_kv * k.split, k.most_tiles);
+  k.part_heads = k.piece_heads <= 8 ? 8 : 16;
   return k;
+}
+inline Cut cut_tiles(Cut k, const fa_cache& c, int tile, int an_sm) {
+  k.most_tiles = ceil_div(cache_rows(c), tile);
+  k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
+  k.cluster = cluster_of(an_sm, (int64_t)c.S * c.H_kv * k.split, k.most_tiles);
+  return k;
+}
+
+inline Cut cut_of(const fa_cache& c, int H) {
+  Cut k = pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8);
+  if (c.dtype != FA_BF16) k.part_heads = k.piece_heads == 1 ? 1 : k.piece_heads <= 4 ? 4 : 8;
+  return cut_tiles(k, c, tile_rows(c), blocks_an_sm(c.dtype == FA_BF16, c.d));
+}
+// The workspace's size: no parts where there are clusters, none in global memory where items are a tile.
+inline size_t workspace_of(const Cut& k, int d) {
+  if (k.cluster > 0 || k.most_tiles <= 1) return 0;
+  return (size_t)k.parts() * k.part_heads * (sizeof(float2) + sizeof(float) * d);
 }
 
 // The runs that the lengths can lead to at most.  Sets a->resident.
@@ -652,9 +675,10 @@ inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int
 }
 
 // Launches `alone` with a cluster an item, or `kernel` with a block a run and the join.
-template <class T, int D, int kTile>
-cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodeParams), void (*alone)(DecodeParams),
-                          int smem, std::atomic<int>* known, std::atomic<int>* known_alone, cudaStream_t s) {
+// P: DecodeParams, or what goes on from there.
+template <class T, int D, int kTile, class P>
+cudaError_t launch_decode(const Cut& k, P a, void (*kernel)(P), void (*alone)(P), int smem,
+                          std::atomic<int>* known, std::atomic<int>* known_alone, cudaStream_t s) {
   int resident = 0;
   a.cluster = k.cluster;
   cudaError_t e = resident_blocks(k.cluster > 0 ? (const void*)alone : (const void*)kernel, smem,
@@ -665,6 +689,69 @@ cudaError_t launch_decode(const Cut& k, DecodeParams a, void (*kernel)(DecodePar
   e = launch_early(kernel, dim3((unsigned)(runs * a.split)), kThreads, smem, s, 1, a);
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
   return launch_join<T, D, kTile>(k, a, runs, s);
+}
+
+// The arguments of fa_decode and fa_decode_e4m3, after H is known to fit: what is wrong with them, and the
+// kernels' parameters.  es: bytes of an element of the pools.
+struct DecodeCall {
+  const fa_cache* c;
+  int32_t H;
+  float scale;
+  const void* Q;
+  int64_t q_stride_s, q_stride_h;
+  const void *K_pages, *V_pages;
+  const int32_t *page_table, *lengths;
+  void* O;
+  int64_t o_stride_s, o_stride_h;
+  float* L;
+  void* workspace;
+  size_t workspace_bytes;
+};
+inline fa_status check_call(const DecodeCall& x, size_t need) {
+  const int es = elem_size(x.c->dtype), d = x.c->d;
+  if (!(x.scale > 0.f) || !isfinite(x.scale * kLog2e) || x.O == x.Q || !aligned16(x.Q) || !aligned16(x.K_pages) ||
+      !aligned16(x.V_pages) || !aligned16(x.O) || !aligned4(x.page_table) || !aligned4(x.lengths) || !aligned4(x.L) ||
+      !good_stride(x.q_stride_s, d, es, false) || !good_stride(x.q_stride_h, d, es, false) ||
+      !good_stride(x.o_stride_s, d, es, true) || !good_stride(x.o_stride_h, d, es, true))
+    return FA_ERR_INVALID_ARG;
+  return need > 0 && (!aligned16(x.workspace) || x.workspace_bytes < need) ? FA_ERR_INVALID_ARG : FA_OK;
+}
+inline void fill(const DecodeCall& x, const Cut& k, size_t need, int es, DecodeParams* a) {
+  const fa_cache& c = *x.c;
+  const int qes = elem_size(c.dtype);
+  a->Q = (const char*)x.Q;
+  a->K = (const char*)x.K_pages;
+  a->V = (const char*)x.V_pages;
+  a->O = (char*)x.O;
+  a->L = x.L;
+  a->table = x.page_table;
+  a->lengths = x.lengths;
+  a->part_o = (float*)x.workspace;
+  a->part_ml = (float2*)(a->part_o + (need > 0 ? (size_t)k.parts() * k.part_heads * c.d : 0));
+  a->page_rows = FastDiv(c.page_rows);
+  a->S = c.S;
+  a->H = x.H;
+  a->group = x.H / c.H_kv;
+  a->split = k.split;
+  a->piece_heads = k.piece_heads;
+  a->items = c.H_kv;
+  a->num_pages = c.num_pages;
+  a->max_pages = c.max_pages;
+  a->cap = (int)cache_rows(c);
+  a->table_stride = c.table_stride;
+  a->qs = x.q_stride_s * qes;
+  a->qh = x.q_stride_h * qes;
+  a->os = x.o_stride_s * qes;
+  a->oh = x.o_stride_h * qes;
+  a->pp = c.stride_page * es;
+  a->ph = c.stride_h * es;
+  a->pn = c.stride_n * es;
+  a->scale2 = x.scale * kLog2e;
+}
+// H against a cache that has been checked.
+inline fa_status check_heads(const fa_cache* c, int32_t H) {
+  if (H < 1 || H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
+  return (int64_t)c->S * H > (1 << 24) || H / c->H_kv > kMostHeads ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);

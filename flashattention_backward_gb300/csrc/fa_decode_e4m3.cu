@@ -1,9 +1,15 @@
 // Attention of one new token over a paged key-value cache in 8 bits
 // (fa_decode_e4m3): k_j and v_j are stored numbers times the scales of their
-// blocks,
-//   s_j = scale q . k_j,  m = max_j s_j,  l = sum_j 2^(s_j - m),
-//   O = sum_j 2^(s_j - m) v_j / l,  L = (m + log2 l) ln 2
-// with scores in units of log 2.
+// blocks, a_j and b_j,
+//   s_j = scale a_j q . k_j,  m = max_j s_j,  l = sum_j 2^(s_j - m),
+//   O = sum_j 2^(s_j - m) b_j v_j / l,  L = (m + log2 l) ln 2
+// with scores in units of log 2 (the scale carries log2 e).
+//
+// Half the bytes of a bf16 cache for the same products: a row and head are 2 d
+// bytes against 4 d flops a query head.  HBM is still the bound with up to 16
+// query heads a key head, but the instructions for every byte are twice as many, so
+// here the design is about those as well.  How the work is shared out and
+// joined is in fa_decode.cuh.
 
 #include "fa_decode.cuh"
 #include "fa_e4m3.cuh"
@@ -11,84 +17,569 @@
 namespace fa {
 namespace {
 
-struct SimpleParams {
-  const char* Q;
-  const uint8_t *K, *V;
+struct E4m3Params : DecodeParams {
   const float *KS, *VS;
-  char* O;
-  float* L;
-  const int32_t *table, *lengths;
-  int32_t* status;
-  FastDiv page_rows, block_rows;
-  int H, group, heads, d, num_pages, max_pages, cap;
-  int64_t table_stride, qs, qh, os, oh, pp, ph, pn;
-  float scale2;
+  FastDiv block_rows;
+  int blocks;           // of a page and head
+  int64_t page_scales;  // scales of a page
 };
 
-// A block a sequence and query head, a warp a row, 8 columns a lane.
-template <class T>
-__global__ void __launch_bounds__(128) decode_simple_kernel(const SimpleParams a) {
-  after_stream();
-  __shared__ float ms[4], ls[4], os[4][256];
-  const int s = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / a.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool mine = lane * 8 < a.d;
-  int n = a.lengths[s];
-  if ((n < 0 || n > a.cap) && threadIdx.x == 0) report_pages(a.status);
-  n = min(max(n, 0), a.cap);
-  float q[8], acc[8];
-  for (int e = 0; e < 8; ++e) {
-    const T* row = reinterpret_cast<const T*>(a.Q + s * a.qs + h * a.qh);
-    q[e] = mine ? (float)row[lane * 8 + e] * a.scale2 : 0.f;
-    acc[e] = 0.f;
+// A warp takes 16 kSub rows of each tile with mma.m16n8k16 in fp16, into which
+// e4m3 numbers go exactly, two at a time:
+//
+//  S = Q K^T     A = 16 query heads x 16 columns, B = 16 columns x 8 keys.  The
+//                columns of a step are those that make a lane's share of B four
+//                bytes of a key, so that a run of 16 bytes serves four steps.
+//  O^T += V^T P^T  A = 16 columns x 16 keys, B = 16 keys x 8 heads: S's accumulators
+//                are P^T's operand as they stand.  ldmatrix turns V round by pairs of
+//                bytes: a lane gets columns 2 i and 2 i + 1 of two keys, a byte
+//                permute makes the two columns' pairs, and the 16 columns of a step are
+//                the even ones and then the odd ones of 16.
+//
+// Queries: a head's are multiplied by the power of two that takes the largest to
+// 2^14 ... 2^15, so that bf16 ones are fp16 numbers exactly, down to 2^-28 of the
+// largest.  fp32 ones become the sum of two, the second 2^11 times itself: it takes
+// the place of a second group of 8 heads, at no more products.
+//
+// Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers.  The maximum that
+// weights are taken against and U are moved only when a weight passes 2^kAhead
+// (its bits are not the fewer for that), so that almost every tile does without
+// the maximum over its lanes and without a look at the accumulators.
+template <int D, int NH, bool kF32>
+struct Mma8 {
+  static constexpr int kSub = D <= 64 ? 2 : 1;
+  static constexpr int kRows = 16 * kSub;       // of a tile, a warp
+  static constexpr int kTile = kWarps * kRows;
+  static constexpr int kRun = D % 64 == 0 ? 16 : D % 32 == 0 ? 8 : 4;  // bytes of a key that a lane reads at a time
+  static constexpr int kRuns = D / (4 * kRun);
+  static constexpr int kPieces = D / 16;        // of 16 bytes in a row
+  // K: an access's lanes take 128 bytes of different banks: 8 rows of 16, 4 of 32 (or of 32 out
+  // of 96), 2 of 64, or of rows of 128 and more, 16 more apart, every second piece of two.
+  static constexpr int kPitchK = D >= 128 ? D + 16 : D;
+  // V: 8 rows' pieces of 16 bytes
+  static constexpr int kPitchV = D == 16 ? 16 : D + 16;
+  static constexpr int kScales = kRows * (kPitchK + kPitchV);  // then the scales of K and V, and which rows are there
+  static constexpr int kSeen = kScales + kRows * 8;
+  static constexpr int kStageBytes = kSeen + 16;
+  static constexpr int kBlocks = D == 16 ? 6 : D == 32 ? 5 : D == 256 ? 2 : 3;
+  static constexpr int kStages = D == 16 ? 5 : D == 96 ? 4 : 3;
+  static constexpr int kVW = D % 64 || D == 256 ? (D == 16 ? 16 : 32) : 64;  // columns of O that are exchanged at a time
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kPad = kVW + 4;          // floats of a row of the exchange buffer
+  static constexpr int kSmem = kRing + kWarps * 8 * kPad * 4;
+  static_assert(!kF32 || NH == 1, "fp32 queries take both groups of heads");
+  static_assert(kStageBytes % 16 == 0 && kScales % 16 == 0, "copies of 16 bytes");
+  // where lane q's c-th run of a key begins
+  __device__ static constexpr int run_at(int c, int q) {
+    return D >= 128 ? (8 * (c / 2) + 2 * q + c % 2) * 16 : (4 * c + q) * kRun;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < n; j += 4) {
-    uint32_t r;
-    const uint32_t col = a.page_rows.div((uint32_t)j, &r);
-    const int page = a.table[s * a.table_stride + col];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) report_pages(a.status);
-      continue;
-    }
-    const int64_t at = page * a.pp + g * a.ph + (int64_t)r * a.pn + lane * 8;
-    const int64_t sc = ((int64_t)page * a.heads + g) * (a.page_rows.d / a.block_rows.d) + a.block_rows.div(r);
-    uint2 k = make_uint2(0, 0), v = make_uint2(0, 0);
-    if (mine) k = *reinterpret_cast<const uint2*>(a.K + at), v = *reinterpret_cast<const uint2*>(a.V + at);
-    const float4 k0 = e4m3x4_to_float4(k.x), k1 = e4m3x4_to_float4(k.y);
-    float x = q[0] * k0.x + q[1] * k0.y + q[2] * k0.z + q[3] * k0.w + q[4] * k1.x + q[5] * k1.y + q[6] * k1.z + q[7] * k1.w;
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    x *= a.KS[sc];
-    const float now = fmaxf(m, x), base = base_of(now), alpha = exp2f(m - base), p = exp2f(x - base), w = p * a.VS[sc];
-    m = now;
-    l = l * alpha + p;
-    const float4 v0 = e4m3x4_to_float4(v.x), v1 = e4m3x4_to_float4(v.y);
-    const float y[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * alpha + w * y[e];
-  }
-  if (lane == 0) ms[warp] = m, ls[warp] = l;
-  if (mine)
-    for (int e = 0; e < 8; ++e) os[warp][lane * 8 + e] = acc[e];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, ms[w]);
-  const float base = base_of(top);
-  for (int w = 0; w < 4; ++w) sum += ls[w] * exp2f(ms[w] - base);
-  const bool none = sum == 0.f;
-  for (int c = threadIdx.x; c < a.d; c += 128) {
-    float o = 0.f;
-    for (int w = 0; w < 4; ++w) o += os[w][c] * exp2f(ms[w] - base);
-    reinterpret_cast<T*>(a.O + s * a.os + h * a.oh)[c] = (T)(none ? 0.f : o / sum);
-  }
-  if (threadIdx.x == 0) a.L[(int64_t)s * a.H + h] = none ? INFINITY : (top + log2f(sum)) * kLn2;
+};
+constexpr float kAhead = 128.f;   // 2^7
+constexpr float kTopWeight = 256.f;  // of a weight when U is set, as fp16: kAhead times that is below 65504
+constexpr float kLeastUnit = 0x1p-100f;
+
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_trans2(uint32_t at, uint32_t& a, uint32_t& b) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 lds8(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
 
-fa_status check_heads(const fa_cache* c, int32_t block_rows, int32_t H) {
+// A warp's copies of its rows of each tile and of their scales, ahead of their use.
+template <class M>
+struct Loader8 {
+  static constexpr int kRows = M::kRows, kStages = M::kStages;
+  const E4m3Params& a;
+  Place<M::kTile> at;   // the tile that is copied next
+  const int64_t end;    // of the run
+  const uint32_t ring;  // of this warp
+  const int piece;      // of the query heads
+  // The row that this lane looks up in that tile: its page is asked for one
+  // tile ahead of the copies that need it.
+  int page = -1;
+  bool in = false;
+  int64_t off = 0;
+  int scale = 0;  // of the page's
+
+  __device__ __forceinline__ Loader8(const E4m3Params& p, const Place<M::kTile>& first, int64_t e, uint32_t r, int h)
+      : a(p), at(first), end(e), ring(r), piece(h) {
+    look_up();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) produce(i);
+  }
+  __device__ __forceinline__ void look_up() {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = at.t * M::kTile + warp * kRows + (lane & (kRows - 1));
+    uint32_t r;
+    const uint32_t col = a.page_rows.div((uint32_t)j, &r);
+    in = j < at.rows;
+    page = in ? a.table[at.s * a.table_stride + col] : -1;
+    off = at.item * a.ph + (int64_t)r * a.pn;
+    scale = at.item * a.blocks + (int)a.block_rows.div(r);
+    if (at.t == 0) {  // a new item: its queries into L1
+      int heads;
+      const char* row = a.Q + at.s * a.qs + (int64_t)first_head(a, at.item, piece, &heads) * a.qh;
+      constexpr int kLines = (M::kPieces * 32 + 127) / 128;
+      for (int k = lane; k < heads * kLines; k += 32) prefetch_l1(row + (k / kLines) * a.qh + (k % kLines) * 128);
+    }
+  }
+  // Copies of the tile looked up, into stage st.  Rows that are not there are
+  // filled with zeros, and not read.  The pieces of a row go to neighbouring
+  // lanes, so that a request takes whole lines.
+  __device__ __forceinline__ uint32_t copy(uint32_t to) {
+    const int lane = threadIdx.x & 31;
+    const bool ok = in && page >= 0 && page < a.num_pages;
+    if (in && !ok) report_pages(a.status);
+    const int64_t from_row = ok ? page * a.pp + off : 0;
+    const int64_t from_scale = ok ? page * a.page_scales + scale : 0;
+    const uint32_t seen = __ballot_sync(0xffffffffu, ok);
+    const uint32_t scales_to = to + M::kScales;
+    if constexpr (kRows == 32) {
+      cp_async4(scales_to + lane * 4, a.KS + from_scale, ok);
+      cp_async4(scales_to + (32 + lane) * 4, a.VS + from_scale, ok);
+    } else {
+      cp_async4(scales_to + lane * 4, (lane < 16 ? a.KS : a.VS) + from_scale, ok);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows * M::kPieces / 32; ++i) {
+      const int row = (i * 32 + lane) / M::kPieces, piece = (i * 32 + lane) % M::kPieces;
+      const int64_t from = __shfl_sync(0xffffffffu, from_row, row) + piece * 16;
+      const bool on = (seen >> row) & 1;
+      cp_async16(to + row * M::kPitchK + piece * 16, a.K + from, on);
+      cp_async16(to + kRows * M::kPitchK + row * M::kPitchV + piece * 16, a.V + from, on);
+    }
+    return kRows == 32 ? seen : seen & 0xffffu;
+  }
+  __device__ __forceinline__ void produce(int st) {
+    const uint32_t to = ring + st * M::kStageBytes;
+    uint32_t seen = 0;
+    if (at.unit < end) {
+      seen = copy(to);
+      at.next(a);
+      if (at.unit < end) look_up();
+    }
+    if ((threadIdx.x & 31) == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + M::kSeen), "r"(seen) : "memory");
+    cp_commit();
+  }
+  // Waits for the oldest tile in flight, in stage st, asks for another, and
+  // returns which rows of it are there.
+  __device__ __forceinline__ uint32_t next(int st) {
+    cp_wait<kStages - 2>();
+    __syncwarp();  // the warp's copies are all there, and its reads of the stage refilled next are done
+    uint32_t seen;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(seen) : "r"(ring + st * M::kStageBytes + M::kSeen) : "memory");
+    produce(st == 0 ? kStages - 1 : st - 1);
+    return seen;
+  }
+};
+
+// A lane's share of a head's queries as fp16 operands: columns 4 c + 0, 1 and 2, 3
+// of its runs, in units of *unit.
+template <class M, class T>
+struct Columns {
+  static constexpr int kWords = M::kRun / 4;  // steps of a run
+  float x[M::kRuns][kWords][4];
+  __device__ __forceinline__ void load(const char* row, int q) {
+#pragma unroll
+    for (int c = 0; c < M::kRuns; ++c)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const char* p = row + (M::run_at(c, q) + 4 * w) * (int)sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          x[c][w][0] = ptx::bf16lo(v.x), x[c][w][1] = ptx::bf16hi(v.x);
+          x[c][w][2] = ptx::bf16lo(v.y), x[c][w][3] = ptx::bf16hi(v.y);
+        } else {
+          const float4 v = *reinterpret_cast<const float4*>(p);
+          x[c][w][0] = v.x, x[c][w][1] = v.y, x[c][w][2] = v.z, x[c][w][3] = v.w;
+        }
+      }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int c = 0; c < M::kRuns; ++c)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[c][w][e] = 0.f;
+  }
+  // Takes the head's largest finite value to 2^14 ... 2^15; returns what the products are to be multiplied by.
+  __device__ __forceinline__ float normalise() {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < M::kRuns; ++c)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t t = __float_as_uint(x[c][w][e]) & 0x7fffffffu;
+          top = max(top, t < 0x7f800000u ? t : 0u);
+        }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = max((int)(top >> 23), 15) - 14;  // 1 ... 240
+    const float by = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < M::kRuns; ++c)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[c][w][i] *= by;
+    return __uint_as_float((uint32_t)e << 23);
+  }
+};
+
+// kAlone: a cluster an item, joined here; else a block a run.
+template <int D, int NH, bool kF32, bool kAlone>
+__global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
+    decode_e4m3_kernel(const __grid_constant__ E4m3Params a) {
+  using M = Mma8<D, NH, kF32>;
+  using T = std::conditional_t<kF32, float, __nv_bfloat16>;
+  constexpr int kTile = M::kTile, kStages = M::kStages, VW = M::kVW, kSub = M::kSub, kWords = M::kRun / 4;
+  constexpr int kHeads = 8 * NH;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 ml[kWarps][kHeads];
+  __shared__ float units[kWarps][kHeads];
+  __shared__ float2 part_ml[kHeads];  // kAlone: this block's part, with o in part_o
+  float4* part_o = reinterpret_cast<float4*>(smem);  // over the ring, which is read by then
+  Place<kTile> at;
+  int64_t end;
+  bool some;
+  after_stream();
+  if constexpr (kAlone) {
+    some = share_of_item(a, &at, &end);
+    if (!some && threadIdx.x < kHeads) part_ml[threadIdx.x] = make_float2(-INFINITY, kNoPart);
+  } else {
+    next_may_start();  // the join
+    some = run_of(a, &at, &end);
+    if (!some) return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int piece = (kAlone ? blockIdx.x / a.cluster : blockIdx.x) % a.split;
+  const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * M::kStageBytes;
+  float* exchange = reinterpret_cast<float*>(smem + M::kRing);
+  Loader8<M> load(a, at, end, ring, piece);
+
+  uint32_t qf[M::kRuns][kWords][2 * (kF32 ? 2 : NH)];
+  float qscale[NH];
+  float acc[NH][M::kPieces][4];  // O^T, unnormalised, in units of unit / kTopWeight: columns 2 g, 2 g + 1 of 16, heads 2 q, 2 q + 1
+  float m[NH], base[NH], l[NH];  // of heads g, g + 8; l of this lane's keys alone
+  float unit[NH], per_unit[NH];
+  int begin = at.t;              // tile at which the item (or this block's part of it) began
+  int stage = 0;
+  bool first = true, last = !some;  // item of the run
+
+  for (bool fresh = true; !last; fresh = false) {
+    Place<kTile> next = at;
+    next.next(a);
+    last = next.unit >= end;
+    const uint32_t seen = load.next(stage);
+
+    if (fresh || at.t == 0) {
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
+      const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        Columns<M, T> x;
+        if (g + 8 * u < heads)
+          x.load(row + (g + 8 * u) * a.qh, q);
+        else
+          x.zero();
+        qscale[u] = x.normalise() * a.scale2;
+#pragma unroll
+        for (int c = 0; c < M::kRuns; ++c)
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x0 = x.x[c][w][2 * e], x1 = x.x[c][w][2 * e + 1];
+              const uint32_t y = pack_f16x2(x0, x1);
+              qf[c][w][2 * u + e] = y;
+              if constexpr (kF32) {  // what is left, 2^11 times itself; nothing of an infinity
+                const float2 z = f16x2_to_float2(y);
+                qf[c][w][2 + e] = pack_f16x2(isinf(x0) ? 0.f : (x0 - z.x) * 2048.f, isinf(x1) ? 0.f : (x1 - z.y) * 2048.f);
+              }
+            }
+        m[u] = -INFINITY;
+        base[u] = 0.f;
+        l[u] = 0.f;
+        unit[u] = kLeastUnit;
+        per_unit[u] = kTopWeight / kLeastUnit;
+#pragma unroll
+        for (int p = 0; p < M::kPieces; ++p)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[u][p][x] = 0.f;
+      }
+      begin = at.t;
+    }
+
+    if (seen) {
+      const uint32_t tile = ring + stage * M::kStageBytes;
+      float s[2 * kSub][4];
+#pragma unroll
+      for (int o = 0; o < 2 * kSub; ++o) {  // 8 keys
+        s[o][0] = s[o][1] = s[o][2] = s[o][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < M::kRuns; ++c) {
+          const uint32_t from = tile + (8 * o + g) * M::kPitchK + M::run_at(c, q);
+          uint32_t k[4];
+          if constexpr (M::kRun == 16) {
+            const uint4 v = lds16(from);
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+          } else if constexpr (M::kRun == 8) {
+            const float2 v = lds8(from);
+            k[0] = __float_as_uint(v.x), k[1] = __float_as_uint(v.y);
+          } else {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(k[0]) : "r"(from));
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            constexpr bool kBoth = NH > 1 || kF32;
+            mma16816_f16(s[o], qf[c][w][0], kBoth ? qf[c][w][kBoth ? 2 : 0] : 0u, qf[c][w][1],
+                         kBoth ? qf[c][w][kBoth ? 3 : 0] : 0u, e4m3x2_lo(k[w]), e4m3x2_hi(k[w]));
+          }
+        }
+      }
+      // keys 8 o + 2 q, 8 o + 2 q + 1 of the warp's
+      float2 ks[2 * kSub], vs[2 * kSub];
+#pragma unroll
+      for (int o = 0; o < 2 * kSub; ++o) {
+        ks[o] = lds8(tile + M::kScales + (8 * o + 2 * q) * 4);
+        vs[o] = lds8(tile + M::kScales + (M::kRows + 8 * o + 2 * q) * 4);
+      }
+      const uint32_t mine = seen >> (2 * q);
+      float x[NH][2 * kSub][2], p[NH][2 * kSub][2], w[NH][2 * kSub][2];
+      bool passed = false;
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        float top = -INFINITY, most = 0.f;
+#pragma unroll
+        for (int o = 0; o < 2 * kSub; ++o)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float dot = kF32 ? fmaf(s[o][2 + e], 1.f / 2048.f, s[o][e]) : s[o][2 * u + e];
+            const float y = dot * qscale[u] * (e ? ks[o].y : ks[o].x);
+            x[u][o][e] = mine >> (8 * o + e) & 1 ? y : -INFINITY;
+            top = fmaxf(top, x[u][o][e]);
+            p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
+            w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
+            most = fmaxf(most, w[u][o][e]);
+          }
+        // 2^7 above the maximum, or above the unit
+        passed |= top > m[u] + 7.f || most > kAhead * unit[u];
+      }
+      if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+        for (int u = 0; u < NH; ++u) {
+          float top = m[u], most = 0.f;
+#pragma unroll
+          for (int o = 0; o < 2 * kSub; ++o) top = fmaxf(top, fmaxf(x[u][o][0], x[u][o][1]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          base[u] = base_of(top);
+          const float alpha = ptx::ex2(m[u] - base[u]);
+          m[u] = top;
+          l[u] *= alpha;
+#pragma unroll
+          for (int o = 0; o < 2 * kSub; ++o)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
+              w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
+              most = fmaxf(most, w[u][o][e]);
+            }
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          // the new unit: the power of two at or above what is largest, the old sums' unit or a weight
+          const float old = alpha * unit[u];
+          const float now = fmaxf(fmaxf(most, old), kLeastUnit);
+          unit[u] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
+          const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[u]));
+          per_unit[u] = kTopWeight * per;
+          const float f = old * per;
+          // the factors belong to heads g, the accumulators to heads 2q, 2q + 1
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
+#pragma unroll
+          for (int c = 0; c < M::kPieces; ++c) {
+            acc[u][c][0] *= f0, acc[u][c][2] *= f0;
+            acc[u][c][1] *= f1, acc[u][c][3] *= f1;
+          }
+        }
+      }
+      uint32_t hi[NH][2 * kSub], lo[NH][2 * kSub];
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+#pragma unroll
+        for (int o = 0; o < 2 * kSub; ++o) {
+          l[u] += p[u][o][0] + p[u][o][1];
+          const float w0 = w[u][o][0] * per_unit[u], w1 = w[u][o][1] * per_unit[u];
+          hi[u][o] = pack_f16x2(w0, w1);
+          const float2 z = f16x2_to_float2(hi[u][o]);
+          lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
+        }
+      // V: pieces of 8 keys x 8 pairs of columns; lane 8 n + r names row r of piece n
+      const uint32_t v_at = tile + M::kRows * M::kPitchK + ((lane & 7) + (lane >> 3 & 1) * 8) * M::kPitchV + (lane >> 4) * 16;
+#pragma unroll
+      for (int b = 0; b < kSub; ++b)
+#pragma unroll
+        for (int c = 0; c < M::kPieces; c += 2) {
+          constexpr int kTwo = M::kPieces > 1 ? 2 : 1;
+          uint32_t r[4];
+          const uint32_t from = v_at + 16 * b * M::kPitchV + c * 16;
+          if constexpr (kTwo == 2)
+            ldmatrix_trans(from, r[0], r[1], r[2], r[3]);
+          else
+            ldmatrix_trans2(from, r[0], r[1]);
+#pragma unroll
+          for (int i = 0; i < kTwo; ++i) {
+            const uint32_t v0 = __byte_perm(r[2 * i], 0, 0x3120), v1 = __byte_perm(r[2 * i + 1], 0, 0x3120);
+            const uint32_t a0 = e4m3x2_lo(v0), a1 = e4m3x2_hi(v0), a2 = e4m3x2_lo(v1), a3 = e4m3x2_hi(v1);
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+              mma16816_f16(acc[u][c + i], a0, a1, a2, a3, hi[u][2 * b], hi[u][2 * b + 1]);
+              mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
+            }
+          }
+        }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+
+    if (at.t + 1 == at.tiles || last) {
+      // ---- the item ends here, or goes on in the next block's run
+      const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
+      // the part of an item that was being read when the run began is the
+      // block's first, any other its second
+      const int slot = (2 * (blockIdx.x / a.split) + (first ? 0 : 1)) * a.split + piece;
+      first = false;
+      int heads;
+      const int h0 = first_head(a, at.item, piece, &heads);
+      __syncthreads();  // ml, units and the exchange buffer have been read
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+        l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+        if (q == 0) {
+          ml[warp][g + 8 * u] = make_float2(m[u], l[u]);
+          units[warp][g + 8 * u] = unit[u] * (1.f / kTopWeight);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        // this warp's factor of heads 2q, 2q + 1
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int head = 8 * u + 2 * q + e;
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k][head].x);
+          f[e] = ptx::ex2(ml[warp][head].x - base_of(top)) * units[warp][head];
+        }
+#pragma unroll
+        for (int c = 0; c < D / VW; ++c) {
+          if (u + c > 0) __syncthreads();
+          float* mine_at = exchange + (warp * 8 + 2 * q) * M::kPad + 2 * g;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < VW / 16; ++i) {
+              const float* o = acc[u][c * (VW / 16) + i];
+              *reinterpret_cast<float2*>(mine_at + e * M::kPad + 16 * i) = make_float2(o[e] * f[e], o[2 + e] * f[e]);
+            }
+          __syncthreads();
+          // a thread adds up four columns of a head
+#pragma unroll
+          for (int k0 = 0; k0 < 2 * VW; k0 += kThreads) {
+            const int k = k0 + threadIdx.x, in8 = k / (VW / 4), col = c * VW + k % (VW / 4) * 4, head = 8 * u + in8;
+            if (in8 >= 8 || head >= heads) continue;
+            float top = -INFINITY, sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k][head].x);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+              sum += ml[k][head].y * ptx::ex2(ml[k][head].x - base_of(top));
+              const float4 y = *reinterpret_cast<const float4*>(exchange + (k * 8 + in8) * M::kPad + col - c * VW);
+              o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+            }
+            if (whole) {
+              const bool none = sum == 0.f;
+              const float inv = none ? 0.f : 1.f / sum;
+              o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+              store4<T>(a.O + at.s * a.os + (int64_t)(h0 + head) * a.oh, col, o);
+              if (col == 0) a.L[(int64_t)at.s * a.H + h0 + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
+            } else if (kAlone) {
+              part_o[(head * D + col) / 4] = o;
+              if (col == 0) part_ml[head] = make_float2(top, sum);
+            } else {
+              const int64_t p = (int64_t)slot * kHeads + head;
+              *reinterpret_cast<float4*>(a.part_o + p * D + col) = o;
+              if (col == 0) a.part_ml[p] = make_float2(top, sum);
+            }
+          }
+        }
+      }
+    }
+    at = next;
+  }
+  if (kAlone && a.cluster > 1) join_cluster<T, D>(a, part_o, part_ml);
+}
+
+template <int D, int NH, bool kF32>
+cudaError_t launch(const Cut& k, const E4m3Params& a, cudaStream_t s) {
+  using M = Mma8<D, NH, kF32>;
+  using T = std::conditional_t<kF32, float, __nv_bfloat16>;
+  static std::atomic<int> known[64], known_alone[64];
+  return launch_decode<T, D, M::kTile, E4m3Params>(k, a, decode_e4m3_kernel<D, NH, kF32, false>,
+                                                   decode_e4m3_kernel<D, NH, kF32, true>, M::kSmem, known, known_alone, s);
+}
+
+template <int D>
+cudaError_t launch_d(const fa_cache& c, const Cut& k, const E4m3Params& a, cudaStream_t s) {
+  if (c.dtype == FA_FP32) return launch<D, 1, true>(k, a, s);
+  if constexpr (D > 16) return k.part_heads == 8 ? launch<D, 1, false>(k, a, s) : launch<D, 2, false>(k, a, s);
+  return cudaErrorInvalidValue;
+}
+
+template <int D>
+Cut cut_d(const fa_cache& c, int H) {
+  using M = Mma8<D, 1, true>;
+  return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks);
+}
+Cut cut_e4m3(const fa_cache& c, int H) {
+  switch (c.d) {
+    case 16: return cut_d<16>(c, H);
+    case 32: return cut_d<32>(c, H);
+    case 64: return cut_d<64>(c, H);
+    case 96: return cut_d<96>(c, H);
+    case 128: return cut_d<128>(c, H);
+    default: return cut_d<256>(c, H);
+  }
+}
+
+fa_status check(const fa_cache* c, int32_t block_rows, int32_t H) {
   const fa_status st = check_cache_e4m3(c, block_rows);
-  if (st != FA_OK) return st;
-  if (H < 1 || H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
-  if ((int64_t)c->S * H > (1 << 24) || H / c->H_kv > kMostHeads) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
+  return st == FA_OK ? check_heads(c, H) : st;
 }
 
 }  // namespace
@@ -96,7 +587,9 @@ fa_status check_heads(const fa_cache* c, int32_t block_rows, int32_t H) {
 
 extern "C" {
 
-size_t fa_decode_e4m3_workspace_bytes(const fa_cache* c, int32_t H) { return 0; }
+size_t fa_decode_e4m3_workspace_bytes(const fa_cache* c, int32_t H) {
+  return fa::check(c, 1, H) == FA_OK ? fa::workspace_of(fa::cut_e4m3(*c, H), c->d) : 0;
+}
 
 fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float scale, const void* Q,
                          int64_t q_stride_s, int64_t q_stride_h, const void* K_pages, const void* V_pages,
@@ -104,50 +597,35 @@ fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float
                          const int32_t* lengths, void* O, int64_t o_stride_s, int64_t o_stride_h, float* L,
                          void* workspace, size_t workspace_bytes, void* stream) {
   fa::NvtxRange range("fa_decode_e4m3");
-  const fa_status st = fa::check_heads(c, block_rows, H);
+  fa_status st = fa::check(c, block_rows, H);
   if (st != FA_OK) return st;
-  const int es = fa::elem_size(c->dtype);
-  if (!(scale > 0.f) || !isfinite(scale * fa::kLog2e) || O == Q || !fa::aligned16(Q) || !fa::aligned16(K_pages) ||
-      !fa::aligned16(V_pages) || !fa::aligned4(K_scales) || !fa::aligned4(V_scales) || !fa::aligned16(O) ||
-      !fa::aligned4(page_table) || !fa::aligned4(lengths) || !fa::aligned4(L) ||
-      !fa::good_stride(q_stride_s, c->d, es, false) || !fa::good_stride(q_stride_h, c->d, es, false) ||
-      !fa::good_stride(o_stride_s, c->d, es, true) || !fa::good_stride(o_stride_h, c->d, es, true))
-    return FA_ERR_INVALID_ARG;
-  fa::SimpleParams a;
+  const fa::DecodeCall x = {c, H, scale, Q, q_stride_s, q_stride_h, K_pages, V_pages, page_table, lengths,
+                            O, o_stride_s, o_stride_h, L, workspace, workspace_bytes};
+  const fa::Cut k = fa::cut_e4m3(*c, H);
+  const size_t need = fa::workspace_of(k, c->d);
+  st = fa::check_call(x, need);
+  if (st == FA_OK && (!fa::aligned4(K_scales) || !fa::aligned4(V_scales))) st = FA_ERR_INVALID_ARG;
+  if (st != FA_OK) return st;
+  fa::E4m3Params a;
   a.status = fa::device_status_word();
   if (!a.status) return FA_ERR_CUDA;
-  a.Q = (const char*)Q;
-  a.K = (const uint8_t*)K_pages;
-  a.V = (const uint8_t*)V_pages;
+  fa::fill(x, k, need, 1, &a);
   a.KS = K_scales;
   a.VS = V_scales;
-  a.O = (char*)O;
-  a.L = L;
-  a.table = page_table;
-  a.lengths = lengths;
-  a.page_rows = fa::FastDiv(c->page_rows);
   a.block_rows = fa::FastDiv(block_rows);
-  a.H = H;
-  a.group = H / c->H_kv;
-  a.heads = c->H_kv;
-  a.d = c->d;
-  a.num_pages = c->num_pages;
-  a.max_pages = c->max_pages;
-  a.cap = (int)fa::cache_rows(*c);
-  a.table_stride = c->table_stride;
-  a.qs = q_stride_s * es;
-  a.qh = q_stride_h * es;
-  a.os = o_stride_s * es;
-  a.oh = o_stride_h * es;
-  a.pp = c->stride_page;
-  a.ph = c->stride_h;
-  a.pn = c->stride_n;
-  a.scale2 = scale * fa::kLog2e;
-  const dim3 grid((unsigned)(c->S * H));
+  a.blocks = c->page_rows / block_rows;
+  a.page_scales = (int64_t)c->H_kv * a.blocks;
   const cudaStream_t s = (cudaStream_t)stream;
-  return fa::status_of(c->dtype == FA_BF16
-                           ? fa::launch_early(fa::decode_simple_kernel<__nv_bfloat16>, grid, 128, 0, s, 1, a)
-                           : fa::launch_early(fa::decode_simple_kernel<float>, grid, 128, 0, s, 1, a));
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (c->d) {
+    case 16: e = fa::launch_d<16>(*c, k, a, s); break;
+    case 32: e = fa::launch_d<32>(*c, k, a, s); break;
+    case 64: e = fa::launch_d<64>(*c, k, a, s); break;
+    case 96: e = fa::launch_d<96>(*c, k, a, s); break;
+    case 128: e = fa::launch_d<128>(*c, k, a, s); break;
+    case 256: e = fa::launch_d<256>(*c, k, a, s); break;
+  }
+  return fa::status_of(e);
 }
 
 }  // extern "C"
