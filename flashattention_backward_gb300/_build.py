@@ -27,7 +27,7 @@ LIB = os.path.join(OUT_DIR, "libfa.so")
 HEADER = os.path.join(PKG, "..", "include", "fa.h")
 SOURCES = ["fa_api.cu", "fa_simt.cu", "fa_bwd_sm103.cu", "fa_bwd_sm103_count.cu", "fa_bwd_d256_sm103.cu",
            "fa_fwd_sm103.cu", "fa_noalloc.cu", "fa_host.cu", "fa_tma.cu", "fa_decode.cu", "fa_decode_fp32.cu", "fa_cache.cu", "fa_pages.cu",
-           "fa_cache_e4m3.cu", "fa_decode_e4m3.cu"]
+           "fa_cache_e4m3.cu", "fa_decode_e4m3.cu", "fa_decode_e4m3_sm103.cu"]
 TORCH_SOURCE = "fa_torch.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

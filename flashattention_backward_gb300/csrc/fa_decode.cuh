@@ -64,6 +64,15 @@ struct DecodeParams {
   float scale2;       // scale * log2(e)
 };
 
+// Of a cache in 8 bits.
+struct E4m3Params : DecodeParams {
+  const float *KS, *VS;
+  FastDiv block_rows;
+  int blocks;           // of a page and head
+  int64_t page_scales;  // scales of a page
+  uint64_t wait_ns;
+};
+
 // Blocks an SM holds of the kernel for that type and head dim: what its ring of
 // tiles in shared memory (228 KB an SM) leaves room for.
 constexpr int blocks_an_sm(bool bf16, int d) {
@@ -188,7 +197,9 @@ struct Units {
   __device__ __forceinline__ int64_t of(int s) const {
     return s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
   }
-  __device__ __forceinline__ Units(const DecodeParams& p, int64_t* shared) : a(p), sums(shared) {
+  __device__ __forceinline__ Units(const DecodeParams& p, int64_t* shared) : a(p), sums(shared) { restart(); }
+  // the first NT sequences once more: find() goes on from them
+  __device__ __forceinline__ void restart() {
     n = of(threadIdx.x);
     lo = block_scan<NT>(n, sums, &all);
   }
@@ -277,6 +288,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const char* src, bool o
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ void prefetch_l1(const char* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -288,6 +302,11 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -657,7 +676,8 @@ cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStrea
 
 // How many blocks of a kernel the device holds at a time; raises the kernel's
 // shared-memory limit.  Asked for once a device, and kept in known[device].
-inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int>* known, int* blocks) {
+inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int>* known, int* blocks,
+                                   int threads = kThreads) {
   int dev = 0, a_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -666,7 +686,7 @@ inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   // clusters of 16 blocks
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a_sm, kernel, kThreads, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a_sm, kernel, threads, smem);
   if (e != cudaSuccess) return e;
   *blocks = a_sm * sm_count();
   if (*blocks < 1) return cudaErrorInvalidConfiguration;
@@ -756,5 +776,9 @@ inline fa_status check_heads(const fa_cache* c, int32_t H) {
 
 cudaError_t launch_decode_bf16(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);
 cudaError_t launch_decode_fp32(const fa_cache& c, const Cut& k, const DecodeParams& a, cudaStream_t s);
+// fa_decode_e4m3 with tcgen05: whether it takes the problem.
+bool takes_sm103(const fa_cache& c, int H);
+Cut cut_e4m3_sm103(const fa_cache& c, int H);
+cudaError_t launch_e4m3_sm103(int d, const Cut& k, const E4m3Params& a, cudaStream_t s);
 
 }  // namespace fa

@@ -6,23 +6,16 @@
 // with scores in units of log 2 (the scale carries log2 e).
 //
 // Half the bytes of a bf16 cache for the same products: a row and head are 2 d
-// bytes against 4 d flops a query head.  HBM is still the bound with up to 16
-// query heads a key head, but the instructions for every byte are twice as many, so
-// here the design is about those as well.  How the work is shared out and
-// joined is in fa_decode.cuh.
+// bytes against 4 d flops a query head.  HBM should be the bound, but the instructions
+// for every byte are twice as many, so here the design is about those as
+// well.  How the work is shared out and joined is in fa_decode.cuh; large problems
+// with d 128 and 256 and few heads are those of fa_decode_e4m3_sm103.cu.
 
 #include "fa_decode.cuh"
 #include "fa_e4m3.cuh"
 
 namespace fa {
 namespace {
-
-struct E4m3Params : DecodeParams {
-  const float *KS, *VS;
-  FastDiv block_rows;
-  int blocks;           // of a page and head
-  int64_t page_scales;  // scales of a page
-};
 
 // A warp takes 16 kSub rows of each tile with mma.m16n8k16 in fp16, into which
 // e4m3 numbers go exactly, two at a time:
@@ -41,10 +34,11 @@ struct E4m3Params : DecodeParams {
 // largest.  fp32 ones become the sum of two, the second 2^11 times itself: it takes
 // the place of a second group of 8 heads, at no more products.
 //
-// Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers.  The maximum that
-// weights are taken against and U are moved only when a weight passes 2^kAhead
-// (its bits are not the fewer for that), so that almost every tile does without
-// the maximum over its lanes and without a look at the accumulators.
+// Weights: P b_j / U, U a power of two, as fp16 numbers: their 11 bits are an eighth of a half step of
+// a bf16 O.  With fp32 as the sum of two.  The maximum that weights are taken
+// against and U are moved only when a weight passes 2^kAhead (its bits are not
+// the fewer for that), so that almost every tile does without the maximum over its
+// lanes and without a look at the accumulators.
 template <int D, int NH, bool kF32>
 struct Mma8 {
   static constexpr int kSub = D <= 64 ? 2 : 1;
@@ -61,7 +55,7 @@ struct Mma8 {
   static constexpr int kScales = kRows * (kPitchK + kPitchV);  // then the scales of K and V, and which rows are there
   static constexpr int kSeen = kScales + kRows * 8;
   static constexpr int kStageBytes = kSeen + 16;
-  static constexpr int kBlocks = D == 16 ? 6 : D == 32 ? 5 : D == 256 ? 2 : 3;
+  static constexpr int kBlocks = D == 16 ? 5 : D == 32 ? 4 : D == 256 ? 2 : 3;
   static constexpr int kStages = D == 16 ? 5 : D == 96 ? 4 : 3;
   static constexpr int kVW = D % 64 || D == 256 ? (D == 16 ? 16 : 32) : 64;  // columns of O that are exchanged at a time
   static constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -99,10 +93,6 @@ __device__ __forceinline__ float2 lds8(uint32_t a) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
-
 // A warp's copies of its rows of each tile and of their scales, ahead of their use.
 template <class M>
 struct Loader8 {
@@ -433,8 +423,10 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
           l[u] += p[u][o][0] + p[u][o][1];
           const float w0 = w[u][o][0] * per_unit[u], w1 = w[u][o][1] * per_unit[u];
           hi[u][o] = pack_f16x2(w0, w1);
-          const float2 z = f16x2_to_float2(hi[u][o]);
-          lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
+          if constexpr (kF32) {
+            const float2 z = f16x2_to_float2(hi[u][o]);
+            lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
+          }
         }
       // V: pieces of 8 keys x 8 pairs of columns; lane 8 n + r names row r of piece n
       const uint32_t v_at = tile + M::kRows * M::kPitchK + ((lane & 7) + (lane >> 3 & 1) * 8) * M::kPitchV + (lane >> 4) * 16;
@@ -456,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
               mma16816_f16(acc[u][c + i], a0, a1, a2, a3, hi[u][2 * b], hi[u][2 * b + 1]);
-              mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
+              if (kF32) mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
             }
           }
         }
@@ -566,7 +558,7 @@ Cut cut_d(const fa_cache& c, int H) {
   using M = Mma8<D, 1, true>;
   return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks);
 }
-Cut cut_e4m3(const fa_cache& c, int H) {
+Cut cut_mma(const fa_cache& c, int H) {
   switch (c.d) {
     case 16: return cut_d<16>(c, H);
     case 32: return cut_d<32>(c, H);
@@ -575,6 +567,13 @@ Cut cut_e4m3(const fa_cache& c, int H) {
     case 128: return cut_d<128>(c, H);
     default: return cut_d<256>(c, H);
   }
+}
+
+// Whether the kernels of fa_decode_e4m3_sm103.cu take the problem.
+bool large(const fa_cache& c, int H, const Cut& k) { return k.cluster == 0 && takes_sm103(c, H); }
+Cut cut_e4m3(const fa_cache& c, int H) {
+  const Cut k = cut_mma(c, H);
+  return large(c, H, k) ? cut_e4m3_sm103(c, H) : k;
 }
 
 fa_status check(const fa_cache* c, int32_t block_rows, int32_t H) {
@@ -615,7 +614,9 @@ fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float
   a.block_rows = fa::FastDiv(block_rows);
   a.blocks = c->page_rows / block_rows;
   a.page_scales = (int64_t)c->H_kv * a.blocks;
+  a.wait_ns = fa::wait_limit_ns();
   const cudaStream_t s = (cudaStream_t)stream;
+  if (fa::large(*c, H, fa::cut_mma(*c, H))) return fa::status_of(fa::launch_e4m3_sm103(c->d, k, a, s));
   cudaError_t e = cudaErrorInvalidValue;
   switch (c->d) {
     case 16: e = fa::launch_d<16>(*c, k, a, s); break;

@@ -22,6 +22,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
   return pack_e4m3x2(a, b) | pack_e4m3x2(c, d) << 16;
 }
+// Two fp16 numbers to e4m3, in the same way.
+__device__ __forceinline__ uint32_t pack_e4m3x2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
 // The numbers in bits 0-15 and in bits 16-31 as two fp16 each, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_lo(uint32_t x) {
   uint32_t r;

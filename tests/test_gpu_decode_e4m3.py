@@ -5,17 +5,19 @@ and graphs.
 
 Tolerances are bounds, not fits.  With u = 2^-24, a score is a sum of d
 products whose absolute sum is at most A (as the oracle returns it), summed in
-fp32 with at most 2u of the sum an addition.  Queries are multiplied as fp16
-numbers of a common power of two: bf16 ones exactly but for 2^-39 of the
-largest, fp32 ones as two, 2^-22 of their value.  Three products follow.  So
-  e_s <= (2 d + 8) u A + e_q A,  e_q = 2^-22 in fp32, d 2^-36 in bf16
-(the queries below lie within 2^3 of one another, so 2^-39 of the largest is at most
-d 2^-36 of A).  A weight is off by e_s plus the rounding of its exponent's product
-(4 u A), 2^-21 of the hardware exponential and 2^-21 as it is multiplied as the
-sum of two fp16 numbers.  Both the weighted sum and the sum of weights carry
+fp32 with at most 2u of the sum an addition.  Queries are multiplied as sums of
+e4m3 numbers in units of a common power of two, three for bf16 and six for fp32,
+each of which leaves at most 2^-4 of what it holds: bf16 ones (8 bits) within 2^-19 of the largest
+of their head are exact, fp32 ones off by 2^-24.  Adding the terms up and three
+products follow.  So
+  e_s <= (2 d + 8) u A + e_q A,  e_q = 2^-24 in fp32, 0 in bf16.
+A weight is off by e_s plus the rounding of its exponent's product (4 u A), 2^-21 of
+the hardware exponential and what it loses as it is multiplied: in bf16 it is
+rounded to fp16 (2^-11) and then held as three terms (2^-12), in fp32 as six
+(2^-24) after two products.  Both the weighted sum and the sum of weights carry
 that error and at most 2 u n of their additions, so
   |O - ref| <= half a step of the output type * |ref| + 2 V (e_w + 2 (n + 64) u)
-  |L - ref| <= e_s + e_w + 2 (n + 64) u + 8 u |L|
+  |L - ref| <= e_s + e_l + 2 (n + 64) u + 8 u |L|,  e_l as e_w without the multiplied weights' loss
 with V the largest |v|, n the number of rows and 64 for the joining of parts."""
 
 import numpy as np
@@ -88,15 +90,16 @@ def check(got, q, kp, vp, ks, vs, table, lengths, scale):
     k, v = (np.nan_to_num(values(f64(p), f64(s))) for p, s in ((kp, ks), (vp, vs)))
     ref, Lr, A, V = decode(f64(q)[:, :, 0], k, v, table.cpu().numpy(), lengths.cpu().numpy(), float(np.float32(scale)))
     n = lengths.cpu().clamp(min=0).numpy()[:, None]
-    e_s = (2 * d + 8) * U * A + (2.0 ** -22 if q.dtype == torch.float32 else d * 2.0 ** -36) * A
-    e_w = e_s + 4 * U * A + 2.0 ** -20
+    e_s = (2 * d + 8) * U * A + (U * A if q.dtype == torch.float32 else 0)
+    e_l = e_s + 4 * U * A + 2.0 ** -21
+    e_w = e_l + (2 * U + U if q.dtype == torch.float32 else 2.0 ** -11 + 2.0 ** -12)
     tol_o = HALF_STEP[q.dtype] * np.abs(ref) + (2 * V * (e_w + 2 * (n + 64) * U))[:, :, None]
     x, y = f64(o)[:, :, 0], f64(L)[:, :, 0]
     assert np.isfinite(x).all()
     assert (np.abs(x - ref) <= tol_o).all(), float((np.abs(x - ref) - tol_o).max())
     empty = np.isinf(Lr)
     assert (x[empty] == 0).all() and np.array_equal(np.isposinf(y), empty)
-    tol_l = e_s + e_w + 2 * (n + 64) * U + 8 * U * np.abs(np.where(empty, 0, Lr))
+    tol_l = e_s + e_l + 2 * (n + 64) * U + 8 * U * np.abs(np.where(empty, 0, Lr))
     assert (np.abs(y[~empty] - Lr[~empty]) <= tol_l[~empty]).all(), float(np.abs(y[~empty] - Lr[~empty]).max())
 
 
