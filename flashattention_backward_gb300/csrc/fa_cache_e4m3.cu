@@ -8,7 +8,10 @@
 // scale costs nothing but what falls below e4m3's smallest normal number; a
 // number of 4 significant bits is not held better by t / 448 itself.
 //
-// Both kernels move bytes: HBM is their bound.
+// Both kernels move bytes and HBM is their bound, as long as the instructions are
+// few: a thread takes 16 numbers of a row at a time, 32 or 64 bytes outside and 16 in
+// the cache, and keeps what it has read in registers from the search for t to
+// the rounding.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -18,7 +21,8 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kKeep = 4;  // units of 16 numbers that a thread keeps
 
 struct AppendParams {
   const char* X[2];   // K, V
@@ -27,44 +31,108 @@ struct AppendParams {
   const int32_t *table, *start, *counts;
   int32_t* status;
   FastDiv many, heads, page_rows, block_rows, row_units;
+  uint32_t teams;      // S * H_kv * many
   int rows, num_pages, max_pages;
+  bool wide;           // rows begin on 32 bytes
   int64_t table_stride;
   int64_t sb, sh, sn;  // byte strides of the new rows
   int64_t pp, ph, pn;  // of the pools
 };
 
-// 16 numbers of a row
+// 16 numbers of a row, as they are
 template <class T>
-__device__ __forceinline__ void load16(const char* p, float (&x)[16]) {
-  const uint4* v = reinterpret_cast<const uint4*>(p);
+struct Unit {
+  static constexpr int kWords = 16 * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const char* p, bool wide) {
+    if (wide) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T); ++i) {
-    const uint4 y = v[i];
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[8 * i + 2 * e] = ptx::bf16lo(w[e]), x[8 * i + 2 * e + 1] = ptx::bf16hi(w[e]);
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                       "=r"(w[i + 6]), "=r"(w[i + 7])
+                     : "l"(p + 4 * i));
     } else {
-      x[4 * i] = __uint_as_float(y.x), x[4 * i + 1] = __uint_as_float(y.y);
-      x[4 * i + 2] = __uint_as_float(y.z), x[4 * i + 3] = __uint_as_float(y.w);
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
     }
   }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return i % 2 ? ptx::bf16hi(w[i / 2]) : ptx::bf16lo(w[i / 2]);
+  }
+  // the bits of the largest |x|, NaN apart, and 0x7f800000 if one is infinite
+  __device__ __forceinline__ uint32_t top() const {
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) t = __hmax2(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+      const float m = fmaxf(__low2float(t), __high2float(t));
+      return isnan(m) ? 0u : __float_as_uint(m);
+    } else {
+      float m = fabsf(at(0));
+#pragma unroll
+      for (int i = 1; i < 16; ++i) m = fmaxf(m, fabsf(at(i)));
+      return isnan(m) ? 0u : __float_as_uint(m);
+    }
+  }
+  // the same of the finite numbers
+  __device__ __forceinline__ uint32_t finite_top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = __float_as_uint(at(i)) & 0x7fffffffu;
+      t = max(t, x < 0x7f800000u ? x : 0u);
+    }
+    return t;
+  }
+  // times `by`, a power of two, to e4m3; infinities become NaN (only looked at if there are any)
+  __device__ __forceinline__ uint4 quantised(float by, bool infinite) const {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = at(i) * by;
+    if (infinite) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = isinf(at(i)) ? NAN : x[i];
+    }
+    return make_uint4(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]),
+                      pack_e4m3x4(x[8], x[9], x[10], x[11]), pack_e4m3x4(x[12], x[13], x[14], x[15]));
+  }
+};
+
+// The largest over a team, a warp or a block.
+template <int kTeam>
+__device__ __forceinline__ uint32_t over_team(uint32_t x) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if constexpr (kTeam > 32) {
+    __shared__ uint32_t tops[kThreads / 32];
+    __syncthreads();  // the last call's readers are done
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) x = max(x, tops[w]);
+  }
+  return x;
 }
 
-// Block of threads (x, y): the x-th touched block of a sequence and head, of K or V.
-template <class T>
+// A team of kTeam threads, a warp or a block, takes one touched block of rows of a sequence and head, of K or V (y).
+template <class T, int kTeam>
 __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const AppendParams a) {
   after_stream();
-  __shared__ uint32_t tops[kThreads / 32];
+  const uint32_t team = kTeam == 32 ? (blockIdx.x * kThreads + threadIdx.x) / 32 : blockIdx.x;
+  const int thread = threadIdx.x % kTeam;
+  if (team >= a.teams) return;
   uint32_t nth, g;
-  const uint32_t s = a.heads.div(a.many.div(blockIdx.x, &nth), &g);
+  const uint32_t s = a.heads.div(a.many.div(team, &nth), &g);
   const int pool = blockIdx.y;
-  const bool first_of_s = nth == 0 && g == 0 && pool == 0 && threadIdx.x == 0;
   const int64_t start = a.start[s];
   int count = a.rows;
   if (a.counts) {
     const int given = a.counts[s];
-    if ((given < 0 || given > count) && first_of_s) report_pages(a.status);
+    if ((given < 0 || given > count) && nth == 0 && g == 0 && pool == 0 && thread == 0) report_pages(a.status);
     count = min(max(given, 0), count);
   }
   if (start < 0) return;
@@ -75,60 +143,84 @@ __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const AppendParam
   const int64_t col = lo < (int64_t(1) << 31) ? (int64_t)a.page_rows.div((uint32_t)lo) : a.max_pages;
   int page = -1;
   if (col < a.max_pages) page = a.table[s * a.table_stride + col];
+
+  // the rows do not wait for their page
+  const char* src = a.X[pool] + s * a.sb + g * a.sh + (from - start) * a.sn;
+  const uint32_t units = (uint32_t)(to - from) * a.row_units.d;
+  auto place = [&](uint32_t u, uint32_t* row) {
+    uint32_t c;
+    *row = a.row_units.div(u, &c);
+    return c * 16;
+  };
+  Unit<T> x[kKeep];
+  uint32_t row, top = 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const uint32_t u = k * kTeam + thread;
+    if (u >= units) continue;
+    const uint32_t c = place(u, &row);
+    x[k].load(src + row * a.sn + c * sizeof(T), a.wide);
+  }
   if (page < 0 || page >= a.num_pages) {
-    if (threadIdx.x == 0) report_pages(a.status);
+    if (thread == 0) report_pages(a.status);
     return;
   }
   const int row0 = (int)(lo - col * a.page_rows.d);
   uint8_t* dst = a.pages[pool] + page * a.pp + g * a.ph + row0 * a.pn;
-  float* scale_at = a.scales[pool] + ((int64_t)page * a.heads.d + g) * (a.page_rows.d / br) + row0 / br;
-  const char* src = a.X[pool] + s * a.sb + g * a.sh + (from - start) * a.sn;
-
-  const int units = (int)(to - from) * a.row_units.d;
-  uint32_t top = 0;
-  for (int u = threadIdx.x; u < units; u += kThreads) {
-    uint32_t c;
-    const uint32_t r = a.row_units.div(u, &c);
-    float x[16];
-    load16<T>(src + r * a.sn + c * 16 * sizeof(T), x);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t t = __float_as_uint(x[e]) & 0x7fffffffu;
-      top = max(top, t < 0x7f800000u ? t : 0u);
-    }
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+  float* scale_at = a.scales[pool] + ((int64_t)page * a.heads.d + g) * (a.page_rows.d / br) + a.block_rows.div(row0);
   const float old = from > lo ? *scale_at : 0.f;
-  __syncthreads();  // everyone has the old scale
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = max(top, tops[w]);
+  for (int k = 0; k < kKeep; ++k)
+    if (k * kTeam + thread < units) top = max(top, x[k].top());
+  // a block that is too large to be kept is read twice
+  for (uint32_t u = kKeep * kTeam + thread; u < units; u += kTeam) {
+    Unit<T> y;
+    const uint32_t c = place(u, &row);
+    y.load(src + row * a.sn + c * sizeof(T), a.wide);
+    top = max(top, y.top());
+  }
+  top = over_team<kTeam>(top);
+  const bool infinite = top >= 0x7f800000u;
+  if (infinite) {  // once more, without what is not finite
+    top = 0;
+    for (uint32_t u = thread; u < units; u += kTeam) {
+      Unit<T> y;
+      const uint32_t c = place(u, &row);
+      y.load(src + row * a.sn + c * sizeof(T), a.wide);
+      top = max(top, y.finite_top());
+    }
+    top = over_team<kTeam>(top);
+  }
   const float scale = fmaxf(scale_for(top), old), inv = inverse(scale);
-  if (threadIdx.x == 0) *scale_at = scale;
-  for (int u = threadIdx.x; u < units; u += kThreads) {
-    uint32_t c;
-    const uint32_t r = a.row_units.div(u, &c);
-    float x[16];
-    load16<T>(src + r * a.sn + c * 16 * sizeof(T), x);
-    uint32_t w[4];
+  // everyone of the team has read the old scale: a warp in step, a block at its barriers
+  if (kTeam == 32) __syncwarp();
+  if (thread == 0) *scale_at = scale;
+  uint8_t* new_rows = dst + (from - lo) * a.pn;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = isfinite(x[e]) ? x[e] * inv : NAN;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = pack_e4m3x4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-    *reinterpret_cast<uint4*>(dst + (from - lo + r) * a.pn + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int k = 0; k < kKeep; ++k) {
+    const uint32_t u = k * kTeam + thread;
+    if (u >= units) continue;
+    const uint32_t c = place(u, &row);
+    *reinterpret_cast<uint4*>(new_rows + row * a.pn + c) = x[k].quantised(inv, infinite);
+  }
+  for (uint32_t u = kKeep * kTeam + thread; u < units; u += kTeam) {
+    Unit<T> y;
+    const uint32_t c = place(u, &row);
+    y.load(src + row * a.sn + c * sizeof(T), a.wide);
+    *reinterpret_cast<uint4*>(new_rows + row * a.pn + c) = y.quantised(inv, infinite);
   }
   if (from > lo && scale > old) {
     const float by = old * inv;
-    for (int u = threadIdx.x; u < (int)(from - lo) * (int)a.row_units.d; u += kThreads) {
-      uint32_t c;
-      const uint32_t r = a.row_units.div(u, &c);
-      uint4* at = reinterpret_cast<uint4*>(dst + r * a.pn + c * 16);
+    const uint32_t before = (uint32_t)(from - lo) * a.row_units.d;
+    for (uint32_t u = thread; u < before; u += kTeam) {
+      const uint32_t c = place(u, &row);
+      uint4* at = reinterpret_cast<uint4*>(dst + row * a.pn + c);
       const uint4 q = *at;
       uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float4 x = e4m3x4_to_float4(w[e]);
-        w[e] = pack_e4m3x4(x.x * by, x.y * by, x.z * by, x.w * by);
+        const float4 y = e4m3x4_to_float4(w[e]);
+        w[e] = pack_e4m3x4(y.x * by, y.y * by, y.z * by, y.w * by);
       }
       *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -145,70 +237,110 @@ struct ReadParams {
   uint32_t total_rows;  // S * H_kv * rows
   int block_of_rows;    // rows that a block of threads takes
   int num_pages, max_pages;
+  bool wide;            // rows outside begin on 32 bytes
   int64_t table_stride;
   int64_t sb, sh, sn;   // byte strides of the rows outside
   int64_t pp, ph, pn;   // of the pools
 };
 
-template <class T>
+// A thread takes kUnits units of 16 numbers, of K and of V.
+template <class T, int kUnits>
 __global__ void __launch_bounds__(kThreads) read_e4m3_kernel(const ReadParams a) {
   after_stream();
-  uint32_t c, i, g;
-  const uint32_t r = a.row_units.div(threadIdx.x, &c);
-  const uint32_t row = blockIdx.x * (uint32_t)a.block_of_rows + r;
-  if (r >= (uint32_t)a.block_of_rows || row >= a.total_rows) return;
-  const uint32_t s = a.heads.div(a.rows.div(row, &i), &g);
-  const bool first_of_s = c == 0 && i == 0 && g == 0;
-  const int64_t start = a.start ? a.start[s] : 0;
-  int count = (int)a.rows.d;
-  if (a.counts) {
-    const int given = a.counts[s];
-    if ((given < 0 || given > count) && first_of_s) report_pages(a.status);
-    count = min(max(given, 0), count);
-  }
-  if (start < 0 && first_of_s) report_pages(a.status);
-  bool on = start >= 0 && (int)i < count;
-  int64_t from = 0, scale_at = 0;
-  if (on) {
+  int64_t from[kUnits], to[kUnits], scale_at[kUnits];
+  bool there[kUnits], on[kUnits];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    uint32_t c, i, g;
+    const uint32_t r = a.row_units.div(k * kThreads + threadIdx.x, &c);
+    const uint32_t row = blockIdx.x * (uint32_t)a.block_of_rows + r;
+    there[k] = r < (uint32_t)a.block_of_rows && row < a.total_rows;
+    on[k] = false;
+    if (!there[k]) continue;
+    const uint32_t s = a.heads.div(a.rows.div(row, &i), &g);
+    const bool first_of_s = c == 0 && i == 0 && g == 0;
+    const int64_t start = a.start ? a.start[s] : 0;
+    int count = (int)a.rows.d;
+    if (a.counts) {
+      const int given = a.counts[s];
+      if ((given < 0 || given > count) && first_of_s) report_pages(a.status);
+      count = min(max(given, 0), count);
+    }
+    if (start < 0 && first_of_s) report_pages(a.status);
+    to[k] = s * a.sb + g * a.sh + i * a.sn + c * 16 * (int)sizeof(T);
+    on[k] = start >= 0 && (int)i < count;
+    if (!on[k]) continue;
     const int64_t pos = start + i;
     const int64_t col = pos < (int64_t(1) << 31) ? (int64_t)a.page_rows.div((uint32_t)pos) : a.max_pages;
     int page = -1;
     if (col < a.max_pages) page = a.table[s * a.table_stride + col];
-    on = page >= 0 && page < a.num_pages;
-    if (!on && c == 0) report_pages(a.status);
-    if (on) {
-      const int in_page = (int)(pos - col * a.page_rows.d);
-      from = page * a.pp + g * a.ph + in_page * a.pn + c * 16;
-      scale_at = ((int64_t)page * a.heads.d + g) * (a.page_rows.d / a.block_rows.d) + a.block_rows.div(in_page);
-    }
+    on[k] = page >= 0 && page < a.num_pages;
+    if (!on[k] && c == 0) report_pages(a.status);
+    if (!on[k]) continue;
+    const int in_page = (int)(pos - col * a.page_rows.d);
+    from[k] = page * a.pp + g * a.ph + in_page * a.pn + c * 16;
+    scale_at[k] = ((int64_t)page * a.heads.d + g) * (a.page_rows.d / a.block_rows.d) + a.block_rows.div(in_page);
   }
-  const int64_t to = s * a.sb + g * a.sh + i * a.sn + c * 16 * (int)sizeof(T);
+  uint4 q[2][kUnits];
+  float scale[2][kUnits];
 #pragma unroll
-  for (int pool = 0; pool < 2; ++pool) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    if (on) {
-      q = *reinterpret_cast<const uint4*>(a.pages[pool] + from);
-      scale = a.scales[pool][scale_at];
-    }
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint4* dst = reinterpret_cast<uint4*>(a.X[pool] + to);
-    float4 x[4];
+  for (int k = 0; k < kUnits; ++k)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = e4m3x4_to_float4(w[e]);
-      x[e] = on ? make_float4(x[e].x * scale, x[e].y * scale, x[e].z * scale, x[e].w * scale) : make_float4(0, 0, 0, 0);
+    for (int pool = 0; pool < 2; ++pool) {
+      q[pool][k] = make_uint4(0, 0, 0, 0);
+      scale[pool][k] = 0.f;
+      if (!on[k]) continue;
+      q[pool][k] = *reinterpret_cast<const uint4*>(a.pages[pool] + from[k]);
+      scale[pool][k] = a.scales[pool][scale_at[k]];
     }
 #pragma unroll
-    for (int e = 0; e < (int)sizeof(T); ++e) {
-      if constexpr (sizeof(T) == 2)
-        dst[e] = make_uint4(ptx::pack_bf16x2(x[2 * e].x, x[2 * e].y), ptx::pack_bf16x2(x[2 * e].z, x[2 * e].w),
-                            ptx::pack_bf16x2(x[2 * e + 1].x, x[2 * e + 1].y), ptx::pack_bf16x2(x[2 * e + 1].z, x[2 * e + 1].w));
-      else
-        *reinterpret_cast<float4*>(dst + e) = x[e];
+  for (int k = 0; k < kUnits; ++k)
+#pragma unroll
+    for (int pool = 0; pool < 2; ++pool) {
+      if (!there[k]) continue;
+      const uint32_t w[4] = {q[pool][k].x, q[pool][k].y, q[pool][k].z, q[pool][k].w};
+      constexpr int kWords = 16 * sizeof(T) / 4;
+      uint32_t out[kWords];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float4 x = e4m3x4_to_float4(w[e]);
+        const float by = scale[pool][k];
+        // nothing is read: 0 times 0
+        x = make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
+        if constexpr (sizeof(T) == 2) {
+          out[2 * e] = ptx::pack_bf16x2(x.x, x.y), out[2 * e + 1] = ptx::pack_bf16x2(x.z, x.w);
+        } else {
+          out[4 * e] = __float_as_uint(x.x), out[4 * e + 1] = __float_as_uint(x.y);
+          out[4 * e + 2] = __float_as_uint(x.z), out[4 * e + 3] = __float_as_uint(x.w);
+        }
+      }
+      char* dst = a.X[pool] + to[k];
+      if (a.wide) {
+#pragma unroll
+        for (int e = 0; e < kWords; e += 8)
+          ptx::st_global_v8(dst + 4 * e, out[e], out[e + 1], out[e + 2], out[e + 3], out[e + 4], out[e + 5], out[e + 6], out[e + 7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kWords; e += 4)
+          *reinterpret_cast<uint4*>(dst + 4 * e) = make_uint4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+      }
     }
-  }
 }
+
+// Whether rows begin on 32 bytes.
+bool on_32(const void* K, const void* V, int64_t sb, int64_t sh, int64_t sn) {
+  return ((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V) | (uint64_t)sb | (uint64_t)sh | (uint64_t)sn) & 31u) == 0;
+}
+
+template <class T>
+cudaError_t launch_append(const AppendParams& a, int most_units, cudaStream_t s) {
+  // a warp keeps kKeep * 32 units
+  if (most_units <= kKeep * 32)
+    return launch_early(append_e4m3_kernel<T, 32>, dim3((unsigned)ceil_div(a.teams, kThreads / 32), 2), kThreads, 0, s, 1, a);
+  return launch_early(append_e4m3_kernel<T, kThreads>, dim3(a.teams, 2), kThreads, 0, s, 1, a);
+}
+
+constexpr int kReadUnits = 2;
 
 // Arguments that both calls take.
 fa_status check_rows(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K, const void* V, int64_t ss,
@@ -265,12 +397,12 @@ fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t ro
   a.pp = c->stride_page;
   a.ph = c->stride_h;
   a.pn = c->stride_n;
-  // many <= rows, so the blocks are fewer than 2^31
-  const dim3 grid((unsigned)((int64_t)c->S * c->H_kv * many), 2);
+  a.teams = (uint32_t)((int64_t)c->S * c->H_kv * many);  // many <= rows, so fewer than 2^31
+  a.wide = fa::on_32(K, V, a.sb, a.sh, a.sn);
+  const int64_t most_units = (int64_t)(rows < block_rows ? rows : block_rows) * (c->d / 16);
+  const int units = (int)(most_units < (1 << 30) ? most_units : 1 << 30);
   const cudaStream_t s = (cudaStream_t)stream;
-  return fa::status_of(c->dtype == FA_BF16
-                           ? fa::launch_early(fa::append_e4m3_kernel<__nv_bfloat16>, grid, fa::kThreads, 0, s, 1, a)
-                           : fa::launch_early(fa::append_e4m3_kernel<float>, grid, fa::kThreads, 0, s, 1, a));
+  return fa::status_of(c->dtype == FA_BF16 ? fa::launch_append<__nv_bfloat16>(a, units, s) : fa::launch_append<float>(a, units, s));
 }
 
 fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K_pages,
@@ -297,7 +429,8 @@ fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows
   a.page_rows = fa::FastDiv(c->page_rows);
   a.block_rows = fa::FastDiv(block_rows);
   a.total_rows = (uint32_t)((int64_t)c->S * c->H_kv * rows);
-  a.block_of_rows = fa::kThreads / (c->d / 16);
+  a.block_of_rows = fa::kReadUnits * fa::kThreads / (c->d / 16);
+  a.wide = fa::on_32(K, V, stride_s * es, stride_h * es, stride_n * es);
   a.num_pages = c->num_pages;
   a.max_pages = c->max_pages;
   a.table_stride = c->table_stride;
@@ -310,8 +443,8 @@ fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows
   const dim3 grid((unsigned)fa::ceil_div(a.total_rows, a.block_of_rows));
   const cudaStream_t s = (cudaStream_t)stream;
   return fa::status_of(c->dtype == FA_BF16
-                           ? fa::launch_early(fa::read_e4m3_kernel<__nv_bfloat16>, grid, fa::kThreads, 0, s, 1, a)
-                           : fa::launch_early(fa::read_e4m3_kernel<float>, grid, fa::kThreads, 0, s, 1, a));
+                           ? fa::launch_early(fa::read_e4m3_kernel<__nv_bfloat16, fa::kReadUnits>, grid, fa::kThreads, 0, s, 1, a)
+                           : fa::launch_early(fa::read_e4m3_kernel<float, fa::kReadUnits>, grid, fa::kThreads, 0, s, 1, a));
 }
 
 }  // extern "C"
