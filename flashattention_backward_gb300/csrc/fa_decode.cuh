@@ -95,7 +95,7 @@ __device__ __forceinline__ int tiles_of(int rows) {
 // kItemCost + n units of work, and the runs are of equal units.  A run that
 // begins inside the first kItemCost units of an item begins with its first
 // tile.  So a run may be empty only between two items, never inside one.  1 is
-// what measured best: 32 sequences of up to 2048 rows, 32 heads of d 64 (items
+// what measured best for rows as they are (those in 8 bits have a kCost of their own): 32 sequences of up to 2048 rows, 32 heads of d 64 (items
 // of up to 32 tiles) took 56.5 us with 0, 46.3 with 1, 46.5 with 2, 47.4 with 3.
 constexpr int kItemCost = 1;
 
@@ -189,13 +189,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* sums, int64_t*
 // The sequences' units, summed over a block of NT threads.  Thread t looks at
 // sequences t, t + NT, ...: up to NT of them are loaded and summed once, of more
 // the sums are taken twice, for the total and for a place among them.
-template <int kTile, int NT>
+template <int kTile, int NT, int kCost>
 struct Units {
   const DecodeParams& a;
   int64_t* sums;     // NT / 32 entries of shared memory
   int64_t n, lo, all;  // of the first NT sequences: this thread's, those before it, all
   __device__ __forceinline__ int64_t of(int s) const {
-    return s < a.S ? (int64_t)(kItemCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
+    return s < a.S ? (int64_t)(kCost + tiles_of<kTile>(rows_of(a, s))) * a.items : 0;
   }
   __device__ __forceinline__ Units(const DecodeParams& p, int64_t* shared) : a(p), sums(shared) { restart(); }
   // the first NT sequences once more: find() goes on from them
@@ -238,7 +238,7 @@ struct Units {
 
 // A place in the row of tiles: tile t of item `item` of sequence s, which is
 // unit `unit` of all.
-template <int kTile>
+template <int kTile, int kCost = kItemCost>
 struct Place {
   int s, item, t, rows, tiles;
   int64_t unit;
@@ -247,22 +247,53 @@ struct Place {
     s = seq;
     rows = rows_of(a, s);
     tiles = tiles_of<kTile>(rows);
-    item = (int)divide(x - base, kItemCost + tiles);
-    const int64_t begin = base + (int64_t)item * (kItemCost + tiles);
-    t = max((int)(x - begin) - kItemCost, 0);
-    unit = begin + kItemCost + t;
+    item = (int)divide(x - base, kCost + tiles);
+    const int64_t begin = base + (int64_t)item * (kCost + tiles);
+    t = max((int)(x - begin) - kCost, 0);
+    unit = begin + kCost + t;
   }
   __device__ __forceinline__ void next(const DecodeParams& a) {
     ++unit;
     if (++t < tiles) return;
     t = 0;
-    unit += kItemCost;
+    unit += kCost;
     if (++item < a.items) return;
     item = 0;
     if (++s < a.S) {
       rows = rows_of(a, s);
       tiles = tiles_of<kTile>(rows);
     }
+  }
+};
+
+// A way through a run, item by item.
+template <int kTile, int kCost = kItemCost>
+struct Walk {
+  int s, item, t;       // the item's sequence and head, and its first tile that is the run's
+  int rows, tiles;      // of the item
+  int count;            // of its tiles, those that are the run's
+  int rows_next;        // of the next sequence, asked for in time
+  int64_t unit, end;    // of tile t; the run's
+  __device__ __forceinline__ void begin(const DecodeParams& a, const Place<kTile, kCost>& at, int64_t e) {
+    s = at.s, item = at.item, t = at.t, rows = at.rows, tiles = at.tiles, unit = at.unit, end = e;
+    count = (int)min((int64_t)(tiles - t), end - unit);
+    rows_next = s + 1 < a.S ? rows_of(a, s + 1) : 0;
+  }
+  __device__ __forceinline__ bool some() const { return unit < end; }
+  // the next item; false if the run ends before it has a tile
+  __device__ __forceinline__ bool next(const DecodeParams& a) {
+    unit += tiles - t + kCost;
+    t = 0;
+    if (unit >= end) return false;
+    if (++item == a.items) {
+      item = 0;
+      ++s;
+      rows = rows_next;
+      tiles = tiles_of<kTile>(rows);
+      if (s + 1 < a.S) rows_next = rows_of(a, s + 1);
+    }
+    count = (int)min((int64_t)tiles, end - unit);
+    return true;
   }
 };
 
@@ -397,10 +428,10 @@ struct Loader {
 };
 
 // This block's run: its first tile and its last unit; false if it has none.
-template <int kTile>
-__device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, int64_t* end) {
+template <int kTile, int kCost>
+__device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile, kCost>* at, int64_t* end) {
   __shared__ int64_t sums[kWarps];
-  Units<kTile, kThreads> units(a, sums);
+  Units<kTile, kThreads, kCost> units(a, sums);
   const Share share = units.share();
   const int run = blockIdx.x / a.split;
   if (run >= share.runs()) return false;
@@ -414,8 +445,8 @@ __device__ __forceinline__ bool run_of(const DecodeParams& a, Place<kTile>* at, 
 
 // With a cluster an item (and piece of its heads): this block's tiles of its item, the k-th of n equal
 // shares; false if it has none.
-template <int kTile>
-__device__ __forceinline__ bool share_of_item(const DecodeParams& a, Place<kTile>* at, int64_t* end) {
+template <int kTile, int kCost>
+__device__ __forceinline__ bool share_of_item(const DecodeParams& a, Place<kTile, kCost>* at, int64_t* end) {
   const int k = blockIdx.x % a.cluster, n = blockIdx.x / a.cluster / a.split;
   at->s = n / a.items;
   at->item = n - at->s * a.items;
@@ -490,7 +521,7 @@ struct JoinShape {
   int slices;    // blocks that a head's columns are cut into; 1 if together > 1
 };
 
-template <class T, int D, int kTile>
+template <class T, int D, int kTile, int kCost>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams a,
                                                                    const JoinShape j) {
   constexpr int kAhead = 8;
@@ -499,7 +530,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   __shared__ int64_t sums[kJoinThreads / 32];
   int s = 0, item = 0, run = 0, slot = 0, following = 0;
   {
-    Units<kTile, kJoinThreads> units(a, sums);
+    Units<kTile, kJoinThreads, kCost> units(a, sums);
     const Share share = units.share();
     int64_t base = 0;
     if (j.by_item) {
@@ -509,11 +540,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     } else if ((int)blockIdx.x < share.runs()) {
       const int64_t x = share.first(blockIdx.x + 1) - 1;
       s = units.find(x, 0, &base);
-      item = (int)divide(x - base, kItemCost + tiles_of<kTile>(rows_of(a, s)));
+      item = (int)divide(x - base, kCost + tiles_of<kTile>(rows_of(a, s)));
     }
-    const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kItemCost + tiles);
-    run = share.run_of(begin + kItemCost);
-    if (j.by_item || run == (int)blockIdx.x) following = share.run_of(begin + kItemCost + tiles - 1) - run;
+    const int64_t tiles = tiles_of<kTile>(rows_of(a, s)), begin = base + item * (kCost + tiles);
+    run = share.run_of(begin + kCost);
+    if (j.by_item || run == (int)blockIdx.x) following = share.run_of(begin + kCost + tiles - 1) - run;
     // a run that holds tiles before the item has it as its second part
     slot = share.first(run) < begin ? 1 : 0;
   }
@@ -592,8 +623,9 @@ struct Cut {
   int split, piece_heads, part_heads;  // pieces of a group, heads of a piece, the same rounded up
   int64_t tiles, most_tiles;          // at most: of all items, of one
   int cluster;                        // blocks an item, or 0: runs
-  // units are tiles and kItemCost for every item, and no item has less than one tile
-  int64_t units() const { return tiles * (1 + kItemCost); }
+  int cost = kItemCost;
+  // units are tiles and cost for every item, and no item has less than one tile
+  int64_t units() const { return tiles * (1 + cost); }
   int64_t parts() const { return 2 * (units() * split < kMaxRuns ? units() * split : kMaxRuns); }
 };
 
@@ -630,7 +662,8 @@ inline Cut pieces_of(int group, int most) {
   k.part_heads = k.piece_heads <= 8 ? 8 : 16;
   return k;
 }
-inline Cut cut_tiles(Cut k, const fa_cache& c, int tile, int an_sm) {
+inline Cut cut_tiles(Cut k, const fa_cache& c, int tile, int an_sm, int cost = kItemCost) {
+  k.cost = cost;
   k.most_tiles = ceil_div(cache_rows(c), tile);
   k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
   k.cluster = cluster_of(an_sm, (int64_t)c.S * c.H_kv * k.split, k.most_tiles);
@@ -657,7 +690,7 @@ inline int runs_of(const Cut& k, int resident, DecodeParams* a) {
   return (int)(k.units() < resident ? k.units() : resident);
 }
 
-template <class T, int D, int kTile>
+template <class T, int D, int kTile, int kCost>
 cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStream_t s) {
   const int64_t items = (int64_t)a.S * a.items;
   JoinShape j = {items <= runs, k.part_heads, 1, 1};
@@ -671,7 +704,7 @@ cudaError_t launch_join(const Cut& k, const DecodeParams& a, int runs, cudaStrea
          kMost / (2 * j.together) * 8 >= runs / x + 2)
     j.together *= 2;
   const dim3 grid((unsigned)x, (unsigned)(ceil_div(a.group, j.together) * j.slices));
-  return launch_early(decode_join_kernel<T, D, kTile>, grid, kJoinThreads, 0, s, 1, a, j);
+  return launch_early(decode_join_kernel<T, D, kTile, kCost>, grid, kJoinThreads, 0, s, 1, a, j);
 }
 
 // How many blocks of a kernel the device holds at a time; raises the kernel's
@@ -696,7 +729,7 @@ inline cudaError_t resident_blocks(const void* kernel, int smem, std::atomic<int
 
 // Launches `alone` with a cluster an item, or `kernel` with a block a run and the join.
 // P: DecodeParams, or what goes on from there.
-template <class T, int D, int kTile, class P>
+template <class T, int D, int kTile, int kCost = kItemCost, class P>
 cudaError_t launch_decode(const Cut& k, P a, void (*kernel)(P), void (*alone)(P), int smem,
                           std::atomic<int>* known, std::atomic<int>* known_alone, cudaStream_t s) {
   int resident = 0;
@@ -708,7 +741,7 @@ cudaError_t launch_decode(const Cut& k, P a, void (*kernel)(P), void (*alone)(P)
   const int runs = runs_of(k, resident, &a);
   e = launch_early(kernel, dim3((unsigned)(runs * a.split)), kThreads, smem, s, 1, a);
   if (e != cudaSuccess || k.most_tiles <= 1) return e;
-  return launch_join<T, D, kTile>(k, a, runs, s);
+  return launch_join<T, D, kTile, kCost>(k, a, runs, s);
 }
 
 // The arguments of fa_decode and fa_decode_e4m3, after H is known to fit: what is wrong with them, and the

@@ -44,6 +44,11 @@ struct Mma8 {
   static constexpr int kSub = D <= 64 ? 2 : 1;
   static constexpr int kRows = 16 * kSub;       // of a tile, a warp
   static constexpr int kTile = kWarps * kRows;
+  // Of an item's beginning and end, in tiles: queries to turn into fragments and a sum over the block cost as much as 256
+  // rows.  With 128, 256, 384 and 512, sequences of up to some thousand rows, 8 key heads, us: d 64, 8 heads a key head
+  // 31.3, 30.7, 30.9, 31.4; d 96, 4: 33.9, 33.7, 34.1, 35.1; d 128, 8: 30.2, 30.0, 30.7, 31.4; d 128, 32: 67.7, 60.7, 62.2,
+  // 62.7; d 256, 16: 57.0, 48.3, 44.1, 44.5.  One tile, as for rows of 16 bits: 30.8, 35.7, 33.2, 75.7, 72.4.
+  static constexpr int kCost = 256 / kTile;
   static constexpr int kRun = D % 64 == 0 ? 16 : D % 32 == 0 ? 8 : 4;  // bytes of a key that a lane reads at a time
   static constexpr int kRuns = D / (4 * kRun);
   static constexpr int kPieces = D / 16;        // of 16 bytes in a row
@@ -55,8 +60,11 @@ struct Mma8 {
   static constexpr int kScales = kRows * (kPitchK + kPitchV);  // then the scales of K and V, and which rows are there
   static constexpr int kSeen = kScales + kRows * 8;
   static constexpr int kStageBytes = kSeen + 16;
-  static constexpr int kBlocks = D == 16 ? 5 : D == 32 ? 4 : D == 256 ? 2 : 3;
-  static constexpr int kStages = D == 16 ? 5 : D == 96 ? 4 : 3;
+  // Blocks an SM, and tiles in flight.  d 64 with 4 and 2 instead of 3 and 3: 33.5 -> 31.0 us (32 sequences of up to 2048
+  // rows, 32 heads); d 32 with 5 blocks instead of 4 spills: 39.1 -> 43.1; d 256 with 4 tiles instead of 3, one block: 72.4
+  // -> 96.7 (16 heads on one); d 128 gains nothing from 4 and 2.
+  static constexpr int kBlocks = D == 16 ? 5 : D == 32 ? 4 : D == 64 ? 4 : D == 256 ? 2 : 3;
+  static constexpr int kStages = D == 16 ? 5 : D == 96 ? 4 : D == 64 ? 2 : 3;
   static constexpr int kVW = D % 64 || D == 256 ? (D == 16 ? 16 : 32) : 64;  // columns of O that are exchanged at a time
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kPad = kVW + 4;          // floats of a row of the exchange buffer
@@ -97,11 +105,17 @@ __device__ __forceinline__ float2 lds8(uint32_t a) {
 template <class M>
 struct Loader8 {
   static constexpr int kRows = M::kRows, kStages = M::kStages;
+  // rows that a warp's request takes, and whether it takes a part of 16 rows
+  static constexpr int kRequest = 32 / M::kPieces;
+  static constexpr bool kWhole = 32 % M::kPieces == 0 && kRequest <= 16;
   const E4m3Params& a;
-  Place<M::kTile> at;   // the tile that is copied next
-  const int64_t end;    // of the run
+  Walk<M::kTile, M::kCost> walk;  // the item that is copied next,
+  int i = 0;            // the tile of it,
+  bool more;            // if there is one
   const uint32_t ring;  // of this warp
   const int piece;      // of the query heads
+  const bool wide;      // 16 rows are on a page
+  const int64_t in_row; // of this lane's piece, from the first row of its requests
   // The row that this lane looks up in that tile: its page is asked for one
   // tile ahead of the copies that need it.
   int page = -1;
@@ -109,24 +123,25 @@ struct Loader8 {
   int64_t off = 0;
   int scale = 0;  // of the page's
 
-  __device__ __forceinline__ Loader8(const E4m3Params& p, const Place<M::kTile>& first, int64_t e, uint32_t r, int h)
-      : a(p), at(first), end(e), ring(r), piece(h) {
-    look_up();
+  __device__ __forceinline__ Loader8(const E4m3Params& p, const Walk<M::kTile, M::kCost>& w, uint32_t r, int h)
+      : a(p), walk(w), more(w.some()), ring(r), piece(h), wide(kWhole && p.page_rows.d % 16 == 0),
+        in_row((int64_t)((threadIdx.x & 31) / M::kPieces) * p.pn + (threadIdx.x & 31) % M::kPieces * 16) {
+    if (more) look_up();
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) produce(i);
+    for (int k = 0; k < kStages - 1; ++k) produce(k);
   }
   __device__ __forceinline__ void look_up() {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = at.t * M::kTile + warp * kRows + (lane & (kRows - 1));
+    const int j = (walk.t + i) * M::kTile + warp * kRows + (lane & (kRows - 1));
     uint32_t r;
     const uint32_t col = a.page_rows.div((uint32_t)j, &r);
-    in = j < at.rows;
-    page = in ? a.table[at.s * a.table_stride + col] : -1;
-    off = at.item * a.ph + (int64_t)r * a.pn;
-    scale = at.item * a.blocks + (int)a.block_rows.div(r);
-    if (at.t == 0) {  // a new item: its queries into L1
+    in = j < walk.rows;
+    page = in ? a.table[walk.s * a.table_stride + col] : -1;
+    off = walk.item * a.ph + (int64_t)r * a.pn;
+    scale = walk.item * a.blocks + (int)a.block_rows.div(r);
+    if (i == 0) {  // a new item: its queries into L1
       int heads;
-      const char* row = a.Q + at.s * a.qs + (int64_t)first_head(a, at.item, piece, &heads) * a.qh;
+      const char* row = a.Q + walk.s * a.qs + (int64_t)first_head(a, walk.item, piece, &heads) * a.qh;
       constexpr int kLines = (M::kPieces * 32 + 127) / 128;
       for (int k = lane; k < heads * kLines; k += 32) prefetch_l1(row + (k / kLines) * a.qh + (k % kLines) * 128);
     }
@@ -148,23 +163,43 @@ struct Loader8 {
     } else {
       cp_async4(scales_to + lane * 4, (lane < 16 ? a.KS : a.VS) + from_scale, ok);
     }
+    if (kWhole && wide && seen == 0xffffffffu) {
+      // the rows are all there, and 16 of them on a page: an address for each 16
 #pragma unroll
-    for (int i = 0; i < kRows * M::kPieces / 32; ++i) {
-      const int row = (i * 32 + lane) / M::kPieces, piece = (i * 32 + lane) % M::kPieces;
-      const int64_t from = __shfl_sync(0xffffffffu, from_row, row) + piece * 16;
-      const bool on = (seen >> row) & 1;
-      cp_async16(to + row * M::kPitchK + piece * 16, a.K + from, on);
-      cp_async16(to + kRows * M::kPitchK + row * M::kPitchV + piece * 16, a.V + from, on);
+      for (int h = 0; h < kRows / 16; ++h) {
+        const int64_t from = __shfl_sync(0xffffffffu, from_row, 16 * h) + in_row;
+#pragma unroll
+        for (int k = 0; k < 16 / kRequest; ++k) {
+          const int row = 16 * h + k * kRequest;
+          const uint32_t in_k = to + (row + lane / M::kPieces) * M::kPitchK + lane % M::kPieces * 16;
+          const uint32_t in_v = to + kRows * M::kPitchK + (row + lane / M::kPieces) * M::kPitchV + lane % M::kPieces * 16;
+          const int64_t x = from + k * kRequest * a.pn;
+          cp_async16(in_k, a.K + x, true);
+          cp_async16(in_v, a.V + x, true);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRows * M::kPieces / 32; ++k) {
+        const int row = (k * 32 + lane) / M::kPieces, at = (k * 32 + lane) % M::kPieces;
+        const int64_t from = __shfl_sync(0xffffffffu, from_row, row) + at * 16;
+        const bool on = (seen >> row) & 1;
+        cp_async16(to + row * M::kPitchK + at * 16, a.K + from, on);
+        cp_async16(to + kRows * M::kPitchK + row * M::kPitchV + at * 16, a.V + from, on);
+      }
     }
     return kRows == 32 ? seen : seen & 0xffffu;
   }
   __device__ __forceinline__ void produce(int st) {
     const uint32_t to = ring + st * M::kStageBytes;
     uint32_t seen = 0;
-    if (at.unit < end) {
+    if (more) {
       seen = copy(to);
-      at.next(a);
-      if (at.unit < end) look_up();
+      if (++i == walk.count) {
+        i = 0;
+        more = walk.next(a);
+      }
+      if (more) look_up();
     }
     if ((threadIdx.x & 31) == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + M::kSeen), "r"(seen) : "memory");
     cp_commit();
@@ -250,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
   __shared__ float units[kWarps][kHeads];
   __shared__ float2 part_ml[kHeads];  // kAlone: this block's part, with o in part_o
   float4* part_o = reinterpret_cast<float4*>(smem);  // over the ring, which is read by then
-  Place<kTile> at;
+  Place<kTile, M::kCost> at;
   int64_t end;
   bool some;
   after_stream();
@@ -266,27 +301,22 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
   const int piece = (kAlone ? blockIdx.x / a.cluster : blockIdx.x) % a.split;
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * M::kStageBytes;
   float* exchange = reinterpret_cast<float*>(smem + M::kRing);
-  Loader8<M> load(a, at, end, ring, piece);
+  Walk<kTile, M::kCost> walk;
+  walk.begin(a, at, end);
+  Loader8<M> load(a, walk, ring, piece);
 
   uint32_t qf[M::kRuns][kWords][2 * (kF32 ? 2 : NH)];
   float qscale[NH];
   float acc[NH][M::kPieces][4];  // O^T, unnormalised, in units of unit / kTopWeight: columns 2 g, 2 g + 1 of 16, heads 2 q, 2 q + 1
   float m[NH], base[NH], l[NH];  // of heads g, g + 8; l of this lane's keys alone
   float unit[NH], per_unit[NH];
-  int begin = at.t;              // tile at which the item (or this block's part of it) began
   int stage = 0;
-  bool first = true, last = !some;  // item of the run
-
-  for (bool fresh = true; !last; fresh = false) {
-    Place<kTile> next = at;
-    next.next(a);
-    last = next.unit >= end;
-    const uint32_t seen = load.next(stage);
-
-    if (fresh || at.t == 0) {
+  bool first = true;             // item of the run
+  if (some) do {
+    {
       int heads;
-      const int h0 = first_head(a, at.item, piece, &heads);
-      const char* row = a.Q + at.s * a.qs + (int64_t)h0 * a.qh;
+      const int h0 = first_head(a, walk.item, piece, &heads);
+      const char* row = a.Q + walk.s * a.qs + (int64_t)h0 * a.qh;
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
         Columns<M, T> x;
@@ -319,151 +349,152 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
 #pragma unroll
           for (int x = 0; x < 4; ++x) acc[u][p][x] = 0.f;
       }
-      begin = at.t;
     }
 
-    if (seen) {
-      const uint32_t tile = ring + stage * M::kStageBytes;
-      float s[2 * kSub][4];
+    for (int i = 0; i < walk.count; ++i) {
+      const uint32_t seen = load.next(stage);
+      if (seen) {
+        const uint32_t tile = ring + stage * M::kStageBytes;
+        float s[2 * kSub][4];
 #pragma unroll
-      for (int o = 0; o < 2 * kSub; ++o) {  // 8 keys
-        s[o][0] = s[o][1] = s[o][2] = s[o][3] = 0.f;
+        for (int o = 0; o < 2 * kSub; ++o) {  // 8 keys
+          s[o][0] = s[o][1] = s[o][2] = s[o][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < M::kRuns; ++c) {
-          const uint32_t from = tile + (8 * o + g) * M::kPitchK + M::run_at(c, q);
-          uint32_t k[4];
-          if constexpr (M::kRun == 16) {
-            const uint4 v = lds16(from);
-            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
-          } else if constexpr (M::kRun == 8) {
-            const float2 v = lds8(from);
-            k[0] = __float_as_uint(v.x), k[1] = __float_as_uint(v.y);
-          } else {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(k[0]) : "r"(from));
-          }
+          for (int c = 0; c < M::kRuns; ++c) {
+            const uint32_t from = tile + (8 * o + g) * M::kPitchK + M::run_at(c, q);
+            uint32_t k[4];
+            if constexpr (M::kRun == 16) {
+              const uint4 v = lds16(from);
+              k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+            } else if constexpr (M::kRun == 8) {
+              const float2 v = lds8(from);
+              k[0] = __float_as_uint(v.x), k[1] = __float_as_uint(v.y);
+            } else {
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(k[0]) : "r"(from));
+            }
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            constexpr bool kBoth = NH > 1 || kF32;
-            mma16816_f16(s[o], qf[c][w][0], kBoth ? qf[c][w][kBoth ? 2 : 0] : 0u, qf[c][w][1],
-                         kBoth ? qf[c][w][kBoth ? 3 : 0] : 0u, e4m3x2_lo(k[w]), e4m3x2_hi(k[w]));
+            for (int w = 0; w < kWords; ++w) {
+              constexpr bool kBoth = NH > 1 || kF32;
+              mma16816_f16(s[o], qf[c][w][0], kBoth ? qf[c][w][kBoth ? 2 : 0] : 0u, qf[c][w][1],
+                           kBoth ? qf[c][w][kBoth ? 3 : 0] : 0u, e4m3x2_lo(k[w]), e4m3x2_hi(k[w]));
+            }
           }
         }
-      }
-      // keys 8 o + 2 q, 8 o + 2 q + 1 of the warp's
-      float2 ks[2 * kSub], vs[2 * kSub];
+        // keys 8 o + 2 q, 8 o + 2 q + 1 of the warp's
+        float2 ks[2 * kSub], vs[2 * kSub];
 #pragma unroll
-      for (int o = 0; o < 2 * kSub; ++o) {
-        ks[o] = lds8(tile + M::kScales + (8 * o + 2 * q) * 4);
-        vs[o] = lds8(tile + M::kScales + (M::kRows + 8 * o + 2 * q) * 4);
-      }
-      const uint32_t mine = seen >> (2 * q);
-      float x[NH][2 * kSub][2], p[NH][2 * kSub][2], w[NH][2 * kSub][2];
-      bool passed = false;
-#pragma unroll
-      for (int u = 0; u < NH; ++u) {
-        float top = -INFINITY, most = 0.f;
-#pragma unroll
-        for (int o = 0; o < 2 * kSub; ++o)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float dot = kF32 ? fmaf(s[o][2 + e], 1.f / 2048.f, s[o][e]) : s[o][2 * u + e];
-            const float y = dot * qscale[u] * (e ? ks[o].y : ks[o].x);
-            x[u][o][e] = mine >> (8 * o + e) & 1 ? y : -INFINITY;
-            top = fmaxf(top, x[u][o][e]);
-            p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
-            w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
-            most = fmaxf(most, w[u][o][e]);
-          }
-        // 2^7 above the maximum, or above the unit
-        passed |= top > m[u] + 7.f || most > kAhead * unit[u];
-      }
-      if (__any_sync(0xffffffffu, passed)) {
+        for (int o = 0; o < 2 * kSub; ++o) {
+          ks[o] = lds8(tile + M::kScales + (8 * o + 2 * q) * 4);
+          vs[o] = lds8(tile + M::kScales + (M::kRows + 8 * o + 2 * q) * 4);
+        }
+        const uint32_t mine = seen >> (2 * q);
+        float x[NH][2 * kSub][2], p[NH][2 * kSub][2], w[NH][2 * kSub][2];
+        bool passed = false;
 #pragma unroll
         for (int u = 0; u < NH; ++u) {
-          float top = m[u], most = 0.f;
-#pragma unroll
-          for (int o = 0; o < 2 * kSub; ++o) top = fmaxf(top, fmaxf(x[u][o][0], x[u][o][1]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          base[u] = base_of(top);
-          const float alpha = ptx::ex2(m[u] - base[u]);
-          m[u] = top;
-          l[u] *= alpha;
+          float top = -INFINITY, most = 0.f;
 #pragma unroll
           for (int o = 0; o < 2 * kSub; ++o)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              const float dot = kF32 ? fmaf(s[o][2 + e], 1.f / 2048.f, s[o][e]) : s[o][2 * u + e];
+              const float y = dot * qscale[u] * (e ? ks[o].y : ks[o].x);
+              x[u][o][e] = mine >> (8 * o + e) & 1 ? y : -INFINITY;
+              top = fmaxf(top, x[u][o][e]);
               p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
               w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
               most = fmaxf(most, w[u][o][e]);
             }
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          // the new unit: the power of two at or above what is largest, the old sums' unit or a weight
-          const float old = alpha * unit[u];
-          const float now = fmaxf(fmaxf(most, old), kLeastUnit);
-          unit[u] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
-          const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[u]));
-          per_unit[u] = kTopWeight * per;
-          const float f = old * per;
-          // the factors belong to heads g, the accumulators to heads 2q, 2q + 1
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
-#pragma unroll
-          for (int c = 0; c < M::kPieces; ++c) {
-            acc[u][c][0] *= f0, acc[u][c][2] *= f0;
-            acc[u][c][1] *= f1, acc[u][c][3] *= f1;
-          }
+          // 2^7 above the maximum, or above the unit
+          passed |= top > m[u] + 7.f || most > kAhead * unit[u];
         }
-      }
-      uint32_t hi[NH][2 * kSub], lo[NH][2 * kSub];
+        if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
-      for (int u = 0; u < NH; ++u)
+          for (int u = 0; u < NH; ++u) {
+            float top = m[u], most = 0.f;
 #pragma unroll
-        for (int o = 0; o < 2 * kSub; ++o) {
-          l[u] += p[u][o][0] + p[u][o][1];
-          const float w0 = w[u][o][0] * per_unit[u], w1 = w[u][o][1] * per_unit[u];
-          hi[u][o] = pack_f16x2(w0, w1);
-          if constexpr (kF32) {
-            const float2 z = f16x2_to_float2(hi[u][o]);
-            lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
-          }
-        }
-      // V: pieces of 8 keys x 8 pairs of columns; lane 8 n + r names row r of piece n
-      const uint32_t v_at = tile + M::kRows * M::kPitchK + ((lane & 7) + (lane >> 3 & 1) * 8) * M::kPitchV + (lane >> 4) * 16;
+            for (int o = 0; o < 2 * kSub; ++o) top = fmaxf(top, fmaxf(x[u][o][0], x[u][o][1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            base[u] = base_of(top);
+            const float alpha = ptx::ex2(m[u] - base[u]);
+            m[u] = top;
+            l[u] *= alpha;
 #pragma unroll
-      for (int b = 0; b < kSub; ++b)
+            for (int o = 0; o < 2 * kSub; ++o)
 #pragma unroll
-        for (int c = 0; c < M::kPieces; c += 2) {
-          constexpr int kTwo = M::kPieces > 1 ? 2 : 1;
-          uint32_t r[4];
-          const uint32_t from = v_at + 16 * b * M::kPitchV + c * 16;
-          if constexpr (kTwo == 2)
-            ldmatrix_trans(from, r[0], r[1], r[2], r[3]);
-          else
-            ldmatrix_trans2(from, r[0], r[1]);
+              for (int e = 0; e < 2; ++e) {
+                p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
+                w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
+                most = fmaxf(most, w[u][o][e]);
+              }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // the new unit: the power of two at or above what is largest, the old sums' unit or a weight
+            const float old = alpha * unit[u];
+            const float now = fmaxf(fmaxf(most, old), kLeastUnit);
+            unit[u] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
+            const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[u]));
+            per_unit[u] = kTopWeight * per;
+            const float f = old * per;
+            // the factors belong to heads g, the accumulators to heads 2q, 2q + 1
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
 #pragma unroll
-          for (int i = 0; i < kTwo; ++i) {
-            const uint32_t v0 = __byte_perm(r[2 * i], 0, 0x3120), v1 = __byte_perm(r[2 * i + 1], 0, 0x3120);
-            const uint32_t a0 = e4m3x2_lo(v0), a1 = e4m3x2_hi(v0), a2 = e4m3x2_lo(v1), a3 = e4m3x2_hi(v1);
-#pragma unroll
-            for (int u = 0; u < NH; ++u) {
-              mma16816_f16(acc[u][c + i], a0, a1, a2, a3, hi[u][2 * b], hi[u][2 * b + 1]);
-              if (kF32) mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
+            for (int c = 0; c < M::kPieces; ++c) {
+              acc[u][c][0] *= f0, acc[u][c][2] *= f0;
+              acc[u][c][1] *= f1, acc[u][c][3] *= f1;
             }
           }
         }
+        uint32_t hi[NH][2 * kSub], lo[NH][2 * kSub];
+#pragma unroll
+        for (int u = 0; u < NH; ++u)
+#pragma unroll
+          for (int o = 0; o < 2 * kSub; ++o) {
+            l[u] += p[u][o][0] + p[u][o][1];
+            const float w0 = w[u][o][0] * per_unit[u], w1 = w[u][o][1] * per_unit[u];
+            hi[u][o] = pack_f16x2(w0, w1);
+            if constexpr (kF32) {
+              const float2 z = f16x2_to_float2(hi[u][o]);
+              lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
+            }
+          }
+        // V: pieces of 8 keys x 8 pairs of columns; lane 8 n + r names row r of piece n
+        const uint32_t v_at = tile + M::kRows * M::kPitchK + ((lane & 7) + (lane >> 3 & 1) * 8) * M::kPitchV + (lane >> 4) * 16;
+#pragma unroll
+        for (int b = 0; b < kSub; ++b)
+#pragma unroll
+          for (int c = 0; c < M::kPieces; c += 2) {
+            constexpr int kTwo = M::kPieces > 1 ? 2 : 1;
+            uint32_t r[4];
+            const uint32_t from = v_at + 16 * b * M::kPitchV + c * 16;
+            if constexpr (kTwo == 2)
+              ldmatrix_trans(from, r[0], r[1], r[2], r[3]);
+            else
+              ldmatrix_trans2(from, r[0], r[1]);
+#pragma unroll
+            for (int i = 0; i < kTwo; ++i) {
+              const uint32_t v0 = __byte_perm(r[2 * i], 0, 0x3120), v1 = __byte_perm(r[2 * i + 1], 0, 0x3120);
+              const uint32_t a0 = e4m3x2_lo(v0), a1 = e4m3x2_hi(v0), a2 = e4m3x2_lo(v1), a3 = e4m3x2_hi(v1);
+#pragma unroll
+              for (int u = 0; u < NH; ++u) {
+                mma16816_f16(acc[u][c + i], a0, a1, a2, a3, hi[u][2 * b], hi[u][2 * b + 1]);
+                if (kF32) mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
+              }
+            }
+          }
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-
-    if (at.t + 1 == at.tiles || last) {
+    {
       // ---- the item ends here, or goes on in the next block's run
-      const bool whole = begin == 0 && at.t + 1 == at.tiles && !(kAlone && a.cluster > 1);
+      const bool whole = walk.t == 0 && walk.count == walk.tiles && !(kAlone && a.cluster > 1);
       // the part of an item that was being read when the run began is the
       // block's first, any other its second
       const int slot = (2 * (blockIdx.x / a.split) + (first ? 0 : 1)) * a.split + piece;
       first = false;
       int heads;
-      const int h0 = first_head(a, at.item, piece, &heads);
+      const int h0 = first_head(a, walk.item, piece, &heads);
       __syncthreads();  // ml, units and the exchange buffer have been read
 #pragma unroll
       for (int u = 0; u < NH; ++u) {
@@ -518,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               const bool none = sum == 0.f;
               const float inv = none ? 0.f : 1.f / sum;
               o = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-              store4<T>(a.O + at.s * a.os + (int64_t)(h0 + head) * a.oh, col, o);
-              if (col == 0) a.L[(int64_t)at.s * a.H + h0 + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
+              store4<T>(a.O + walk.s * a.os + (int64_t)(h0 + head) * a.oh, col, o);
+              if (col == 0) a.L[(int64_t)walk.s * a.H + h0 + head] = none ? INFINITY : (top + log2f(sum)) * kLn2;
             } else if (kAlone) {
               part_o[(head * D + col) / 4] = o;
               if (col == 0) part_ml[head] = make_float2(top, sum);
@@ -532,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
         }
       }
     }
-    at = next;
-  }
+  } while (walk.next(a));
   if (kAlone && a.cluster > 1) join_cluster<T, D>(a, part_o, part_ml);
 }
 
@@ -542,7 +572,7 @@ cudaError_t launch(const Cut& k, const E4m3Params& a, cudaStream_t s) {
   using M = Mma8<D, NH, kF32>;
   using T = std::conditional_t<kF32, float, __nv_bfloat16>;
   static std::atomic<int> known[64], known_alone[64];
-  return launch_decode<T, D, M::kTile, E4m3Params>(k, a, decode_e4m3_kernel<D, NH, kF32, false>,
+  return launch_decode<T, D, M::kTile, M::kCost>(k, a, decode_e4m3_kernel<D, NH, kF32, false>,
                                                    decode_e4m3_kernel<D, NH, kF32, true>, M::kSmem, known, known_alone, s);
 }
 
@@ -556,7 +586,7 @@ cudaError_t launch_d(const fa_cache& c, const Cut& k, const E4m3Params& a, cudaS
 template <int D>
 Cut cut_d(const fa_cache& c, int H) {
   using M = Mma8<D, 1, true>;
-  return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks);
+  return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks, M::kCost);
 }
 Cut cut_mma(const fa_cache& c, int H) {
   switch (c.d) {

@@ -52,6 +52,9 @@ namespace {
 template <int D, int HP>
 struct Tile8 {
   static constexpr int kRows = 128;             // keys
+  // Of an item's beginning and end, in tiles, with 1, 2, 3 and 4: 64 sequences of up to 8192 rows of d 128 82.9, 83.8, 84.1,
+  // 84.8 us; 32 of up to 2048 of d 256 35.0, 32.1, 31.9, 32.5.
+  static constexpr int kCost = D == 256 ? 2 : 1;
   static constexpr int kTerms = 3;
   static constexpr int kCols = kTerms * HP;     // term t of head h is column t HP + h
   static constexpr int kN = 16;                 // of a product
@@ -70,7 +73,6 @@ struct Tile8 {
   static constexpr int kLoaders = 4 / kGroups;  // warps of a group that copy
   static constexpr int kBlocks32 = 4 / kLoaders;  // blocks of 32 rows that each of them takes
   static constexpr int kStages = 3;
-  static constexpr int kAhead = 1;              // tiles in flight behind the one that is waited for
   static constexpr int kThreadsAll = 32 * kGroups * (6 + kLoaders);
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kQ = kRing;              // two items' queries
@@ -172,34 +174,6 @@ __device__ __forceinline__ bool group_or(int group, bool x) {
   return r != 0;
 }
 
-// A group's way through its run, item by item.
-struct Walk {
-  int s, item, t;       // the item's sequence and head, and its first tile that is the run's
-  int rows, tiles;      // of the item
-  int count;            // of its tiles, those that are the run's
-  int rows_next;        // of the next sequence, asked for in time
-  int64_t unit, end;    // of tile t; the run's
-  __device__ __forceinline__ void begin(const E4m3Params& a) {
-    count = (int)min((int64_t)(tiles - t), end - unit);
-    if (s + 1 < a.S) rows_next = rows_of(a, s + 1);
-  }
-  // the next item; false if the run ends before it has a tile
-  __device__ __forceinline__ bool next(const E4m3Params& a) {
-    unit += tiles - t + kItemCost;
-    t = 0;
-    if (unit >= end) return false;
-    if (++item == a.items) {
-      item = 0;
-      ++s;
-      rows = rows_next;
-      tiles = tiles_of<128>(rows);
-      if (s + 1 < a.S) rows_next = rows_of(a, s + 1);
-    }
-    count = (int)min((int64_t)tiles, end - unit);
-    return true;
-  }
-};
-
 // A place in a ring of N barriers and the parity of its use.
 template <int N>
 struct Turn {
@@ -212,9 +186,9 @@ struct Turn {
 
 // The run of a group: its number, and where it begins and ends; false if it has none.
 template <class M>
-__device__ __forceinline__ bool run_of_group(const E4m3Params& a, int group, Walk* walk, int* run) {
+__device__ __forceinline__ bool run_of_group(const E4m3Params& a, int group, Walk<M::kRows, M::kCost>* walk, int* run) {
   __shared__ int64_t sums[M::kThreadsAll / 32];
-  Units<M::kRows, M::kThreadsAll> units(a, sums);
+  Units<M::kRows, M::kThreadsAll, M::kCost> units(a, sums);
   const Share share = units.share();
   const int first = blockIdx.x / a.split * M::kGroups;
   *run = first + group;
@@ -229,11 +203,10 @@ __device__ __forceinline__ bool run_of_group(const E4m3Params& a, int group, Wal
     int64_t base;
     const int s = units.find(x, 0, &base);
     if (g == group) {
-      Place<M::kRows> at;
+      Place<M::kRows, M::kCost> at;
       at.set(a, s, base, x);
-      *walk = {at.s, at.item, at.t, at.rows, at.tiles, 0, 0, at.unit, share.first(first + g + 1)};
-      some = walk->unit < walk->end;
-      walk->begin(a);
+      walk->begin(a, at, share.first(first + g + 1));
+      some = walk->some();
     }
   }
   return some;
@@ -241,9 +214,9 @@ __device__ __forceinline__ bool run_of_group(const E4m3Params& a, int group, Wal
 
 // ---------------------------------------------------------------- copying
 template <class M>
-__device__ __forceinline__ void copy_tiles(const E4m3Params& a, Walk walk, uint32_t ring, Bars<M>* bars, uint32_t (*seen_at)[4],
+__device__ __forceinline__ void copy_tiles(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, uint32_t ring, Bars<M>* bars, uint32_t (*seen_at)[4],
                                            int loader, const ptx::Waiter& waiter) {
-  constexpr int kStages = M::kStages, kAhead = M::kAhead, NB = M::kBlocks32;
+  constexpr int kStages = M::kStages, NB = M::kBlocks32;
   const int lane = threadIdx.x & 31;
   // This lane's row of each block of 32: its page is asked for one tile ahead of the copies.
   int page[NB], scale[NB];
@@ -332,31 +305,21 @@ __device__ __forceinline__ void copy_tiles(const E4m3Params& a, Walk walk, uint3
         look_up(t0 + i + 1);
       else if ((more = walk.next(a)))
         look_up(0);
-      if (n >= kAhead) {
-        cp_wait<kAhead>();
+      if (n > 0) {  // one stays in flight: with more, what follows sees each tile that much later
+        cp_wait<1>();
         publish();
       }
     }
     if (!ok) break;
   }
-  // the last ones, one after the other
-  auto drain = [&](auto left) {
-    constexpr int kLeft = decltype(left)::value;
-    cp_wait<kLeft>();
-    if (ok && n > kLeft) publish();
-  };
-  if constexpr (kAhead > 4) drain(std::integral_constant<int, 4>());
-  if constexpr (kAhead > 3) drain(std::integral_constant<int, 3>());
-  if constexpr (kAhead > 2) drain(std::integral_constant<int, 2>());
-  if constexpr (kAhead > 1) drain(std::integral_constant<int, 1>());
-  drain(std::integral_constant<int, 0>());
-  static_assert(kAhead <= 5, "the list above");
+  cp_wait<0>();
+  if (ok && n > 0) publish();  // the last
 }
 
 // --------------------------------------------------------------- products
 // One thread: a warp's votes at every wait made 1650 cycles a tile.
 template <class M, int D>
-__device__ __forceinline__ void issue_products(const E4m3Params& a, Walk walk, uint32_t ring, Bars<M>* bars, uint32_t tmem,
+__device__ __forceinline__ void issue_products(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, uint32_t ring, Bars<M>* bars, uint32_t tmem,
                                                const ptx::Waiter& waiter) {
   constexpr int kStages = M::kStages, kN = M::kN;
   constexpr uint32_t kShape = 1u << 4 | (uint32_t)(kN >> 3) << 17 | 8u << 24;  // fp32 sums, n columns, 128 rows
@@ -422,7 +385,7 @@ __device__ __forceinline__ void issue_products(const E4m3Params& a, Walk walk, u
 // ---------------------------------------------------------------- queries
 // Each item's queries as terms, an item ahead, in units of 1 / *qscales times the softmax scale.
 template <class M, int D, int HP>
-__device__ __forceinline__ void store_queries(const E4m3Params& a, Walk at, int piece, uint32_t ring, Bars<M>* bars,
+__device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows, M::kCost> at, int piece, uint32_t ring, Bars<M>* bars,
                                               float (*qscales)[HP], const ptx::Waiter& waiter) {
   constexpr int kUnits = (D / 4 + 31) / 32;  // of 4 columns of a head, a lane
   const int lane = threadIdx.x & 31;
@@ -492,7 +455,7 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <class M, int D, int HP>
-__device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk walk, int run, int piece, int group, uint32_t ring,
+__device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, int run, int piece, int group, uint32_t ring,
                                             Bars<M>* bars, uint32_t (*seen_at)[4], float (*qscales)[HP],
                                             float (*over_warps)[kWarps][HP], uint32_t tmem, const ptx::Waiter& waiter) {
   constexpr int kStages = M::kStages, kTerms = M::kTerms, kCols = M::kCols, kN = M::kN, kHalves = M::kHalves;
@@ -517,120 +480,120 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk walk, int 
       qscale[h] = qscales[q.at][h];
     }
     for (int i = 0; i < walk.count; ++i) {
-    const int st = turn.at;
-    const uint32_t tile = ring + st * M::kStageBytes;
-    const bool bad = !ptx::warp_wait2(bar(bars->s_full[two.at]), two.phase, bar(bars->full[st]), turn.phase, waiter);
-    ptx::tc_fence_after();
-    const bool mine = seen_at[st][warp] >> lane & 1;
-    const float ks = lds4(tile + M::kScales + thread * 4), vs = lds4(tile + M::kScales + 512 + thread * 4);
-    float x[HP], w[HP], p[HP];
-    {
-      Row<kCols> r;
-      r.load(my_row + two.at * kN);
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(bars->s_empty[two.at]));
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        const float y = fmaf(sum_terms<HP, kTerms>(r, h) * qscale[h], ks, -base[h]);  // the score above the base
-        x[h] = mine ? y : -INFINITY;
-      }
-    }
-    // weights in units of U, as terms: this key's 16 columns of P
-    auto store_weights = [&](const float (&w)[HP]) {
-      const uint32_t to = tile + thread * 16;
-      uint32_t t[kTerms];
-      if constexpr (HP == 1) {
-        cut_terms<kTerms>(w[0], 0.f, t);
-        const uint32_t x = (t[0] & 0xffu) | (t[1] & 0xffu) << 8 | (t[2] & 0xffu) << 16;
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
-      } else {
-        uint32_t u[kTerms];
-        cut_terms<kTerms>(w[0], w[1], t);
-        cut_terms<kTerms>(w[2], w[3], u);
-        ptx::st_shared_v4(to, __byte_perm(t[0], u[0], 0x5410), __byte_perm(t[1], u[1], 0x5410), __byte_perm(t[2], u[2], 0x5410), 0);
-      }
-      ptx::fence_proxy_async_smem();
-    };
-    bool passed = bad || unset;
-#pragma unroll
-    for (int h = 0; h < HP; ++h) {
-      p[h] = ptx::ex2(x[h]);
-      w[h] = p[h] * vs * per_unit[h];
-      passed |= x[h] > kMostScore || w[h] > kMostWeight;
-    }
-    store_weights(w);
-    if (group_or(group, passed)) {
-      // ---- a score or a weight passed its limit: the maximum and the unit move
-      if (i > 0) wait_o();
+      const int st = turn.at;
+      const uint32_t tile = ring + st * M::kStageBytes;
+      const bool bad = !ptx::warp_wait2(bar(bars->s_full[two.at]), two.phase, bar(bars->full[st]), turn.phase, waiter);
       ptx::tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        x[h] += base[h];
-        const float top = warp_max(x[h]);
-        if (lane == 0) over_warps[0][warp][h] = top;
-      }
-      if (group_or(group, *waiter.abort != 0)) return;  // a wait ran out
-      unset = false;
-      float f[HP];
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        float top = m[h];
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, over_warps[0][k][h]);
-        base[h] = base_of(top);
-        const float alpha = ptx::ex2(m[h] - base[h]);
-        m[h] = top;
-        unset |= top == -INFINITY;
-        l[h] *= alpha;
-        f[h] = alpha * unit[h];
-        p[h] = ptx::ex2(x[h] - base[h]);
-        w[h] = p[h] * vs;
-      }
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        const float top = warp_max(w[h]);
-        if (lane == 0) over_warps[1][warp][h] = top;
-      }
-      group_sync(group);
-#pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        // the power of two at or above what is largest, the sums' unit or a weight
-        float now = fmaxf(f[h], kLeastUnit);
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) now = fmaxf(now, over_warps[1][k][h]);
-        unit[h] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
-        const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[h]));
-        per_unit[h] = kSetWeight * per;
-        f[h] *= per;
-        w[h] *= per_unit[h];
-      }
-      if (i > 0) {
-#pragma unroll
-        for (int x = 0; x < kHalves; ++x) {
-          Row<kCols> r;
-          r.load(tO + x * kN);
-          if constexpr (HP == 1)
-            asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tO + x * kN), "f"(r[0] * f[0]),
-                         "f"(r[1] * f[0]), "f"(r[2] * f[0]), "r"(r.r[3])
-                         : "memory");
-          else {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) r.r[c] = __float_as_uint(r[c] * f[c % HP]);
-            ptx::tmem_st16(tO + x * kN, r.r);
-          }
-        }
-        ptx::tmem_st_wait();
+      const bool mine = seen_at[st][warp] >> lane & 1;
+      const float ks = lds4(tile + M::kScales + thread * 4), vs = lds4(tile + M::kScales + 512 + thread * 4);
+      float x[HP], w[HP], p[HP];
+      {
+        Row<kCols> r;
+        r.load(my_row + two.at * kN);
         ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(bars->s_empty[two.at]));
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float y = fmaf(sum_terms<HP, kTerms>(r, h) * qscale[h], ks, -base[h]);  // the score above the base
+          x[h] = mine ? y : -INFINITY;
+        }
+      }
+      // weights in units of U, as terms: this key's 16 columns of P
+      auto store_weights = [&](const float (&w)[HP]) {
+        const uint32_t to = tile + thread * 16;
+        uint32_t t[kTerms];
+        if constexpr (HP == 1) {
+          cut_terms<kTerms>(w[0], 0.f, t);
+          const uint32_t x = (t[0] & 0xffu) | (t[1] & 0xffu) << 8 | (t[2] & 0xffu) << 16;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
+        } else {
+          uint32_t u[kTerms];
+          cut_terms<kTerms>(w[0], w[1], t);
+          cut_terms<kTerms>(w[2], w[3], u);
+          ptx::st_shared_v4(to, __byte_perm(t[0], u[0], 0x5410), __byte_perm(t[1], u[1], 0x5410), __byte_perm(t[2], u[2], 0x5410), 0);
+        }
+        ptx::fence_proxy_async_smem();
+      };
+      bool passed = bad || unset;
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        p[h] = ptx::ex2(x[h]);
+        w[h] = p[h] * vs * per_unit[h];
+        passed |= x[h] > kMostScore || w[h] > kMostWeight;
       }
       store_weights(w);
-      group_sync(group);
-    }
-    if (thread == 0) ptx::mbar_arrive(bar(bars->p_full[two.at]));
+      if (group_or(group, passed)) {
+        // ---- a score or a weight passed its limit: the maximum and the unit move
+        if (i > 0) wait_o();
+        ptx::tc_fence_after();
 #pragma unroll
-    for (int h = 0; h < HP; ++h) l[h] += p[h];
+        for (int h = 0; h < HP; ++h) {
+          x[h] += base[h];
+          const float top = warp_max(x[h]);
+          if (lane == 0) over_warps[0][warp][h] = top;
+        }
+        if (group_or(group, *waiter.abort != 0)) return;  // a wait ran out
+        unset = false;
+        float f[HP];
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          float top = m[h];
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, over_warps[0][k][h]);
+          base[h] = base_of(top);
+          const float alpha = ptx::ex2(m[h] - base[h]);
+          m[h] = top;
+          unset |= top == -INFINITY;
+          l[h] *= alpha;
+          f[h] = alpha * unit[h];
+          p[h] = ptx::ex2(x[h] - base[h]);
+          w[h] = p[h] * vs;
+        }
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float top = warp_max(w[h]);
+          if (lane == 0) over_warps[1][warp][h] = top;
+        }
+        group_sync(group);
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          // the power of two at or above what is largest, the sums' unit or a weight
+          float now = fmaxf(f[h], kLeastUnit);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) now = fmaxf(now, over_warps[1][k][h]);
+          unit[h] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
+          const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[h]));
+          per_unit[h] = kSetWeight * per;
+          f[h] *= per;
+          w[h] *= per_unit[h];
+        }
+        if (i > 0) {
+#pragma unroll
+          for (int x = 0; x < kHalves; ++x) {
+            Row<kCols> r;
+            r.load(tO + x * kN);
+            if constexpr (HP == 1)
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tO + x * kN), "f"(r[0] * f[0]),
+                           "f"(r[1] * f[0]), "f"(r[2] * f[0]), "r"(r.r[3])
+                           : "memory");
+            else {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) r.r[c] = __float_as_uint(r[c] * f[c % HP]);
+              ptx::tmem_st16(tO + x * kN, r.r);
+            }
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        }
+        store_weights(w);
+        group_sync(group);
+      }
+      if (thread == 0) ptx::mbar_arrive(bar(bars->p_full[two.at]));
+#pragma unroll
+      for (int h = 0; h < HP; ++h) l[h] += p[h];
 
-    turn.next();
-    two.next();
+      turn.next();
+      two.next();
     }
       // ---- the item ends here, or goes on in the next group's run
       const bool whole = walk.t == 0 && walk.count == walk.tiles;
@@ -701,7 +664,7 @@ __global__ void __launch_bounds__(Tile8<D, HP>::kThreadsAll, 1) decode_sm103_ker
                     : asks   ? warp - 5 * M::kGroups
                              : (warp - 6 * M::kGroups) / M::kLoaders;
   Bars<M>* bars = &all_bars[group];
-  Walk walk = {};
+  Walk<M::kRows, M::kCost> walk = {};
   int run;
   after_stream();
   next_may_start();  // the join
@@ -769,26 +732,28 @@ cudaError_t launch(const Cut& k, E4m3Params a, cudaStream_t s) {
   const int runs = runs_of(k, resident * M::kGroups, &a);
   e = launch_early(kernel, dim3((unsigned)(ceil_div(runs, M::kGroups) * a.split)), M::kThreadsAll, M::kSmem, s, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_join<__nv_bfloat16, D, M::kRows>(k, a, runs, s);
+  return launch_join<__nv_bfloat16, D, M::kRows, M::kCost>(k, a, runs, s);
 }
 
 }  // namespace
 
-// What the table can hold decides, as the lengths are not known here.  By tiles a group (128 rows; 304 groups of d 128, 152 of d 256),
-// 8 sequences of as many rows, the kernels of fa_decode_e4m3.cu against these, in us:
-//   d 128, 1 head a key head:   4: 15.1, 16.2   8: 21.2, 22.2   12: 28.2, 28.3   16: 34.0, 34.0   32: 59.2, 57.4
-//   d 128, 4 heads:             4: 15.7, 17.1   8: 21.6, 23.2   12: 28.9, 29.3   16: 34.7, 35.1   32: 59.8, 59.0
-//   d 256, 1 head:              4: 15.9, 16.3   6: 20.1, 19.3    8: 23.2, 22.0   16: 36.2, 34.2   32: 61.6, 56.1
-//   d 256, 4 heads:             4: 16.9, 17.6   6: 20.8, 20.8    8: 23.8, 23.7   16: 37.2, 36.0   32: 62.9, 58.7
-// d 96 gains nothing at any size (32: 50.2, 49.1 and 50.4, 50.7), d 64 and 32 and eight heads or more lose.
+// What the table can hold decides, as the lengths are not known here.  By tiles that a group has if it is full (128 rows; 304 groups
+// of d 128, 152 of d 256), 32 sequences, half full on average, the kernels of fa_decode_e4m3.cu against these, in us:
+//   d 128, 1 head a key head:  32: 33.3, 35.1   48: 44.7, 45.3   64: 60.0, 57.4   96: 81.0, 77.7
+//   d 128, 4 heads:            32: 34.1, 36.9   48: 45.6, 46.9   64: 60.5, 58.5   96: 85.5, 79.1
+//   d 256, 1 head:             24: 28.7, 28.7   32: 34.9, 34.4   48: 47.0, 45.1   96: 84.9, 77.7
+//   d 256, 4 heads:            24: 29.1, 31.4   32: 35.8, 37.2   48: 48.5, 47.6   96: 86.5, 80.1
+// 8 sequences that fill it: d 128 with 1 head, 16: 33.7, 33.6, 32: 58.9, 57.0; d 256 with 4, 12: 29.3, 30.5, 16: 36.2, 35.9,
+// 32: 61.4, 57.9.  d 96 gains nothing at any size, d 64 and 32 and eight heads or more lose.
 bool takes_sm103(const fa_cache& c, int H) {
   const int64_t tiles = (int64_t)c.S * c.H_kv * cache_rows(c) / 128;
-  return c.dtype == FA_BF16 && H / c.H_kv <= 4 && ((c.d == 128 && tiles >= 304 * 24) || (c.d == 256 && tiles >= 152 * 8));
+  return c.dtype == FA_BF16 && H / c.H_kv <= 4 && ((c.d == 128 && tiles >= 304 * 56) || (c.d == 256 && tiles >= 152 * 40));
 }
 
 Cut cut_e4m3_sm103(const fa_cache& c, int H) {
   Cut k = pieces_of(H / c.H_kv, 4);
   k.part_heads = k.piece_heads == 1 ? 1 : 4;
+  k.cost = c.d == 256 ? Tile8<256, 4>::kCost : Tile8<128, 4>::kCost;
   k.most_tiles = ceil_div(cache_rows(c), 128);
   k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
   k.cluster = 0;

@@ -32,7 +32,7 @@ def is_large(args):
 
 def large(S, H, Hk, d, page, lengths, **kw):
     """More columns than the rows need."""
-    rows = SM * (2 * 24 if d == 128 else 8) * 128 // (S * Hk) + 128
+    rows = SM * (2 * 56 if d == 128 else 40) * 128 // (S * Hk) + 128
     args = make(S, H, Hk, d, page, lengths, wide=rows // page + 1, **kw)
     assert is_large(args)
     return args
