@@ -639,8 +639,13 @@ inline int tile_rows(const fa_cache& c) { return c.dtype == FA_FP32 && c.d == 25
 // runs, 9.1 with 16 blocks of 4 tiles and 12.6 with 8 of 8; 8 of 512, 32 heads on 8,
 // 10.2 in runs and 7.7 with 4 blocks of 2 tiles.
 constexpr int kClusterTiles = 2;
+// Tiles a block at most, by a cluster's size.
+struct ClusterTiles {
+  int sixteen = kClusterTiles, some = kClusterTiles, one = kClusterTiles;
+  int of(int blocks) const { return blocks == kMostBlocks ? sixteen : blocks == 1 ? one : some; }
+};
 // an_sm: blocks of the kernel that an SM holds.
-inline int cluster_of(int an_sm, int64_t items, int64_t most_tiles) {
+inline int cluster_of(int an_sm, int64_t items, int64_t most_tiles, const ClusterTiles& most) {
   // clusters that the GPU holds of each size, for each block an SM, as a GB300 of 152 SMs answers when asked: a cluster
   // stays inside a GPC.  Written down, because the workspace's size goes by this too, which is asked for without a GPU;
   // one that holds other numbers of them computes the same, in more or fewer waves.
@@ -649,7 +654,7 @@ inline int cluster_of(int an_sm, int64_t items, int64_t most_tiles) {
   } sizes[] = {{kMostBlocks, 7}, {8, 15}, {4, 36}, {2, 76}, {1, 152}};
   for (const auto& z : sizes) {
     if (items > (int64_t)z.fit * an_sm || z.blocks / 2 >= most_tiles) continue;  // too many, or blocks without a tile
-    return most_tiles <= (int64_t)z.blocks * kClusterTiles ? z.blocks : 0;
+    return most_tiles <= (int64_t)z.blocks * most.of(z.blocks) ? z.blocks : 0;
   }
   return 0;
 }
@@ -662,11 +667,11 @@ inline Cut pieces_of(int group, int most) {
   k.part_heads = k.piece_heads <= 8 ? 8 : 16;
   return k;
 }
-inline Cut cut_tiles(Cut k, const fa_cache& c, int tile, int an_sm, int cost = kItemCost) {
+inline Cut cut_tiles(Cut k, const fa_cache& c, int tile, int an_sm, int cost = kItemCost, const ClusterTiles& most = {}) {
   k.cost = cost;
   k.most_tiles = ceil_div(cache_rows(c), tile);
   k.tiles = (int64_t)c.S * c.H_kv * k.most_tiles;
-  k.cluster = cluster_of(an_sm, (int64_t)c.S * c.H_kv * k.split, k.most_tiles);
+  k.cluster = cluster_of(an_sm, (int64_t)c.S * c.H_kv * k.split, k.most_tiles, most);
   return k;
 }
 

@@ -583,10 +583,22 @@ cudaError_t launch_d(const fa_cache& c, const Cut& k, const E4m3Params& a, cudaS
   return cudaErrorInvalidValue;
 }
 
+// Clusters of 16 blocks get two tiles a block at most, of 2 to 8 six, blocks alone twelve: then the runs and the join are
+// quicker.  Clusters against runs, 8 key heads and 4 heads a key head, all sequences of the table's size, us:
+//   16 blocks, 3 tiles:  d 64 9.9, 10.1   d 96 9.3, 9.9    d 128 10.4, 9.8   fp32 of d 128 11.1, 10.5
+//   8 blocks, 6 tiles:   d 64 11.9, 12.7  d 96 10.3, 12.0  d 128 11.3, 12.2  d 256, 4 blocks: 16.5, 18.3
+//             8:         d 64 14.0, 14.3  d 96 12.0, 12.9  d 128 13.5, 13.8                   18.8, 20.5
+//   1 block, 12 tiles:   d 64 17.0, 18.0  d 96 13.6, 15.8  d 128 14.9, 17.9  d 256 22.6, 26.7
+// and of all sizes up to it:
+//   8 blocks, 6 tiles:   d 64 11.2, 11.3  d 96 9.9, 11.0   d 128 10.7, 11.2  d 256, 4 blocks: 13.7, 14.0
+//             8:         d 64 12.8, 11.9  d 96 11.0, 11.1  d 128 12.0, 11.6                   17.0, 14.2
+//   1 block, 12 tiles:   d 64 12.9, 13.0  d 96 11.7, 12.4  d 128 12.7, 13.6  d 256 19.4, 21.2
+constexpr ClusterTiles kTilesAlone = {2, 6, 12};
+
 template <int D>
 Cut cut_d(const fa_cache& c, int H) {
   using M = Mma8<D, 1, true>;
-  return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks, M::kCost);
+  return cut_tiles(pieces_of(H / c.H_kv, c.dtype == FA_BF16 ? 16 : 8), c, M::kTile, M::kBlocks, M::kCost, kTilesAlone);
 }
 Cut cut_mma(const fa_cache& c, int H) {
   switch (c.d) {

@@ -191,6 +191,14 @@ def test_clusters_of_every_size(S, n, dtype):
     run_and_check(make(S, 4, 1, 128, 64, lengths, dtype, seed=S, block=32))
 
 
+@pytest.mark.parametrize("S,n", [(30, 2900), (100, 1400), (200, 760), (400, 740)])
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (128, torch.float32)])
+def test_clusters_of_several_tiles_a_block(S, n, d, dtype):
+    """8, 4 and 2 blocks an item and one alone, as many tiles a block as there may be and one more, and none."""
+    lengths = [max(0, n - 31 * (i % 100)) for i in range(S)]
+    run_and_check(make(S, 2, 1, d, 64, lengths, dtype, seed=S, block=32))
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 def test_peaked_scores(dtype):
     """Scores with a deviation of 4: the running maximum moves, most weights vanish."""
