@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t over_team(uint32_t x) {
 template <class T, int kTeam>
 __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const AppendParams a) {
   after_stream();
-  const uint32_t team = kTeam == 32 ? (blockIdx.x * kThreads + threadIdx.x) / 32 : blockIdx.x;
+  const uint32_t team = kTeam == 32 ? blockIdx.x * (kThreads / 32) + threadIdx.x / 32 : blockIdx.x;
   const int thread = threadIdx.x % kTeam;
   if (team >= a.teams) return;
   uint32_t nth, g;

@@ -69,7 +69,9 @@ inline fa_status check_cache(const fa_cache* c) {
 inline fa_status check_cache_e4m3(const fa_cache* c, int32_t block_rows) {
   const fa_status st = check_pools(c, 1);
   if (st != FA_OK) return st;
-  return block_rows >= 1 && c->page_rows % block_rows == 0 ? FA_OK : FA_ERR_INVALID_ARG;
+  if (block_rows < 1 || c->page_rows % block_rows != 0) return FA_ERR_INVALID_ARG;
+  // a page's scales are counted in 32 bits
+  return (int64_t)c->H_kv * (c->page_rows / block_rows) < (int64_t(1) << 31) ? FA_OK : FA_ERR_UNSUPPORTED;
 }
 
 inline fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }

@@ -348,7 +348,7 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
  * its block's scale is the value it stands for.  block_rows divides page_rows:
  * 1 is a scale a row, page_rows one a page and head.  The scales of a pool are dense,
  * [num_pages, H_kv, page_rows / block_rows]; what stands there before a block's
- * first row is written does not matter.
+ * first row is written does not matter.  H_kv * page_rows / block_rows < 2^31.
  * fa_cache says the rest: its dtype is that of Q, O and the rows outside the
  * cache, its strides are those of the e4m3 pools, in elements, which are bytes, and
  * multiples of 16.  dtype, d and limits as above.  The page calls below are the same
@@ -364,7 +364,7 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
  * even; what is not finite becomes NaN.  Where the scale grows, the rows before
  * are divided by what it grew by and rounded once more: exact, but for
  * numbers that end below 2^-6.  Rows of a touched block behind the new ones are
- * taken to hold nothing.
+ * taken to hold nothing.  A page that is written to stands once in the table.
  * rows >= 1, S * H_kv * rows < 2^31.  Neither the pools nor the scales of K and
  * V may be the same memory. */
 fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K, const void* V,

@@ -301,6 +301,27 @@ def test_offsets_beyond_32_bits():
         assert np.array_equal(f64(y), dense(p, s, [[0, 1, 2, 3]], None, None, 1000))
 
 
+def test_more_blocks_than_32_bits_count_threads():
+    """One row over and over, each a block of its own."""
+    n, page = (1 << 27) + 50, 1 << 20
+    pages = n // page + 1
+    kp, vp = (torch.zeros(pages, 1, page, 16, dtype=torch.uint8, device=DEV).view(F8) for _ in range(2))
+    ks, vs = (torch.zeros(pages, 1, page, device=DEV) for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    x = torch.arange(1.0, 17.0, device=DEV)
+    fa.cache_append_e4m3(x.expand(1, 1, n, 16), (-x).expand(1, 1, n, 16), kp, vp, ks, vs, table, ints([0]))
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    # 16 is below 448 * 2^-4 = 28 and above 14; all of 1 ... 16 have four significant bits
+    for scales in (ks, vs):
+        assert (scales.view(-1)[:n] == 2.0 ** -4).all() and (scales.view(-1)[n:] == 0).all()
+    for pool, sign in ((kp, 1), (vp, -1)):
+        rows = pool.view(torch.uint8).view(-1, 16)
+        for part in (rows[:50], rows[n - 100:n]):
+            assert torch.equal(part.view(F8).float(), (sign * 16 * x).expand(len(part), 16))
+        assert (rows[n:] == 0).all()
+
+
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("block", [1, 4, 8])
 def test_a_run_of_all_calls(graph, block):

@@ -65,6 +65,12 @@ def test_blocks_divide_a_page(lib, block):
         assert getattr(lib, name)(*args) == INVALID, name
 
 
+def test_a_page_has_fewer_scales_than_32_bits_count(lib):
+    big = dict(H_kv=4, page_rows=1 << 29, max_pages=1, stride_n=64, stride_h=64 << 29, stride_page=64 << 31)
+    for name, args in _args(_cache(**big), 1).items():
+        assert getattr(lib, name)(*args) == UNSUPPORTED, name
+
+
 def test_pointers_and_sizes_are_checked(lib):
     wrong = dict(
         fa_decode_e4m3=[(2, 0), (2, 3), (2, -2), (3, 0.0), (3, math.nan), (3, math.inf), (3, 3e38), (3, -1.0), (4, 0),
