@@ -6,7 +6,7 @@
 //
 // HBM is the bound if the instructions that every byte takes are few enough.  As
 // 16-bit numbers for mma.sync they are half of the time: 450 instructions for 4 KB (d 128),
-// 54 % of the issue slots, with little to wait for.  So the stored numbers go into tcgen05.mma
+// 48 % of the issue slots, and each warp waits for its own chain of them.  So the stored numbers go into tcgen05.mma
 // as they are, keys and values as the operand of 128 rows:
 //
 //  S [128 keys, 16] = K [128, d] Q^T             K-major, under the swizzle of 128 bytes
@@ -39,8 +39,8 @@
 // and no reduction over its keys.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 64 sequences of up to 8192 rows, 32 heads on 8
-// of d 128, 494 MB: 83.6 us, 87 % (the kernels of fa_decode_e4m3.cu: 88.6).  8 of 9728, 8 heads of d 256, 319 MB: 56 us,
-// 84 % (61.6); 32 heads on 8: 58.7 (62.9).
+// of d 128, 494 MB: 82.5 to 83.7 us, 88 % (the kernels of fa_decode_e4m3.cu: 87.2).  8 of 9728, 8 heads of d 256, 319 MB:
+// 55.4 us, 85 % (60.2); 32 heads on 8: 57.9 (61.4).
 
 #include "fa_decode.cuh"
 #include "fa_e4m3.cuh"
