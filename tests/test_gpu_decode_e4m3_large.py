@@ -198,6 +198,25 @@ def test_shared_pages():
     run_and_check(args)
 
 
+def test_offsets_beyond_32_bits():
+    """Pages further than 2^32 bytes into the pools, scales further than 2^31 bytes into theirs."""
+    pages, page, d = 140000, 256, 128  # 4.6e9 bytes a pool
+    ids = [139999, 3, 135000, 139990]
+    q, *small, table, lengths = make(1, 4, 1, d, page, [1000], seed=11, block=1, spare=0, junk=False)
+    far = [torch.empty(pages, 1, page, d, dtype=torch.uint8, device=DEV).view(F8) for _ in range(2)]
+    far += [torch.empty(pages, 1, page, device=DEV) for _ in range(2)]
+    for t, x in zip(far, small):
+        for i, p in enumerate(ids):
+            t[p] = x[table[0, i].item()]
+    wide = torch.full((1, SM * 2 * 56 * 128 // page + 1), -1, dtype=torch.int32, device=DEV)
+    wide[0, :4] = torch.tensor(ids)
+    assert is_large((q, *far, wide, lengths))
+    got = fa.attention_decode_e4m3(q, *far, wide, lengths)
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    check(got, q, *small, table, lengths, d ** -0.5)
+
+
 def test_strided_queries_and_given_outputs():
     q, *cache, table, lengths = large(5, 8, 2, 128, 16, [100, 0, 7, 64, 1000], seed=9)
     fused = torch.rand(5, 12, 128, device=DEV).add_(0.25).to(torch.bfloat16)  # queries, keys and values of one projection
