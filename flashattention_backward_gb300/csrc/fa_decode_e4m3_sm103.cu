@@ -12,12 +12,16 @@
 //  S [128 keys, 16] = K [128, d] Q^T             K-major, under the swizzle of 128 bytes
 //  O^T [d, 16] += V^T [d, 128 keys] P [128, 16]  the same rows of V, read MN-major
 //
-// and the other operand, queries and weights, is cut into e4m3 numbers of 4 bits
-// each, x = t0 + t1 / 32 + t2 / 1024, side by side as columns: three for a head, of the 16 that
-// a product has at least.  A head's queries are multiplied by the power of two that takes the largest
-// to 2^7 ... 2^8 before that: the 8 bits of a bf16 number are held exactly down to 2^-19 of the
-// largest, and to 2^-27 of it below.  Weights are rounded to the 11 bits of an fp16
-// number, of which three terms hold all but half a step: an eighth of half a step of O, at most.
+// and the other operand, queries and weights, is cut into terms of 8 bits, side by side as
+// columns, of which a product has 16 at least.
+//  Queries are three e4m3 numbers, x = t0 + t1 / 32 + t2 / 1024.  A head's are multiplied by the power of two
+//  that takes the largest to 2^7 ... 2^8 before that: the 8 bits of a bf16 number are held exactly down to
+//  2^-19 of the largest, and to 2^-27 of it below.
+//  Weights are four e5m2 numbers, x = t0 + t1 / 16 + t2 / 256 + t3 / 4096, off by at most 2^-15 of the weight or, if
+//  that is more, 2^-29, where the largest is 2^7 or more: 2^-36 of the largest weight.  Range counts here more than
+//  bits: the sum that O is divided by has every weight in fp32, and many small ones behind one that is large may be
+//  most of O.  Three e4m3 terms, 32 apart, with the largest weight at 2 lost all below 2^-20 of it: with 2^15 rows of
+//  2^-17 behind a first one whose value is 0, O was off by a fifth and more.
 // Sums are fp32: against 64 bits S and O were off by at most 2^-21.5 of the sum of their
 // terms' absolute values, with terms of 14 binades.
 //
@@ -35,7 +39,7 @@
 //
 // The maximum that weights are taken against moves only where a score passes it by 7
 // (weights up to 2^7 are as exact), and so does the power of two U that the weights are in
-// units of: p_j b_j / U is at most 2 when U is set and 256 ever.  So a tile takes one barrier
+// units of: p_j b_j / U is at most 2^8 when U is set and 2^15 ever.  So a tile takes one barrier
 // and no reduction over its keys.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 64 sequences of up to 8192 rows, 32 heads on 8
@@ -55,9 +59,9 @@ struct Tile8 {
   // Of an item's beginning and end, in tiles, with 1, 2, 3 and 4: 64 sequences of up to 8192 rows of d 128 82.9, 83.8, 84.1,
   // 84.8 us; 32 of up to 2048 of d 256 35.0, 32.1, 31.9, 32.5.
   static constexpr int kCost = D == 256 ? 2 : 1;
-  static constexpr int kTerms = 3;
-  static constexpr int kCols = kTerms * HP;     // term t of head h is column t HP + h
-  static constexpr int kN = 16;                 // of a product
+  // Terms of a number; term t of head h is column t HP + h.
+  static constexpr int kTermsQ = 3, kTermsP = 4;
+  static constexpr int kN = 16;                 // columns of a product
   static constexpr int kPieces = D / 16;        // of 16 bytes in a row
   static constexpr int kLd = 128;               // bytes between rows, a swizzle's width; d 256 is two halves
   static constexpr int kHalves = D == 256 ? 2 : 1;
@@ -80,7 +84,7 @@ struct Tile8 {
   static constexpr int kSmem = 1024 + kGroups * kGroupBytes;
   static constexpr int kGroupCols = kN * (2 + kHalves);  // S twice, O
   static constexpr uint32_t kTmem = kGroups * kGroupCols <= 64 ? 64 : 128;
-  static_assert(HP == 1 || HP == 4, "columns and their packing");
+  static_assert(HP == 1 || (HP == 4 && kTermsP * HP == kN), "columns and their packing");
   static_assert(kSmem <= 232448 - 4096 && kGroups * kGroupCols <= (int)kTmem && kGroupBytes % 1024 == 0, "shared and tensor memory");
   // where the piece of 16 bytes of a row is, from the beginning of a tile or of the queries' terms (`rows` of a half)
   __device__ static __forceinline__ int place(int row, int piece, int rows = kRows) {
@@ -88,9 +92,9 @@ struct Tile8 {
   }
 };
 constexpr uint32_t kSwizzle128 = 2;   // as descriptors name it
-constexpr float kStep = 32.f;         // between terms
-constexpr float kMostWeight = 256.f;  // in units of U, ever
-constexpr float kSetWeight = 2.f;     // and when U is set
+constexpr float kStepQ = 32.f, kStepP = 16.f;  // between terms
+constexpr float kMostWeight = 32768.f;  // in units of U, ever: e5m2's half step of it, 16 times itself, is below 57344
+constexpr float kSetWeight = 256.f;     // and when U is set
 constexpr float kMostScore = 7.f;     // above the maximum that weights are taken against
 constexpr float kLeastUnit = 0x1p-100f;
 
@@ -141,24 +145,40 @@ struct Row {
 
 // Terms added up: head h of HP.
 template <int HP, int kTerms, class R>
-__device__ __forceinline__ float sum_terms(const R& r, int h) {
+__device__ __forceinline__ float sum_terms(const R& r, int h, float step) {
   float x = r[(kTerms - 1) * HP + h];
 #pragma unroll
-  for (int t = kTerms - 2; t >= 0; --t) x = fmaf(x, 1.f / kStep, r[t * HP + h]);
+  for (int t = kTerms - 2; t >= 0; --t) x = fmaf(x, 1.f / step, r[t * HP + h]);
   return x;
 }
 
-// Two numbers, |x| <= 256, as terms: term t's in bits 0-7 and 8-15 of w[t].  They are rounded to fp16, whose 11 bits three
-// terms hold but for half a step of the last: what is left after a term is exact.
+// Two numbers of a query, |x| <= 256, as terms: term t's in bits 0-7 and 8-15 of w[t].  fp16 holds the 8 bits
+// of a bf16 number down to 2^-17, and what is left after a term exactly; the last term's steps are 2^-19.
 template <int kTerms>
-__device__ __forceinline__ void cut_terms(float x0, float x1, uint32_t (&w)[kTerms]) {
+__device__ __forceinline__ void cut_query(float x0, float x1, uint32_t (&w)[kTerms]) {
   __half2 x = __floats2half2_rn(x0, x1);
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) {
     w[t] = pack_e4m3x2(x);
     if (t + 1 == kTerms) break;
     const uint32_t y = e4m3x2_lo(w[t]);
-    x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&y)), __float2half2_rn(kStep));
+    x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&y)), __float2half2_rn(kStepQ));
+  }
+}
+
+// Two weights, 0 <= x <= kMostWeight, as terms of e5m2, as above.  What is left after the first, at most an eighth of a
+// weight's power of two, goes on as a number of fp16: its 11 bits are all that three more terms hold.
+template <int kTerms>
+__device__ __forceinline__ void cut_weights(float x0, float x1, uint32_t (&w)[kTerms]) {
+  w[0] = pack_e5m2x2(x0, x1);
+  const float2 first = f16x2_to_float2(e5m2x2(w[0]));
+  __half2 x = __floats2half2_rn((x0 - first.x) * kStepP, (x1 - first.y) * kStepP);
+#pragma unroll
+  for (int t = 1; t < kTerms; ++t) {
+    w[t] = pack_e5m2x2(x);
+    if (t + 1 == kTerms) break;
+    const uint32_t y = e5m2x2(w[t]);
+    x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2*>(&y)), __float2half2_rn(kStepP));
   }
 }
 
@@ -323,7 +343,7 @@ __device__ __forceinline__ void issue_products(const E4m3Params& a, Walk<M::kRow
                                                const ptx::Waiter& waiter) {
   constexpr int kStages = M::kStages, kN = M::kN;
   constexpr uint32_t kShape = 1u << 4 | (uint32_t)(kN >> 3) << 17 | 8u << 24;  // fp32 sums, n columns, 128 rows
-  constexpr uint32_t kMnMajor = 1u << 15 | 1u << 16;                           // both operands
+  constexpr uint32_t kWeights = 1u << 15 | 1u << 16 | 1u << 10;                // both operands MN-major, the second of e5m2
   auto bar = [&](uint64_t& b) { return ptx::smem_addr(&b); };
   auto wait = [&](uint64_t& b, uint32_t phase) { return ptx::wait_bounded(bar(b), phase, waiter, true); };
   const uint32_t tO = tmem + 2 * kN;
@@ -341,7 +361,7 @@ __device__ __forceinline__ void issue_products(const E4m3Params& a, Walk<M::kRow
     for (int x = 0; x < M::kHalves; ++x)
 #pragma unroll
       for (int k = 0; k < M::kRows / 32; ++k)
-        mma_e4m3(tO + x * kN, further(v, x * M::kRows * M::kLd + 32 * M::kLd * k), further(p, 512 * k), kShape | kMnMajor,
+        mma_e4m3(tO + x * kN, further(v, x * M::kRows * M::kLd + 32 * M::kLd * k), further(p, 512 * k), kShape | kWeights,
                  k > 0 || adds);
     ptx::tc_commit(bar(bars->empty[before.at]));
     ptx::tc_commit(bar(bars->o_done[two_before.at]));
@@ -429,11 +449,11 @@ __device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows
         if (u >= D / 4) continue;
 #pragma unroll
         for (int x = 0; x < 4; ++x) e[k][x] = isfinite(e[k][x]) ? e[k][x] * by : NAN;
-        uint32_t w0[M::kTerms], w1[M::kTerms];
-        cut_terms<M::kTerms>(e[k][0], e[k][1], w0);
-        cut_terms<M::kTerms>(e[k][2], e[k][3], w1);
+        uint32_t w0[M::kTermsQ], w1[M::kTermsQ];
+        cut_query<M::kTermsQ>(e[k][0], e[k][1], w0);
+        cut_query<M::kTermsQ>(e[k][2], e[k][3], w1);
 #pragma unroll
-        for (int t = 0; t < M::kTerms; ++t) {
+        for (int t = 0; t < M::kTermsQ; ++t) {
           const uint32_t at4 = sQ + M::place(t * HP + h, u / 4, M::kN) + u % 4 * 4;
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at4), "r"(__byte_perm(w0[t], w1[t], 0x5410)) : "memory");
         }
@@ -458,7 +478,7 @@ template <class M, int D, int HP>
 __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, int run, int piece, int group, uint32_t ring,
                                             Bars<M>* bars, uint32_t (*seen_at)[4], float (*qscales)[HP],
                                             float (*over_warps)[kWarps][HP], uint32_t tmem, const ptx::Waiter& waiter) {
-  constexpr int kStages = M::kStages, kTerms = M::kTerms, kCols = M::kCols, kN = M::kN, kHalves = M::kHalves;
+  constexpr int kStages = M::kStages, kTermsQ = M::kTermsQ, kTermsP = M::kTermsP, kN = M::kN, kHalves = M::kHalves;
   auto bar = [&](uint64_t& b) { return ptx::smem_addr(&b); };
   const int thread = threadIdx.x % kThreads, lane = thread & 31, warp = thread >> 5;
   const uint32_t my_row = tmem + ((uint32_t)(warp * 32) << 16), tO = my_row + 2 * kN;
@@ -488,29 +508,30 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
       const float ks = lds4(tile + M::kScales + thread * 4), vs = lds4(tile + M::kScales + 512 + thread * 4);
       float x[HP], w[HP], p[HP];
       {
-        Row<kCols> r;
+        Row<kTermsQ * HP> r;
         r.load(my_row + two.at * kN);
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(bars->s_empty[two.at]));
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          const float y = fmaf(sum_terms<HP, kTerms>(r, h) * qscale[h], ks, -base[h]);  // the score above the base
+          const float y = fmaf(sum_terms<HP, kTermsQ>(r, h, kStepQ) * qscale[h], ks, -base[h]);  // the score above the base
           x[h] = mine ? y : -INFINITY;
         }
       }
       // weights in units of U, as terms: this key's 16 columns of P
       auto store_weights = [&](const float (&w)[HP]) {
         const uint32_t to = tile + thread * 16;
-        uint32_t t[kTerms];
+        uint32_t t[kTermsP];
         if constexpr (HP == 1) {
-          cut_terms<kTerms>(w[0], 0.f, t);
-          const uint32_t x = (t[0] & 0xffu) | (t[1] & 0xffu) << 8 | (t[2] & 0xffu) << 16;
+          cut_weights<kTermsP>(w[0], 0.f, t);
+          const uint32_t x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
         } else {
-          uint32_t u[kTerms];
-          cut_terms<kTerms>(w[0], w[1], t);
-          cut_terms<kTerms>(w[2], w[3], u);
-          ptx::st_shared_v4(to, __byte_perm(t[0], u[0], 0x5410), __byte_perm(t[1], u[1], 0x5410), __byte_perm(t[2], u[2], 0x5410), 0);
+          uint32_t u[kTermsP];
+          cut_weights<kTermsP>(w[0], w[1], t);
+          cut_weights<kTermsP>(w[2], w[3], u);
+          ptx::st_shared_v4(to, __byte_perm(t[0], u[0], 0x5410), __byte_perm(t[1], u[1], 0x5410),
+                            __byte_perm(t[2], u[2], 0x5410), __byte_perm(t[3], u[3], 0x5410));
         }
         ptx::fence_proxy_async_smem();
       };
@@ -570,17 +591,16 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
         if (i > 0) {
 #pragma unroll
           for (int x = 0; x < kHalves; ++x) {
-            Row<kCols> r;
+            Row<kTermsP * HP> r;
             r.load(tO + x * kN);
-            if constexpr (HP == 1)
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tO + x * kN), "f"(r[0] * f[0]),
-                           "f"(r[1] * f[0]), "f"(r[2] * f[0]), "r"(r.r[3])
-                           : "memory");
-            else {
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) r.r[c] = __float_as_uint(r[c] * f[c % HP]);
+            for (int c = 0; c < kTermsP * HP; ++c) r.r[c] = __float_as_uint(r[c] * f[c % HP]);
+            if constexpr (HP == 1)
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tO + x * kN), "r"(r.r[0]),
+                           "r"(r.r[1]), "r"(r.r[2]), "r"(r.r[3])
+                           : "memory");
+            else
               ptx::tmem_st16(tO + x * kN, r.r);
-            }
           }
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
@@ -618,7 +638,7 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
       // a thread stores a column
 #pragma unroll
       for (int x = 0; x < kHalves; ++x) {
-        Row<kCols> r;
+        Row<kTermsP * HP> r;
         r.load(tO + x * kN);
         const int col = x * 128 + thread;
         if (col >= D) continue;
@@ -628,7 +648,7 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
           float sum = 0.f;
 #pragma unroll
           for (int k = 0; k < kWarps; ++k) sum += over_warps[2][k][h];
-          float o = sum_terms<HP, kTerms>(r, h) * (unit[h] * (1.f / kSetWeight));
+          float o = sum_terms<HP, kTermsP>(r, h, kStepP) * (unit[h] * (1.f / kSetWeight));
           if (whole) {
             const bool none = sum == 0.f;
             o = none ? 0.f : o * (1.f / sum);

@@ -47,6 +47,19 @@ __device__ __forceinline__ float4 e4m3x4_to_float4(uint32_t x) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Two numbers to e5m2, in the same way, |x| <= 57344; and back: an e5m2 number is the upper byte of an fp16 one.
+__device__ __forceinline__ uint32_t pack_e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_e5m2x2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t x) { return __byte_perm(x, 0, 0x1404); }
+
 // The smallest power of two s with t <= 448 s, 2^-126 at least, for the bits of
 // a finite t >= 0.  448 is 1.75 * 2^8: the addition carries into the exponent
 // where t's mantissa is above 1.75.
