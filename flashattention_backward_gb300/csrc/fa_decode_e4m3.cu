@@ -12,8 +12,8 @@
 // with d 128 and 256 and few heads are those of fa_decode_e4m3_sm103.cu.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 32 sequences of up to 2048 rows, 32 heads of d 64, 118 MB:
-// 31.3 us, 56 %.  125 MB of 32 sequences and 8 key heads with 4 heads a key head: d 128 28.8 us, 64 %, d 96 (145 MB) 33.5,
-// 64 %, d 32 39.2, 47 %; with 16: d 128 37.5, d 256 47.7; in fp32 with 8: d 64 31.5, d 128 31.5.  About 8 us of each are the
+// 32.2 us, 54 %.  125 MB of 32 sequences and 8 key heads with 4 heads a key head: d 128 29.5 us, 62 %, d 96 (145 MB) 34.4,
+// 62 %, d 32 40.7, 45 %; with 16: d 128 39.7, d 256 49.1; in fp32 with 8: d 64 31.5, d 128 31.5.  About 8 us of each are the
 // start of a call, the last tiles and the join, whatever the size; the smallest call takes 3.4.  A tile of 4 KB a warp takes 450
 // instructions at d 128 and 580 at d 64, half of the issue slots: fixed latencies, on three to four warps a scheduler,
 // bound the rest (16 instructions fewer a tile, without the mask, gained 1 %; a barrier fewer an item nothing).
@@ -41,9 +41,11 @@ namespace {
 // largest.  fp32 ones become the sum of two, the second 2^11 times itself: it takes
 // the place of a second group of 8 heads, at no more products.
 //
-// Weights: P b_j / U, U a power of two, as fp16 numbers: their 11 bits are an eighth of a half step of
-// a bf16 O.  With fp32 as the sum of two.  The maximum that weights are taken
-// against and U are moved only when a weight passes 2^kAhead (its bits are not
+// Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers: off by at most 2^-22 of the weight or, if that
+// is more, 2^-25, where the largest is 2^7 or more.  So the rounding of O is the only one to fewer than 16 bits, as in
+// fa_decode.  One number for bf16, 11 bits, takes 31.2 us for 32.2 (32 sequences of up to 2048 rows, 32 heads of d 64) and, with 16
+// heads a key head of d 128, 107 for 116 (64 of up to 8192), but where values cancel it loses bits that O has.
+// The maximum that weights are taken against and U are moved only when a weight passes 2^kAhead (its bits are not
 // the fewer for that), so that almost every tile does without the maximum over its
 // lanes and without a look at the accumulators.
 template <int D, int NH, bool kF32>
@@ -461,10 +463,8 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
             l[u] += p[u][o][0] + p[u][o][1];
             const float w0 = w[u][o][0] * per_unit[u], w1 = w[u][o][1] * per_unit[u];
             hi[u][o] = pack_f16x2(w0, w1);
-            if constexpr (kF32) {
-              const float2 z = f16x2_to_float2(hi[u][o]);
-              lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
-            }
+            const float2 z = f16x2_to_float2(hi[u][o]);
+            lo[u][o] = pack_f16x2(w0 - z.x, w1 - z.y);
           }
         // V: pieces of 8 keys x 8 pairs of columns; lane 8 n + r names row r of piece n
         const uint32_t v_at = tile + M::kRows * M::kPitchK + ((lane & 7) + (lane >> 3 & 1) * 8) * M::kPitchV + (lane >> 4) * 16;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
 #pragma unroll
               for (int u = 0; u < NH; ++u) {
                 mma16816_f16(acc[u][c + i], a0, a1, a2, a3, hi[u][2 * b], hi[u][2 * b + 1]);
-                if (kF32) mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
+                mma16816_f16(acc[u][c + i], a0, a1, a2, a3, lo[u][2 * b], lo[u][2 * b + 1]);
               }
             }
           }
