@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
   float qscale[NH];
   float acc[NH][M::kPieces][4];  // O^T, unnormalised, in units of unit / kTopWeight: columns 2 g, 2 g + 1 of 16, heads 2 q, 2 q + 1
   float m[NH], base[NH], l[NH];  // of heads g, g + 8; l of this lane's keys alone
-  float unit[NH], per_unit[NH];
+  // the largest weight that a unit was set for, and kTopWeight / unit.  Where the maximum moves the largest goes down by
+  // what the weights do, not in powers of two: else a unit stays up when its row is long of no account
+  float largest[NH], per_unit[NH];
   int stage = 0;
   bool first = true;             // item of the run
   if (some) do {
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
         m[u] = -INFINITY;
         base[u] = 0.f;
         l[u] = 0.f;
-        unit[u] = kLeastUnit;
+        largest[u] = kLeastUnit;
         per_unit[u] = kTopWeight / kLeastUnit;
 #pragma unroll
         for (int p = 0; p < M::kPieces; ++p)
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               most = fmaxf(most, w[u][o][e]);
             }
           // 2^7 above the maximum, or above the unit
-          passed |= top > m[u] + 7.f || most > kAhead * unit[u];
+          passed |= top > m[u] + 7.f || most * per_unit[u] > kAhead * kTopWeight;
         }
         if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
@@ -439,13 +441,10 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // the new unit: the power of two at or above what is largest, the old sums' unit or a weight
-            const float old = alpha * unit[u];
-            const float now = fmaxf(fmaxf(most, old), kLeastUnit);
-            unit[u] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
-            const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[u]));
-            per_unit[u] = kTopWeight * per;
-            const float f = old * per;
+            largest[u] = fmaxf(fmaxf(most, alpha * largest[u]), kLeastUnit);
+            const float old = alpha * inverse(per_unit[u]);
+            per_unit[u] = kTopWeight * inverse(unit_for(largest[u]));
+            const float f = old * per_unit[u];
             // the factors belong to heads g, the accumulators to heads 2q, 2q + 1
             const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
 #pragma unroll
@@ -509,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
         if (q == 0) {
           ml[warp][g + 8 * u] = make_float2(m[u], l[u]);
-          units[warp][g + 8 * u] = unit[u] * (1.f / kTopWeight);
+          units[warp][g + 8 * u] = inverse(per_unit[u]);
         }
       }
       __syncthreads();

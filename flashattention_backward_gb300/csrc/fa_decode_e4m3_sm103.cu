@@ -482,7 +482,9 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
   auto bar = [&](uint64_t& b) { return ptx::smem_addr(&b); };
   const int thread = threadIdx.x % kThreads, lane = thread & 31, warp = thread >> 5;
   const uint32_t my_row = tmem + ((uint32_t)(warp * 32) << 16), tO = my_row + 2 * kN;
-  float m[HP], base[HP], l[HP], unit[HP], per_unit[HP], qscale[HP];  // all but l are the group's
+  float m[HP], base[HP], l[HP], qscale[HP];  // all but l are the group's
+  // the largest weight that a unit was set for, and kSetWeight / unit; as in fa_decode_e4m3.cu
+  float largest[HP], per_unit[HP];
   Turn<kStages> turn;
   Turn<2> two, q;
   // the O of the tile before the one that it is the turn of
@@ -495,7 +497,7 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
     for (int h = 0; h < HP; ++h) {
       m[h] = -INFINITY;
       base[h] = l[h] = 0.f;
-      unit[h] = kLeastUnit;
+      largest[h] = kLeastUnit;
       per_unit[h] = kSetWeight / kLeastUnit;
       qscale[h] = qscales[q.at][h];
     }
@@ -566,7 +568,8 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
           m[h] = top;
           unset |= top == -INFINITY;
           l[h] *= alpha;
-          f[h] = alpha * unit[h];
+          f[h] = alpha * inverse(per_unit[h]);
+          largest[h] *= alpha;
           p[h] = ptx::ex2(x[h] - base[h]);
           w[h] = p[h] * vs;
         }
@@ -578,14 +581,11 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
         group_sync(group);
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          // the power of two at or above what is largest, the sums' unit or a weight
-          float now = fmaxf(f[h], kLeastUnit);
+          largest[h] = fmaxf(largest[h], kLeastUnit);
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) now = fmaxf(now, over_warps[1][k][h]);
-          unit[h] = __uint_as_float((__float_as_uint(now) + 0x7fffffu) & 0x7f800000u);
-          const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit[h]));
-          per_unit[h] = kSetWeight * per;
-          f[h] *= per;
+          for (int k = 0; k < kWarps; ++k) largest[h] = fmaxf(largest[h], over_warps[1][k][h]);
+          per_unit[h] = kSetWeight * inverse(unit_for(largest[h]));
+          f[h] *= per_unit[h];
           w[h] *= per_unit[h];
         }
         if (i > 0) {
@@ -648,7 +648,7 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
           float sum = 0.f;
 #pragma unroll
           for (int k = 0; k < kWarps; ++k) sum += over_warps[2][k][h];
-          float o = sum_terms<HP, kTermsP>(r, h, kStepP) * (unit[h] * (1.f / kSetWeight));
+          float o = sum_terms<HP, kTermsP>(r, h, kStepP) * inverse(per_unit[h]);
           if (whole) {
             const bool none = sum == 0.f;
             o = none ? 0.f : o * (1.f / sum);

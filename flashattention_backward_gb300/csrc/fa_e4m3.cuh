@@ -70,4 +70,9 @@ __device__ __forceinline__ float scale_for(uint32_t t) {
 // 1 / s of a power of two, 2^-126 to 2^126.
 __device__ __forceinline__ float inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 
+// The power of two that weights are in units of, for the largest of them: at or above it.
+__device__ __forceinline__ float unit_for(float largest) {
+  return __uint_as_float((__float_as_uint(largest) + 0x7fffffu) & 0x7f800000u);
+}
+
 }  // namespace fa

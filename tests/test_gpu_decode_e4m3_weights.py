@@ -51,8 +51,9 @@ PATHS = {
 }
 
 
-def cache(path, n, gaps, v, v_scales, top=30, columns=0, page=64):
-    """One sequence's rows with scores `gaps` (in bits) below `top` bits, a scale a row: q = 1, keys 1 times their scales."""
+def cache(path, n, gaps, v, v_scales, top=30, columns=0, page=64, heads=None):
+    """One sequence's rows with scores `gaps` (in bits) below `top` bits, a scale a row: q = 1, keys 1 times their scales.
+    heads: factors of the scores, for each query head of a key head."""
     d, group, dtype, S, _ = PATHS[path]
     pages = -(-n // page)
     kp = torch.full((pages, HK, page, d), 0x38, dtype=torch.uint8)  # 1.0
@@ -69,6 +70,8 @@ def cache(path, n, gaps, v, v_scales, top=30, columns=0, page=64):
     flat[:n] = torch.as_tensor(v, dtype=torch.float32)
     vp.copy_(flat.view(pages, 1, page, d).expand(-1, HK, -1, -1))
     q = torch.ones(S, HK * group, 1, d, dtype=dtype)
+    if heads is not None:
+        q *= torch.tensor(heads, dtype=dtype).repeat(HK)[:, None, None]
     table = torch.full((S, max(pages, columns)), -1, dtype=torch.int32)
     table[:, :pages] = torch.arange(pages)
     lengths = torch.full((S,), n, dtype=torch.int32)
@@ -86,17 +89,19 @@ def check(path, args, n):
     assert fa.get_device_status() == 0
     rows = lambda t: t[:, 0].reshape(-1, *t.shape[3:])[:n].cpu().float().double().numpy()
     k, v, b = rows(ks), rows(vp), rows(vs)
-    score = k * d * np.float64(np.float32(d ** -0.5))
-    p = np.exp(score - score.max())
-    w, l = p * b, p.sum()
-    ref, total = (w @ v) / l, (w @ np.abs(v)) / l
     r, a = (2.0 ** -15, 2.0 ** -36) if sm103 else (2.0 ** -22, 2.0 ** -32)
-    e = 2 * (2.0 ** -22 + np.abs(score).max() * 4 * 2.0 ** -24) + 2 * (4 * n / 64 + 64) * 2.0 ** -23
-    tol = HALF_STEP[dtype] * np.abs(ref) + (r + e) * total + a * n * w.max() * np.abs(v).max() / l
-    off = np.abs(o.cpu().double().numpy() - ref)
-    assert (off <= tol).all(), (float((off / tol).max()), float((off.max((0, 1, 2)) / np.abs(ref).clip(1e-300)).max()))
-    want = score.max() + np.log(l)
-    assert (np.abs(L.cpu().double().numpy() - want) <= np.abs(score).max() * 8 * 2.0 ** -24 + e + 2.0 ** -22 * abs(want)).all()
+    for h in range(group):
+        score = k * (d * np.float64(np.float32(d ** -0.5)) * q[0, h, 0, 0].item())
+        p = np.exp(score - score.max())
+        w, l = p * b, p.sum()
+        ref, total = (w @ v) / l, (w @ np.abs(v)) / l
+        e = 2 * (2.0 ** -22 + np.abs(score).max() * 4 * 2.0 ** -24) + 2 * (4 * n / 64 + 64) * 2.0 ** -23
+        tol = HALF_STEP[dtype] * np.abs(ref) + (r + e) * total + a * n * w.max() * np.abs(v).max() / l
+        off = np.abs(o[:, h::group].cpu().double().numpy() - ref)
+        assert (off <= tol).all(), (h, float((off / tol).max()), float((off.max((0, 1, 2)) / np.abs(ref).clip(1e-300)).max()))
+        want = score.max() + np.log(l)
+        off = np.abs(L[:, h::group].cpu().double().numpy() - want)
+        assert (off <= np.abs(score).max() * 8 * 2.0 ** -24 + e + 2.0 ** -22 * abs(want)).all()
 
 
 def some_values(n, d, seed, mean):
@@ -139,3 +144,16 @@ def test_values_that_cancel(path):
     gaps = np.where(np.arange(n) % 2, -np.log2((1 + 0.9 * 2.0 ** -11) / 2), 0.0)
     v = torch.where(torch.arange(n) % 2 > 0, 1.0, -0.5)[:, None].expand(-1, d)
     check(path, cache(path, n, gaps, v, np.ones(n), top=2, columns=3800 // 64 if PATHS[path][4] else 0), n)
+
+
+@pytest.mark.parametrize("path", [p for p in PATHS if PATHS[p][1] > 1])
+def test_a_large_scale_that_is_left_behind(path):
+    """The first row's scale is 2^80 times the others' and its value 0.  The scores rise from tile to tile: by 8 bits and more in
+    one head, so that the maxima of all move, and by 0.9 in the others, whose first row has as much weight as any at last."""
+    n, (d, group) = 12000, PATHS[path][:2]
+    v = some_values(n, d, 3, torch.arange(d) % 2)
+    v[0] = 0
+    scales = np.ones(n)
+    scales[0] = 2.0 ** 80
+    top = 0.9 * (n // 128)
+    check(path, cache(path, n, top - 0.9 * (np.arange(n) // 128), v, scales, top=top, heads=[9.5] + [1] * (group - 1)), n)
