@@ -87,7 +87,6 @@ struct Mma8 {
 };
 constexpr float kAhead = 128.f;   // 2^7
 constexpr float kTopWeight = 256.f;  // of a weight when U is set, as fp16: kAhead times that is below 65504
-constexpr float kLeastUnit = 0x1p-100f;
 
 __device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
         m[u] = -INFINITY;
         base[u] = 0.f;
         l[u] = 0.f;
-        largest[u] = kLeastUnit;
+        largest[u] = 0.f;
         per_unit[u] = kTopWeight / kLeastUnit;
 #pragma unroll
         for (int p = 0; p < M::kPieces; ++p)
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            largest[u] = fmaxf(fmaxf(most, alpha * largest[u]), kLeastUnit);
+            largest[u] = fmaxf(most, alpha * largest[u]);
             const float old = alpha * inverse(per_unit[u]);
             per_unit[u] = kTopWeight * inverse(unit_for(largest[u]));
             const float f = old * per_unit[u];

@@ -96,7 +96,6 @@ constexpr float kStepQ = 32.f, kStepP = 16.f;  // between terms
 constexpr float kMostWeight = 32768.f;  // in units of U, ever: e5m2's half step of it, 16 times itself, is below 57344
 constexpr float kSetWeight = 256.f;     // and when U is set
 constexpr float kMostScore = 7.f;     // above the maximum that weights are taken against
-constexpr float kLeastUnit = 0x1p-100f;
 
 // A group's barriers.
 template <class M>
@@ -497,7 +496,7 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
     for (int h = 0; h < HP; ++h) {
       m[h] = -INFINITY;
       base[h] = l[h] = 0.f;
-      largest[h] = kLeastUnit;
+      largest[h] = 0.f;
       per_unit[h] = kSetWeight / kLeastUnit;
       qscale[h] = qscales[q.at][h];
     }
@@ -581,7 +580,6 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
         group_sync(group);
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          largest[h] = fmaxf(largest[h], kLeastUnit);
 #pragma unroll
           for (int k = 0; k < kWarps; ++k) largest[h] = fmaxf(largest[h], over_warps[1][k][h]);
           per_unit[h] = kSetWeight * inverse(unit_for(largest[h]));
