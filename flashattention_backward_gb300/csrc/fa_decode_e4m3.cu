@@ -254,7 +254,8 @@ struct Columns {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[c][w][e] = 0.f;
   }
-  // Takes the head's largest finite value to 2^14 ... 2^15; returns what the products are to be multiplied by.
+  // Takes the head's largest value to 2^14 ... 2^15; returns what the products are to be multiplied by.  With one that is not
+  // finite all become NaN: an infinity could make all scores -inf, as if there were no rows.
   __device__ __forceinline__ float normalise() {
     uint32_t top = 0;
 #pragma unroll
@@ -262,14 +263,11 @@ struct Columns {
 #pragma unroll
       for (int w = 0; w < kWords; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t t = __float_as_uint(x[c][w][e]) & 0x7fffffffu;
-          top = max(top, t < 0x7f800000u ? t : 0u);
-        }
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[c][w][e]) & 0x7fffffffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = max((int)(top >> 23), 15) - 14;  // 1 ... 240
-    const float by = __uint_as_float((uint32_t)(254 - e) << 23);
+    const float by = top < 0x7f800000u ? __uint_as_float((uint32_t)(254 - e) << 23) : NAN;
 #pragma unroll
     for (int c = 0; c < M::kRuns; ++c)
 #pragma unroll
@@ -344,9 +342,9 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               const float x0 = x.x[c][w][2 * e], x1 = x.x[c][w][2 * e + 1];
               const uint32_t y = pack_f16x2(x0, x1);
               qf[c][w][2 * u + e] = y;
-              if constexpr (kF32) {  // what is left, 2^11 times itself; nothing of an infinity
+              if constexpr (kF32) {  // what is left, 2^11 times itself
                 const float2 z = f16x2_to_float2(y);
-                qf[c][w][2 + e] = pack_f16x2(isinf(x0) ? 0.f : (x0 - z.x) * 2048.f, isinf(x1) ? 0.f : (x1 - z.y) * 2048.f);
+                qf[c][w][2 + e] = pack_f16x2((x0 - z.x) * 2048.f, (x1 - z.y) * 2048.f);
               }
             }
         m[u] = -INFINITY;

@@ -93,3 +93,26 @@ def test_smallest_scales_beside_large_ones(path):
         want = values(f64(vp), f64(vs))[last[s], :, :8].mean(1)  # the others' weights are exp(-128 sqrt(d))
         got = f64(o)[s, :, 0].reshape(2, -1, d)
         assert np.abs(got - want[:, None]).max() <= (HALF_STEP[q.dtype] + 2.0 ** -14) * 448 * 2.0 ** -126
+
+
+@pytest.mark.parametrize("key", [1.0, -1.0, None])
+@pytest.mark.parametrize("path", PATHS)
+def test_an_infinite_query_makes_nan_of_its_head(path, key):
+    """Of any sign, whatever the keys' signs are (None: as they come) and however few there are; all scores may be
+    -inf by it. The other heads, and a sequence without rows, know nothing of it."""
+    args = cache(path, [300, 0, 17, 1, 1], seed=5)
+    if key:
+        args[1].view(torch.uint8).fill_(0x38 if key > 0 else 0xb8)
+    clean = fa.attention_decode_e4m3(*args)
+    q = args[0]
+    inf, d = float("inf"), q.shape[3]
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=q.device)
+    for s, h, c, x in ((0, 0, 0, inf), (0, -1, d - 1, -inf), (1, 0, 1, -inf), (2, 1, 17, -inf), (2, 0, 5, inf), (3, 0, 8, inf),
+                       (3, 1, 15, -inf), (4, 1, 3, inf), (4, 0, d // 2, -inf)):
+        q[s, h, 0, c] = x
+        hit[s, h] = s != 1
+    o, L = fa.attention_decode_e4m3(*args)
+    torch.cuda.synchronize()
+    assert fa.get_device_status() == 0
+    assert o[hit].isnan().all() and L[hit].isnan().all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(L[~hit], clean[1][~hit])
