@@ -621,10 +621,6 @@ Cut cut_e4m3(const fa_cache& c, int H) {
   return large(c, H, k) ? cut_e4m3_sm103(c, H) : k;
 }
 
-fa_status check(const fa_cache* c, int32_t block_rows, int32_t H) {
-  const fa_status st = check_cache_e4m3(c, block_rows);
-  return st == FA_OK ? check_heads(c, H) : st;
-}
 
 }  // namespace
 }  // namespace fa
@@ -632,7 +628,9 @@ fa_status check(const fa_cache* c, int32_t block_rows, int32_t H) {
 extern "C" {
 
 size_t fa_decode_e4m3_workspace_bytes(const fa_cache* c, int32_t H) {
-  return fa::check(c, 1, H) == FA_OK ? fa::workspace_of(fa::cut_e4m3(*c, H), c->d) : 0;
+  // the size does not go by the scales, whose number is for the call to check
+  const bool good = fa::check_pools(c, 1) == FA_OK && fa::check_heads(c, H) == FA_OK;
+  return good ? fa::workspace_of(fa::cut_e4m3(*c, H), c->d) : 0;
 }
 
 fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float scale, const void* Q,
@@ -641,7 +639,8 @@ fa_status fa_decode_e4m3(const fa_cache* c, int32_t block_rows, int32_t H, float
                          const int32_t* lengths, void* O, int64_t o_stride_s, int64_t o_stride_h, float* L,
                          void* workspace, size_t workspace_bytes, void* stream) {
   fa::NvtxRange range("fa_decode_e4m3");
-  fa_status st = fa::check(c, block_rows, H);
+  fa_status st = fa::check_cache_e4m3(c, block_rows);
+  if (st == FA_OK) st = fa::check_heads(c, H);
   if (st != FA_OK) return st;
   const fa::DecodeCall x = {c, H, scale, Q, q_stride_s, q_stride_h, K_pages, V_pages, page_table, lengths,
                             O, o_stride_s, o_stride_h, L, workspace, workspace_bytes};
