@@ -257,88 +257,74 @@ struct ReadParams {
   int64_t pp, ph, pn;   // of the pools
 };
 
-// A thread takes kUnits units of 16 numbers, of K and of V.
-template <class T, int kUnits>
+// A thread takes 16 numbers, of K and of V.
+template <class T>
 __global__ void __launch_bounds__(kThreads) read_e4m3_kernel(const ReadParams a) {
   after_stream();
-  int64_t from[kUnits], to[kUnits], scale_at[kUnits];
-  bool there[kUnits], on[kUnits];
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k) {
-    uint32_t c, i, g;
-    const uint32_t r = a.row_units.div(k * kThreads + threadIdx.x, &c);
-    const uint32_t row = blockIdx.x * (uint32_t)a.block_of_rows + r;
-    there[k] = r < (uint32_t)a.block_of_rows && row < a.total_rows;
-    on[k] = false;
-    if (!there[k]) continue;
-    const uint32_t s = a.heads.div(a.rows.div(row, &i), &g);
-    const bool first_of_s = c == 0 && i == 0 && g == 0;
-    const int64_t start = a.start ? a.start[s] : 0;
-    int count = (int)a.rows.d;
-    if (a.counts) {
-      const int given = a.counts[s];
-      if ((given < 0 || given > count) && first_of_s) report_pages(a.status);
-      count = min(max(given, 0), count);
-    }
-    if (start < 0 && first_of_s) report_pages(a.status);
-    to[k] = s * a.sb + g * a.sh + i * a.sn + c * 16 * (int)sizeof(T);
-    on[k] = start >= 0 && (int)i < count;
-    if (!on[k]) continue;
+  uint32_t c, i, g;
+  const uint32_t r = a.row_units.div(threadIdx.x, &c);
+  const uint32_t row = blockIdx.x * (uint32_t)a.block_of_rows + r;
+  if (r >= (uint32_t)a.block_of_rows || row >= a.total_rows) return;
+  const uint32_t s = a.heads.div(a.rows.div(row, &i), &g);
+  const bool first_of_s = c == 0 && i == 0 && g == 0;
+  const int64_t start = a.start ? a.start[s] : 0;
+  int count = (int)a.rows.d;
+  if (a.counts) {
+    const int given = a.counts[s];
+    if ((given < 0 || given > count) && first_of_s) report_pages(a.status);
+    count = min(max(given, 0), count);
+  }
+  if (start < 0 && first_of_s) report_pages(a.status);
+  const int64_t to = s * a.sb + g * a.sh + i * a.sn + c * 16 * (int)sizeof(T);
+  uint4 q[2] = {};
+  float scale[2] = {};  // where nothing is read: 0 times 0
+  if (start >= 0 && (int)i < count) {
     const int64_t pos = start + i;
     const int64_t col = pos < (int64_t(1) << 31) ? (int64_t)a.page_rows.div((uint32_t)pos) : a.max_pages;
     int page = -1;
     if (col < a.max_pages) page = a.table[s * a.table_stride + col];
-    on[k] = page >= 0 && page < a.num_pages;
-    if (!on[k] && c == 0) report_pages(a.status);
-    if (!on[k]) continue;
-    const int in_page = (int)(pos - col * a.page_rows.d);
-    from[k] = page * a.pp + g * a.ph + in_page * a.pn + c * 16;
-    scale_at[k] = ((int64_t)page * a.heads.d + g) * (a.page_rows.d / a.block_rows.d) + a.block_rows.div(in_page);
+    if (page >= 0 && page < a.num_pages) {
+      const int in_page = (int)(pos - col * a.page_rows.d);
+      const int64_t from = page * a.pp + g * a.ph + in_page * a.pn + c * 16;
+      const int64_t scale_at =
+          ((int64_t)page * a.heads.d + g) * (a.page_rows.d / a.block_rows.d) + a.block_rows.div(in_page);
+#pragma unroll
+      for (int pool = 0; pool < 2; ++pool) {
+        q[pool] = *reinterpret_cast<const uint4*>(a.pages[pool] + from);
+        scale[pool] = a.scales[pool][scale_at];
+      }
+    } else if (c == 0) {
+      report_pages(a.status);
+    }
   }
-  uint4 q[2][kUnits];
-  float scale[2][kUnits];
 #pragma unroll
-  for (int k = 0; k < kUnits; ++k)
+  for (int pool = 0; pool < 2; ++pool) {
+    const uint32_t w[4] = {q[pool].x, q[pool].y, q[pool].z, q[pool].w};
+    constexpr int kWords = 16 * sizeof(T) / 4;
+    uint32_t out[kWords];
 #pragma unroll
-    for (int pool = 0; pool < 2; ++pool) {
-      q[pool][k] = make_uint4(0, 0, 0, 0);
-      scale[pool][k] = 0.f;
-      if (!on[k]) continue;
-      q[pool][k] = *reinterpret_cast<const uint4*>(a.pages[pool] + from[k]);
-      scale[pool][k] = a.scales[pool][scale_at[k]];
-    }
-#pragma unroll
-  for (int k = 0; k < kUnits; ++k)
-#pragma unroll
-    for (int pool = 0; pool < 2; ++pool) {
-      if (!there[k]) continue;
-      const uint32_t w[4] = {q[pool][k].x, q[pool][k].y, q[pool][k].z, q[pool][k].w};
-      constexpr int kWords = 16 * sizeof(T) / 4;
-      uint32_t out[kWords];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float4 x = e4m3x4_to_float4(w[e]);
-        const float by = scale[pool][k];
-        // nothing is read: 0 times 0
-        x = make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
-        if constexpr (sizeof(T) == 2) {
-          out[2 * e] = ptx::pack_bf16x2(x.x, x.y), out[2 * e + 1] = ptx::pack_bf16x2(x.z, x.w);
-        } else {
-          out[4 * e] = __float_as_uint(x.x), out[4 * e + 1] = __float_as_uint(x.y);
-          out[4 * e + 2] = __float_as_uint(x.z), out[4 * e + 3] = __float_as_uint(x.w);
-        }
-      }
-      char* dst = a.X[pool] + to[k];
-      if (a.wide) {
-#pragma unroll
-        for (int e = 0; e < kWords; e += 8)
-          ptx::st_global_v8(dst + 4 * e, out[e], out[e + 1], out[e + 2], out[e + 3], out[e + 4], out[e + 5], out[e + 6], out[e + 7]);
+    for (int e = 0; e < 4; ++e) {
+      float4 x = e4m3x4_to_float4(w[e]);
+      const float by = scale[pool];
+      x = make_float4(x.x * by, x.y * by, x.z * by, x.w * by);
+      if constexpr (sizeof(T) == 2) {
+        out[2 * e] = ptx::pack_bf16x2(x.x, x.y), out[2 * e + 1] = ptx::pack_bf16x2(x.z, x.w);
       } else {
-#pragma unroll
-        for (int e = 0; e < kWords; e += 4)
-          *reinterpret_cast<uint4*>(dst + 4 * e) = make_uint4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+        out[4 * e] = __float_as_uint(x.x), out[4 * e + 1] = __float_as_uint(x.y);
+        out[4 * e + 2] = __float_as_uint(x.z), out[4 * e + 3] = __float_as_uint(x.w);
       }
     }
+    char* dst = a.X[pool] + to;
+    if (a.wide) {
+#pragma unroll
+      for (int e = 0; e < kWords; e += 8)
+        ptx::st_global_v8(dst + 4 * e, out[e], out[e + 1], out[e + 2], out[e + 3], out[e + 4], out[e + 5], out[e + 6], out[e + 7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kWords; e += 4)
+        *reinterpret_cast<uint4*>(dst + 4 * e) = make_uint4(out[e], out[e + 1], out[e + 2], out[e + 3]);
+    }
+  }
 }
 
 // Whether rows begin on 32 bytes.
@@ -353,8 +339,6 @@ cudaError_t launch_append(const AppendParams& a, int most_units, cudaStream_t s)
     return launch_early(append_e4m3_kernel<T, 32>, dim3((unsigned)ceil_div(a.teams, kThreads / 32), 2), kThreads, 0, s, 1, a);
   return launch_early(append_e4m3_kernel<T, kThreads>, dim3(a.teams, 2), kThreads, 0, s, 1, a);
 }
-
-constexpr int kReadUnits = 1;
 
 // Arguments that both calls take.
 fa_status check_rows(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K, const void* V, int64_t ss,
@@ -443,7 +427,7 @@ fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows
   a.page_rows = fa::FastDiv(c->page_rows);
   a.block_rows = fa::FastDiv(block_rows);
   a.total_rows = (uint32_t)((int64_t)c->S * c->H_kv * rows);
-  a.block_of_rows = fa::kReadUnits * fa::kThreads / (c->d / 16);
+  a.block_of_rows = fa::kThreads / (c->d / 16);
   a.wide = fa::on_32(K, V, stride_s * es, stride_h * es, stride_n * es);
   a.num_pages = c->num_pages;
   a.max_pages = c->max_pages;
@@ -457,8 +441,8 @@ fa_status fa_cache_read_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows
   const dim3 grid((unsigned)fa::ceil_div(a.total_rows, a.block_of_rows));
   const cudaStream_t s = (cudaStream_t)stream;
   return fa::status_of(c->dtype == FA_BF16
-                           ? fa::launch_early(fa::read_e4m3_kernel<__nv_bfloat16, fa::kReadUnits>, grid, fa::kThreads, 0, s, 1, a)
-                           : fa::launch_early(fa::read_e4m3_kernel<float, fa::kReadUnits>, grid, fa::kThreads, 0, s, 1, a));
+                           ? fa::launch_early(fa::read_e4m3_kernel<__nv_bfloat16>, grid, fa::kThreads, 0, s, 1, a)
+                           : fa::launch_early(fa::read_e4m3_kernel<float>, grid, fa::kThreads, 0, s, 1, a));
 }
 
 }  // extern "C"
