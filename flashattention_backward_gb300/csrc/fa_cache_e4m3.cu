@@ -368,6 +368,8 @@ fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t ro
   const fa_status st = fa::check_rows(c, block_rows, rows, K, V, stride_s, stride_h, stride_n, K_pages, V_pages,
                                       K_scales, V_scales, page_table, start, counts, false);
   if (st != FA_OK) return st;
+  // a block's units are counted in 32 bits, and a loop over them ends by that
+  if ((int64_t)block_rows * (c->d / 16) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   const int es = fa::elem_size(c->dtype);
   fa::AppendParams a;
   a.status = fa::device_status_word();
@@ -397,8 +399,7 @@ fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t ro
   a.pn = c->stride_n;
   a.teams = (uint32_t)((int64_t)c->S * c->H_kv * many);  // many <= rows, so fewer than 2^31
   a.wide = fa::on_32(K, V, a.sb, a.sh, a.sn);
-  const int64_t most_units = (int64_t)(rows < block_rows ? rows : block_rows) * (c->d / 16);
-  const int units = (int)(most_units < (1 << 30) ? most_units : 1 << 30);
+  const int units = (rows < block_rows ? rows : block_rows) * (c->d / 16);
   const cudaStream_t s = (cudaStream_t)stream;
   return fa::status_of(c->dtype == FA_BF16 ? fa::launch_append<__nv_bfloat16>(a, units, s) : fa::launch_append<float>(a, units, s));
 }

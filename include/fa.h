@@ -365,7 +365,7 @@ fa_status fa_cache_copy_pages(const fa_cache* c, int32_t max_moves, const int32_
  * are divided by what it grew by and rounded once more: exact, but for
  * numbers that end below 2^-6.  Rows of a touched block behind the new ones are
  * taken to hold nothing.  A page that is written to stands once in the table.
- * rows >= 1, S * H_kv * rows < 2^31.  Neither the pools nor the scales of K and
+ * rows >= 1, S * H_kv * rows < 2^31, block_rows * d < 2^35.  Neither the pools nor the scales of K and
  * V may be the same memory. */
 fa_status fa_cache_append_e4m3(const fa_cache* c, int32_t block_rows, int32_t rows, const void* K, const void* V,
                                int64_t stride_s, int64_t stride_h, int64_t stride_n, void* K_pages, void* V_pages,

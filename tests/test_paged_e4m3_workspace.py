@@ -1,4 +1,5 @@
-"""The size of fa_decode_e4m3's workspace for caches that are legal with some numbers of scales alone."""
+"""The paged cache in 8 bits at the largest pages, on the host: the size of fa_decode_e4m3's workspace where some numbers
+of scales alone are allowed, and blocks that fa_cache_append_e4m3 could not count its way through."""
 
 import ctypes
 
@@ -42,3 +43,21 @@ def test_a_cache_or_heads_that_are_refused_have_none(lib):
         assert fa.fa_decode_e4m3_workspace_bytes(fa.FaCache(**{**good, **bad}), 4) == 0
     for heads in (0, 3, -2, 2 * 513):
         assert fa.fa_decode_e4m3_workspace_bytes(fa.FaCache(**good), heads) == 0
+
+
+@pytest.mark.parametrize("d,dtype", [(16, fa.FA_FP32), (32, fa.FA_BF16), (64, fa.FA_FP32), (96, fa.FA_BF16), (128, fa.FA_BF16),
+                                     (256, fa.FA_FP32), (256, fa.FA_BF16)])
+def test_an_append_into_too_large_a_block_is_refused(lib, d, dtype):
+    """With 2^31 units of 16 numbers or more in a block their count, or its way round 32 bits, would not end. Rows outside
+    may have a stride of 0, so that little memory is needed to ask for it."""
+    for log_rows in (26, 27, 28, 29, 30):
+        rows = 1 << log_rows
+        c = fa.FaCache(num_pages=1, page_rows=rows, H_kv=1, d=d, dtype=dtype, S=1, max_pages=1, reserved=0,
+                       stride_page=rows * d, stride_h=rows * d, stride_n=d, table_stride=1)
+        for block in (rows, rows // 2, rows // 4):
+            # no place for the new rows: what fits is refused for that, before it reaches a device
+            args = [ctypes.byref(c), block, 1, 0, 0, 0, 0, 0, BAD, 2 * BAD, 3 * BAD, 4 * BAD, BAD, BAD, BAD, None]
+            assert lib.fa_cache_append_e4m3(*args) == fa.FA_ERR_INVALID_ARG
+            if block * d >= 1 << 35:
+                args[3:5] = 5 * BAD, 6 * BAD
+                assert lib.fa_cache_append_e4m3(*args) == fa.FA_ERR_UNSUPPORTED
