@@ -84,6 +84,7 @@ struct Tile8 {
   static constexpr int kSmem = 1024 + kGroups * kGroupBytes;
   static constexpr int kGroupCols = kN * (2 + kHalves);  // S twice, O
   static constexpr uint32_t kTmem = kGroups * kGroupCols <= 64 ? 64 : 128;
+  static_assert(D == 128 || D == 256, "rows of one or two swizzles' width");
   static_assert(HP == 1 || (HP == 4 && kTermsP * HP == kN), "columns and their packing");
   static_assert(kSmem <= 232448 - 4096 && kGroups * kGroupCols <= (int)kTmem && kGroupBytes % 1024 == 0, "shared and tensor memory");
   // where the piece of 16 bytes of a row is, from the beginning of a tile or of the queries' terms (`rows` of a half)
@@ -406,7 +407,7 @@ __device__ __forceinline__ void issue_products(const E4m3Params& a, Walk<M::kRow
 template <class M, int D, int HP>
 __device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows, M::kCost> at, int piece, uint32_t ring, Bars<M>* bars,
                                               float (*qscales)[HP], const ptx::Waiter& waiter) {
-  constexpr int kUnits = (D / 4 + 31) / 32;  // of 4 columns of a head, a lane
+  constexpr int kUnits = D / 128;  // of 4 columns of a head, a lane
   const int lane = threadIdx.x & 31;
   for (int n = 0;; ++n) {
     const int to = n & 1;
@@ -421,8 +422,7 @@ __device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows
       for (int k = 0; k < kUnits; ++k) {
         const int u = lane + 32 * k;
         y[h][k] = make_uint2(0, 0);
-        if (h < heads && u < D / 4)
-          y[h][k] = *reinterpret_cast<const uint2*>(a.Q + at.s * a.qs + (int64_t)(h0 + h) * a.qh + u * 8);
+        if (h < heads) y[h][k] = *reinterpret_cast<const uint2*>(a.Q + at.s * a.qs + (int64_t)(h0 + h) * a.qh + u * 8);
       }
 #pragma unroll
     for (int h = 0; h < HP; ++h) {
@@ -445,7 +445,6 @@ __device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
         const int u = lane + 32 * k;
-        if (u >= D / 4) continue;
 #pragma unroll
         for (int x = 0; x < 4; ++x) e[k][x] = isfinite(e[k][x]) ? e[k][x] * by : NAN;
         uint32_t w0[M::kTermsQ], w1[M::kTermsQ];
@@ -639,7 +638,6 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
         Row<kTermsP * HP> r;
         r.load(tO + x * kN);
         const int col = x * 128 + thread;
-        if (col >= D) continue;
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
           if (h >= heads) continue;
