@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
   uint32_t qf[M::kRuns][kWords][2 * (kF32 ? 2 : NH)];
   float qscale[NH];
   float acc[NH][M::kPieces][4];  // O^T, unnormalised, in units of unit / kTopWeight: columns 2 g, 2 g + 1 of 16, heads 2 q, 2 q + 1
-  float m[NH], base[NH], l[NH];  // of heads g, g + 8; l of this lane's keys alone
+  float m[NH], l[NH];  // of heads g, g + 8; l of this lane's keys alone
   // the largest weight that a unit was set for, and kTopWeight / unit.  Where the maximum moves the largest goes down by
   // what the weights do, not in powers of two: else a unit stays up when its row is long of no account
   float largest[NH], per_unit[NH];
@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               }
             }
         m[u] = -INFINITY;
-        base[u] = 0.f;
         l[u] = 0.f;
         largest[u] = 0.f;
         per_unit[u] = kTopWeight / kLeastUnit;
@@ -400,16 +399,18 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
         bool passed = false;
 #pragma unroll
         for (int u = 0; u < NH; ++u) {
+          const float base = base_of(m[u]);
           float top = -INFINITY, most = 0.f;
 #pragma unroll
           for (int o = 0; o < 2 * kSub; ++o)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float dot = kF32 ? fmaf(s[o][2 + e], 1.f / 2048.f, s[o][e]) : s[o][2 * u + e];
-              const float y = dot * qscale[u] * (e ? ks[o].y : ks[o].x);
+              // the two scales first, as the product with one of them may be too large or too small
+              const float y = dot * (qscale[u] * (e ? ks[o].y : ks[o].x));
               x[u][o][e] = mine >> (8 * o + e) & 1 ? y : -INFINITY;
               top = fmaxf(top, x[u][o][e]);
-              p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
+              p[u][o][e] = ptx::ex2(x[u][o][e] - base);
               w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
               most = fmaxf(most, w[u][o][e]);
             }
@@ -424,15 +425,14 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
             for (int o = 0; o < 2 * kSub; ++o) top = fmaxf(top, fmaxf(x[u][o][0], x[u][o][1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            base[u] = base_of(top);
-            const float alpha = ptx::ex2(m[u] - base[u]);
+            const float base = base_of(top), alpha = ptx::ex2(m[u] - base);
             m[u] = top;
             l[u] *= alpha;
 #pragma unroll
             for (int o = 0; o < 2 * kSub; ++o)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                p[u][o][e] = ptx::ex2(x[u][o][e] - base[u]);
+                p[u][o][e] = ptx::ex2(x[u][o][e] - base);
                 w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
                 most = fmaxf(most, w[u][o][e]);
               }

@@ -514,7 +514,8 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
         ptx::mbar_arrive(bar(bars->s_empty[two.at]));
 #pragma unroll
         for (int h = 0; h < HP; ++h) {
-          const float y = fmaf(sum_terms<HP, kTermsQ>(r, h, kStepQ) * qscale[h], ks, -base[h]);  // the score above the base
+          // the score above the base; the two scales first, as the sum times one of them may be too large or too small
+          const float y = fmaf(sum_terms<HP, kTermsQ>(r, h, kStepQ), qscale[h] * ks, -base[h]);
           x[h] = mine ? y : -INFINITY;
         }
       }

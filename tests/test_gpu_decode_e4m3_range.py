@@ -116,3 +116,14 @@ def test_an_infinite_query_makes_nan_of_its_head(path, key):
     assert fa.get_device_status() == 0
     assert o[hit].isnan().all() and L[hit].isnan().all()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(L[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("e", [126, 118, -118, -126])
+@pytest.mark.parametrize("path", PATHS)
+def test_queries_and_keys_at_opposite_ends(path, e):
+    """Queries of up to 2^e and keys with scales that take the scores back to some units."""
+    args = cache(path, [300, 0, 17, 1], seed=6)
+    q, ks = args[0], args[3]
+    q.mul_(2.0 ** (e - 1))
+    ks.mul_(2.0 ** (1 - e if e > 0 else -e - 8))
+    check(args, 2.0 ** -9)
