@@ -12,10 +12,10 @@
 // with d 128 and 256 and few heads are those of fa_decode_e4m3_sm103.cu.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 32 sequences of up to 2048 rows, 32 heads of d 64, 118 MB:
-// 32.2 us, 54 %.  125 MB of 32 sequences and 8 key heads with 4 heads a key head: d 128 29.5 us, 62 %, d 96 (145 MB) 34.4,
-// 62 %, d 32 40.7, 45 %; with 16: d 128 39.7, d 256 49.1; in fp32 with 8: d 64 31.5, d 128 31.5.  About 8 us of each are the
-// start of a call, the last tiles and the join, whatever the size; the smallest call takes 3.4.  A tile of 4 KB a warp takes 450
-// instructions at d 128 and 580 at d 64, half of the issue slots: fixed latencies, on three to four warps a scheduler,
+// 32.3 us, 54 %.  125 MB of 32 sequences and 8 key heads with 4 heads a key head: d 128 29.6 us, 62 %, d 96 (145 MB) 34.6,
+// 62 %, d 32 41.0, 45 %; with 16: d 128 39.8, d 256 47.2; in fp32 with 8: d 64 31.5, d 128 31.5.  About 8 us of each are the
+// start of a call, the last tiles and the join, whatever the size; the smallest call takes 3.4.  A warp's instructions for 4 KB are 450
+// at d 128 and 570 at d 64, half of the issue slots: fixed latencies, on three to four warps a scheduler,
 // bound the rest (16 instructions fewer a tile, without the mask, gained 1 %; a barrier fewer an item nothing).
 
 #include "fa_decode.cuh"
@@ -55,8 +55,8 @@ struct Mma8 {
   static constexpr int kTile = kWarps * kRows;
   // Of an item's beginning and end, in tiles: queries to turn into fragments and a sum over the block cost as much as 256
   // rows.  With 128, 256, 384 and 512, sequences of up to some thousand rows, 8 key heads, us: d 64, 8 heads a key head
-  // 31.3, 30.7, 30.9, 31.4; d 96, 4: 33.9, 33.7, 34.1, 35.1; d 128, 8: 30.2, 30.0, 30.7, 31.4; d 128, 32: 67.7, 60.7, 62.2,
-  // 62.7; d 256, 16: 57.0, 48.3, 44.1, 44.5.  One tile, as for rows of 16 bits: 30.8, 35.7, 33.2, 75.7, 72.4.
+  // 31.7, 30.7, 31.6, 32.0; d 96, 4: 34.0, 34.5, 35.1, 36.1; d 128, 8: 30.6, 30.2, 31.1, 31.9; d 128, 32: 70.1, 65.5, 67.4,
+  // 68.1; d 256, 16: 55.9, 47.2, 45.5, 46.9.  One tile, as for rows of 16 bits: 31.7, 35.6, 33.3, 78.4, 71.4.
   static constexpr int kCost = 256 / kTile;
   static constexpr int kRun = D % 64 == 0 ? 16 : D % 32 == 0 ? 8 : 4;  // bytes of a key that a lane reads at a time
   static constexpr int kRuns = D / (4 * kRun);
@@ -588,14 +588,14 @@ cudaError_t launch_d(const fa_cache& c, const Cut& k, const E4m3Params& a, cudaS
 
 // Clusters of 16 blocks get two tiles a block at most, of 2 to 8 six, blocks alone twelve: then the runs and the join are
 // quicker.  Clusters against runs, 8 key heads and 4 heads a key head, all sequences of the table's size, us:
-//   16 blocks, 3 tiles:  d 64 9.9, 10.1   d 96 9.3, 9.9    d 128 10.4, 9.8   fp32 of d 128 11.1, 10.5
-//   8 blocks, 6 tiles:   d 64 11.9, 12.7  d 96 10.3, 12.0  d 128 11.3, 12.2  d 256, 4 blocks: 16.5, 18.3
-//             8:         d 64 14.0, 14.3  d 96 12.0, 12.9  d 128 13.5, 13.8                   18.8, 20.5
-//   1 block, 12 tiles:   d 64 17.0, 18.0  d 96 13.6, 15.8  d 128 14.9, 17.9  d 256 22.6, 26.7
+//   16 blocks, 3 tiles:  d 64 10.1, 10.1  d 96 9.6, 9.9    d 128 10.6, 9.8   fp32 of d 128 10.8, 10.2
+//   8 blocks, 6 tiles:   d 64 11.9, 12.9  d 96 10.6, 12.2  d 128 11.5, 12.5  d 256, 4 blocks: 16.6, 18.7
+//             8:         d 64 14.3, 14.5  d 96 12.2, 13.2  d 128 13.7, 14.1                   19.0, 21.0
+//   1 block, 12 tiles:   d 64 17.3, 18.6  d 96 13.9, 16.1  d 128 15.4, 18.6  d 256 22.7, 27.0
 // and of all sizes up to it:
-//   8 blocks, 6 tiles:   d 64 11.2, 11.3  d 96 9.9, 11.0   d 128 10.7, 11.2  d 256, 4 blocks: 13.7, 14.0
-//             8:         d 64 12.8, 11.9  d 96 11.0, 11.1  d 128 12.0, 11.6                   17.0, 14.2
-//   1 block, 12 tiles:   d 64 12.9, 13.0  d 96 11.7, 12.4  d 128 12.7, 13.6  d 256 19.4, 21.2
+//   8 blocks, 6 tiles:   d 64 11.3, 11.6  d 96 10.3, 11.0  d 128 11.0, 11.5  d 256, 4 blocks: 14.2, 14.2
+//             8:         d 64 13.2, 12.1  d 96 11.3, 11.3  d 128 12.2, 11.7                   17.5, 14.7
+//   1 block, 12 tiles:   d 64 13.2, 13.5  d 96 12.2, 12.8  d 128 13.5, 14.1  d 256 19.5, 21.6
 constexpr ClusterTiles kTilesAlone = {2, 6, 12};
 
 template <int D>

@@ -43,8 +43,8 @@
 // and no reduction over its keys.
 //
 // Measured (GPU time; the share is of the 6.8 TB/s of a copy): 64 sequences of up to 8192 rows, 32 heads on 8
-// of d 128, 494 MB: 82.5 to 83.7 us, 88 % (the kernels of fa_decode_e4m3.cu: 87.2).  8 of 9728, 8 heads of d 256, 319 MB:
-// 55.4 us, 85 % (60.2); 32 heads on 8: 57.9 (61.4).
+// of d 128, 494 MB: 82.7 to 83.8 us, 87 to 88 % (the kernels of fa_decode_e4m3.cu: 88.7).  32 of up to 7296, 8 heads of d 256,
+// 462 MB: 77.3 us, 88 % (83.5); 32 heads on 8: 79.9 (85.1).
 
 #include "fa_decode.cuh"
 #include "fa_e4m3.cuh"
@@ -756,12 +756,12 @@ cudaError_t launch(const Cut& k, E4m3Params a, cudaStream_t s) {
 
 // What the table can hold decides, as the lengths are not known here.  By tiles that a group has if it is full (128 rows; 304 groups
 // of d 128, 152 of d 256), 32 sequences, half full on average, the kernels of fa_decode_e4m3.cu against these, in us:
-//   d 128, 1 head a key head:  32: 33.3, 35.1   48: 44.7, 45.3   64: 60.0, 57.4   96: 81.0, 77.7
-//   d 128, 4 heads:            32: 34.1, 36.9   48: 45.6, 46.9   64: 60.5, 58.5   96: 85.5, 79.1
-//   d 256, 1 head:             24: 28.7, 28.7   32: 34.9, 34.4   48: 47.0, 45.1   96: 84.9, 77.7
-//   d 256, 4 heads:            24: 29.1, 31.4   32: 35.8, 37.2   48: 48.5, 47.6   96: 86.5, 80.1
-// 8 sequences that fill it: d 128 with 1 head, 16: 33.7, 33.6, 32: 58.9, 57.0; d 256 with 4, 12: 29.3, 30.5, 16: 36.2, 35.9,
-// 32: 61.4, 57.9.  d 96 gains nothing at any size, d 64 and 32 and eight heads or more lose.
+//   d 128, 1 head a key head:  32: 34.3, 35.9   48: 45.0, 45.9   64: 58.3, 57.4   96: 81.4, 77.8
+//   d 128, 4 heads:            32: 34.6, 37.2   48: 45.5, 47.1   64: 58.9, 58.5   96: 85.6, 79.0
+//   d 256, 1 head:             24: 29.1, 28.5   32: 35.0, 34.6   48: 47.0, 44.9   96: 83.5, 77.3
+//   d 256, 4 heads:            24: 29.6, 31.4   32: 36.2, 37.3   48: 48.2, 47.4   96: 85.1, 79.9
+// 8 sequences that fill it: d 128 with 1 head, 16: 33.3, 33.8, 32: 58.2, 57.0; d 256 with 4, 12: 29.1, 31.0, 16: 35.7, 36.1,
+// 32: 61.8, 58.6.  d 96 gains nothing at any size, d 64 and 32 and eight heads or more lose.
 bool takes_sm103(const fa_cache& c, int H) {
   const int64_t tiles = (int64_t)c.S * c.H_kv * cache_rows(c) / 128;
   return c.dtype == FA_BF16 && H / c.H_kv <= 4 && ((c.d == 128 && tiles >= 304 * 56) || (c.d == 256 && tiles >= 152 * 40));

@@ -5,16 +5,17 @@ and graphs.
 
 Tolerances are bounds, not fits.  With u = 2^-24, a score is a sum of d
 products whose absolute sum is at most A (as the oracle returns it), summed in
-fp32 with at most 2u of the sum an addition.  Queries are multiplied as sums of
-e4m3 numbers in units of a common power of two, three for bf16 and six for fp32,
-each of which leaves at most 2^-4 of what it holds: bf16 ones (8 bits) within 2^-19 of the largest
-of their head are exact, fp32 ones off by 2^-24.  Adding the terms up and three
-products follow.  So
+fp32 with at most 2u of the sum an addition.  Queries are multiplied in units of a
+common power of two of their head: bf16 ones (8 bits) as an fp16 number, or three e4m3 numbers
+on the tensor-memory path, exactly where they are within 2^-19 of the largest; fp32 ones as the sum
+of two fp16 numbers, off by at most 2^-23.  Adding the two up and three products
+follow, which leaves four of the eight below, one for the other half of 2^-23.  So
   e_s <= (2 d + 8) u A + e_q A,  e_q = 2^-24 in fp32, 0 in bf16.
 A weight is off by e_s plus the rounding of its exponent's product (4 u A), 2^-21 of
-the hardware exponential and what it loses as it is multiplied: in bf16 it is
-rounded to fp16 (2^-11) and then held as three terms (2^-12), in fp32 as six
-(2^-24) after two products.  Both the weighted sum and the sum of weights carry
+the hardware exponential and what it loses as it is multiplied, for which 2^-11 +
+2^-12 are allowed in bf16 and 3u in fp32 here.  The kernels are off by less: 2^-15 with four e5m2
+numbers (tensor memory), 2^-23 with two fp16 numbers (the others), or a share of the
+largest weight; test_gpu_decode_e4m3_weights.py holds them to that.  Both the weighted sum and the sum of weights carry
 that error and at most 2 u n of their additions, so
   |O - ref| <= half a step of the output type * |ref| + 2 V (e_w + 2 (n + 64) u)
   |L - ref| <= e_s + e_l + 2 (n + 64) u + 8 u |L|,  e_l as e_w without the multiplied weights' loss
