@@ -210,7 +210,7 @@ __device__ __forceinline__ bool run_of_group(const E4m3Params& a, int group, Wal
   __shared__ int64_t sums[M::kThreadsAll / 32];
   Units<M::kRows, M::kThreadsAll, M::kCost> units(a, sums);
   const Share share = units.share();
-  const int first = blockIdx.x / a.split * M::kGroups;
+  const int first = blockIdx.x * M::kGroups;
   *run = first + group;
   bool some = false;
 #pragma unroll 1
@@ -405,7 +405,7 @@ __device__ __forceinline__ void issue_products(const E4m3Params& a, Walk<M::kRow
 // ---------------------------------------------------------------- queries
 // Each item's queries as terms, an item ahead, in units of 1 / *qscales times the softmax scale.
 template <class M, int D, int HP>
-__device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows, M::kCost> at, int piece, uint32_t ring, Bars<M>* bars,
+__device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows, M::kCost> at, uint32_t ring, Bars<M>* bars,
                                               float (*qscales)[HP], const ptx::Waiter& waiter) {
   constexpr int kUnits = D / 128;  // of 4 columns of a head, a lane
   const int lane = threadIdx.x & 31;
@@ -414,7 +414,7 @@ __device__ __forceinline__ void store_queries(const E4m3Params& a, Walk<M::kRows
     if (n >= 2 && !ptx::warp_wait(ptx::smem_addr(&bars->q_empty[to]), ((n >> 1) - 1) & 1, waiter)) return;
     const uint32_t sQ = ring + M::kQ + to * M::kQBytes;
     int heads;
-    const int h0 = first_head(a, at.item, piece, &heads);
+    const int h0 = first_head(a, at.item, 0, &heads);
     uint2 y[HP][kUnits];
 #pragma unroll
     for (int h = 0; h < HP; ++h)
@@ -473,7 +473,7 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <class M, int D, int HP>
-__device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, int run, int piece, int group, uint32_t ring,
+__device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, M::kCost> walk, int run, int group, uint32_t ring,
                                             Bars<M>* bars, uint32_t (*seen_at)[4], float (*qscales)[HP],
                                             float (*over_warps)[kWarps][HP], uint32_t tmem, const ptx::Waiter& waiter) {
   constexpr int kStages = M::kStages, kTermsQ = M::kTermsQ, kTermsP = M::kTermsP, kN = M::kN, kHalves = M::kHalves;
@@ -617,10 +617,10 @@ __device__ __forceinline__ void weigh_tiles(const E4m3Params& a, Walk<M::kRows, 
       const bool whole = walk.t == 0 && walk.count == walk.tiles;
       // the part of an item that was being read when the run began is the
       // run's first, any other its second
-      const int slot = (2 * run + (first ? 0 : 1)) * a.split + piece;
+      const int slot = 2 * run + (first ? 0 : 1);
       first = false;
       int heads;
-      const int h0 = first_head(a, walk.item, piece, &heads);
+      const int h0 = first_head(a, walk.item, 0, &heads);
 #pragma unroll
       for (int h = 0; h < HP; ++h) {
         float sum = l[h];
@@ -712,19 +712,18 @@ __global__ void __launch_bounds__(Tile8<D, HP>::kThreadsAll, 1) decode_sm103_ker
   }
   __syncthreads();
   ptx::tc_fence_after();
-  const int piece = blockIdx.x % a.split;
   const uint32_t ring = ((ptx::smem_addr(dynamic) + 1023u) & ~1023u) + group * M::kGroupBytes;
   const uint32_t tmem = tmem_at + group * M::kGroupCols;
   const ptx::Waiter waiter{&abort_flags[group], a.status, a.wait_ns};
   if (some) {
     if (weighs) {
-      weigh_tiles<M, D, HP>(a, walk, run, piece, group, ring, bars, all_seen[group], all_qscales[group], all_over_warps[group], tmem,
+      weigh_tiles<M, D, HP>(a, walk, run, group, ring, bars, all_seen[group], all_qscales[group], all_over_warps[group], tmem,
                             waiter);
     } else if (issues) {
       if ((threadIdx.x & 31) == 0) issue_products<M, D>(a, walk, ring, bars, tmem, waiter);
       __syncwarp();
     } else if (asks) {
-      store_queries<M, D, HP>(a, walk, piece, ring, bars, all_qscales[group], waiter);
+      store_queries<M, D, HP>(a, walk, ring, bars, all_qscales[group], waiter);
     } else {
       copy_tiles<M>(a, walk, ring, bars, all_seen[group], (warp - 6 * M::kGroups) % M::kLoaders, waiter);
     }
@@ -747,7 +746,7 @@ cudaError_t launch(const Cut& k, E4m3Params a, cudaStream_t s) {
   cudaError_t e = resident_blocks((const void*)kernel, M::kSmem, known, &resident, M::kThreadsAll);
   if (e != cudaSuccess) return e;
   const int runs = runs_of(k, resident * M::kGroups, &a);
-  e = launch_early(kernel, dim3((unsigned)(ceil_div(runs, M::kGroups) * a.split)), M::kThreadsAll, M::kSmem, s, 1, a);
+  e = launch_early(kernel, dim3((unsigned)ceil_div(runs, M::kGroups)), M::kThreadsAll, M::kSmem, s, 1, a);
   if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, D, M::kRows, M::kCost>(k, a, runs, s);
 }
@@ -768,7 +767,7 @@ bool takes_sm103(const fa_cache& c, int H) {
 }
 
 Cut cut_e4m3_sm103(const fa_cache& c, int H) {
-  Cut k = pieces_of(H / c.H_kv, 4);
+  Cut k = pieces_of(H / c.H_kv, 4);  // one: takes_sm103
   k.part_heads = k.piece_heads == 1 ? 1 : 4;
   k.cost = c.d == 256 ? Tile8<256, 4>::kCost : Tile8<128, 4>::kCost;
   k.most_tiles = ceil_div(cache_rows(c), 128);
