@@ -42,11 +42,10 @@ namespace {
 // the place of a second group of 8 heads, at no more products.
 //
 // Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers: off by at most 2^-22 of the weight or, if that
-// is more, 2^-25, where the largest is 2^7 or more.  So the rounding of O is the only one to fewer than 16 bits, as in
+// is more, 2^-25, where the largest is 2^10 or more: 2^-35 of the largest.  So the rounding of O is the only one to fewer than 16 bits, as in
 // fa_decode.  One number for bf16, 11 bits, takes 31.2 us for 32.2 (32 sequences of up to 2048 rows, 32 heads of d 64) and, with 16
 // heads a key head of d 128, 107 for 116 (64 of up to 8192), but where values cancel it loses bits that O has.
-// The maximum that weights are taken against and U are moved only when a weight passes 2^kAhead (its bits are not
-// the fewer for that), so that almost every tile does without the maximum over its
+// The maximum that weights are taken against and U are moved only when a score passes the one by 7 or a weight 2^15, so that almost every tile does without the maximum over its
 // lanes and without a look at the accumulators.
 template <int D, int NH, bool kF32>
 struct Mma8 {
@@ -85,8 +84,10 @@ struct Mma8 {
     return D >= 128 ? (8 * (c / 2) + 2 * q + c % 2) * 16 : (4 * c + q) * kRun;
   }
 };
-constexpr float kAhead = 128.f;   // 2^7
-constexpr float kTopWeight = 256.f;  // of a weight when U is set, as fp16: kAhead times that is below 65504
+constexpr float kMostScore = 7.f;     // above the maximum that weights are taken against: 2^7 of them are as exact
+// Of a weight when U is set, and ever: as far up as fp16 reaches, for the sake of the small ones, but for some room to grow.
+// With 2^8, after which U moves less often, calls are 0 to 1 % quicker, and weights reach less far down by 2^3.
+constexpr float kTopWeight = 2048.f, kMostWeight = 32768.f;
 
 __device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -414,8 +415,7 @@ __global__ void __launch_bounds__(kThreads, Mma8<D, NH, kF32>::kBlocks)
               w[u][o][e] = p[u][o][e] * (e ? vs[o].y : vs[o].x);
               most = fmaxf(most, w[u][o][e]);
             }
-          // 2^7 above the maximum, or above the unit
-          passed |= top > m[u] + 7.f || most * per_unit[u] > kAhead * kTopWeight;
+          passed |= top > m[u] + kMostScore || most * per_unit[u] > kMostWeight;
         }
         if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll

@@ -71,9 +71,9 @@ __device__ __forceinline__ float scale_for(uint32_t t) {
 __device__ __forceinline__ float inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 
 // The power of two that weights are in units of, for the largest of them: at or above it, but between kLeastUnit and
-// 2^126, so that it has an inverse and 2^8 times that is finite.  Scales go from 2^-126 to beyond 2^126: with the
-// smallest the largest weight is still 1 of the 2^8 that it is elsewhere when a unit is set, with the largest it is 2^10.
-constexpr float kLeastUnit = 0x1p-118f;
+// 2^126, so that it has an inverse and 2^11 times that, which is what weights are multiplied by at most, is finite.  Scales
+// go from 2^-126 to beyond 2^126: the largest weight is less by up to 2^11 with the smallest, and twice that with the largest.
+constexpr float kLeastUnit = 0x1p-115f;
 __device__ __forceinline__ float unit_for(float largest) {
   const uint32_t up = (__float_as_uint(fmaxf(largest, kLeastUnit)) + 0x7fffffu) & 0x7f800000u;
   return __uint_as_float(min(up, 0x7e800000u));

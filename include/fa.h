@@ -395,7 +395,7 @@ fa_status fa_cache_copy_pages_e4m3(const fa_cache* c, int32_t block_rows, int32_
  * of lengths, pages and empty sequences.  Scales are positive and finite.
  * Scores and sums are fp32.  The weights, times the scales of V, are multiplied as
  * numbers of 15 bits at least with FA_BF16 and of 22 with FA_FP32, or in steps of
- * 2^-31 of the largest, or of 2^-148, where those are larger.
+ * 2^-34 of the largest, or of 2^-148, where those are larger.
  * A NaN in a visible row makes NaN of what it goes into, an infinity in Q of its
  * head. */
 size_t fa_decode_e4m3_workspace_bytes(const fa_cache* c, int32_t H);

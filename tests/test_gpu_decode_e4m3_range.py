@@ -2,8 +2,9 @@
 the largest.
 
 Bounds as in test_gpu_decode_e4m3.py, with what weights are held in as in test_gpu_decode_e4m3_weights.py.  At a scale b
-below 2^-118 the largest weight is 2^126 b when a unit is set, not 2^7 or more, so that weights are off by up to
-2^-25 / 2^126 = 2^-151, and their products with b, below 2^-126, by 2^-150: together less than 2^-149 / b of the largest.
+below 2^-115 the largest weight is 2^126 b (2^123 b on tensor memory) when a unit is set, not 2^10 (2^7) or more, so that
+weights are off by up to 2^-25 / 2^126 = 2^-151 (2^-29 / 2^123), and their products with b, below 2^-126, by 2^-150: together
+less than 2^-149 / b of the largest.
 The weighted sums of a warp or a part, below 2^-126 too, are rounded to 2^-149."""
 
 import numpy as np
@@ -44,7 +45,7 @@ def check(args, b):
     ref, Lr, A, V = decode(f64(q)[:, :, 0], k, v, table.cpu().numpy(), lengths.cpu().numpy(), scale)
     d, n = q.shape[3], lengths.cpu().numpy()[:, None]
     e_s = (2 * d + 9) * U * A
-    e_w = e_s + 4 * U * A + 2.0 ** -21 + 2.0 ** -15 + max(2.0 ** -32, 2.0 ** -149 / b)
+    e_w = e_s + 4 * U * A + 2.0 ** -21 + 2.0 ** -15 + max(2.0 ** -35, 2.0 ** -149 / b)
     tol = HALF_STEP[q.dtype] * np.abs(ref) + (2 * V * (e_w + 2 * (n + 64) * U))[:, :, None] + 2.0 ** -140
     if q.dtype == torch.float32:
         tol -= (2 * V * 2.0 ** -15 * (1 - 2.0 ** -7))[:, :, None]  # weights of 22 bits
@@ -55,7 +56,7 @@ def check(args, b):
     assert (np.abs(f64(L)[:, :, 0][seen] - Lr[seen]) <= tol[seen] + 8 * U * np.abs(Lr[seen])).all()
 
 
-@pytest.mark.parametrize("e", [-126, -125, -122, -120, -118, -117, -101, -99])
+@pytest.mark.parametrize("e", [-126, -125, -122, -120, -118, -117, -115, -114, -101, -99])
 @pytest.mark.parametrize("path", PATHS)
 def test_smallest_scales_of_values(path, e):
     args = cache(path, [300, 0, 17, 1], seed=1)

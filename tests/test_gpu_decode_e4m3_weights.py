@@ -12,7 +12,7 @@ the scores (4 of 2^-24 of the largest score, in the exponent), in the weighted s
 made tile by tile: at most 4 of a product's partial sums a tile of 64 rows or more, and 64 for the
 joining, each off by at most 2^-23 of the sum of absolute values.
   tensor-memory path, bf16:  r = 2^-15, a = 2^-36 (four terms of e5m2, the largest weight at 2^7 or more of 2^-29)
-  the other path:            r = 2^-22, a = 2^-32 (two fp16 numbers, the largest weight at 2^7 or more of 2^-25)"""
+  the other path:            r = 2^-22, a = 2^-35 (two fp16 numbers, the largest weight at 2^10 or more of 2^-25)"""
 
 import numpy as np
 import pytest
@@ -89,7 +89,7 @@ def check(path, args, n):
     assert fa.get_device_status() == 0
     rows = lambda t: t[:, 0].reshape(-1, *t.shape[3:])[:n].cpu().float().double().numpy()
     k, v, b = rows(ks), rows(vp), rows(vs)
-    r, a = (2.0 ** -15, 2.0 ** -36) if sm103 else (2.0 ** -22, 2.0 ** -32)
+    r, a = (2.0 ** -15, 2.0 ** -36) if sm103 else (2.0 ** -22, 2.0 ** -35)
     for h in range(group):
         score = k * (d * np.float64(np.float32(d ** -0.5)) * q[0, h, 0, 0].item())
         p = np.exp(score - score.max())
@@ -123,6 +123,19 @@ def test_many_small_weights_behind_a_large_one(path, by, gap):
     else:
         scales[0] = 2.0 ** gap
     check(path, cache(path, n, gaps, v, scales), n)
+
+
+@pytest.mark.parametrize("gap", [26.5, 28.5])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_weights_at_the_end_of_their_range(path, gap):
+    """As above, with weights that are a few steps of what they are held in, the value 1 for all, and large ones for each
+    warp, which has a unit of its own, of the first tile."""
+    n, d = 12000, PATHS[path][0]
+    v = torch.ones(n, d)
+    v[:128:16] = 0
+    gaps = np.full(n, gap)
+    gaps[:128:16] = 0
+    check(path, cache(path, n, gaps, v, np.ones(n), top=32), n)
 
 
 @pytest.mark.parametrize("path", list(PATHS))
