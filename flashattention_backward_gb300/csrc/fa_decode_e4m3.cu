@@ -41,12 +41,13 @@ namespace {
 // largest.  fp32 ones become the sum of two, the second 2^11 times itself: it takes
 // the place of a second group of 8 heads, at no more products.
 //
-// Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers: off by at most 2^-22 of the weight or, if that
-// is more, 2^-25, where the largest is 2^10 or more: 2^-35 of the largest.  So the rounding of O is the only one to fewer than 16 bits, as in
-// fa_decode.  One number for bf16, 11 bits, takes 31.2 us for 32.2 (32 sequences of up to 2048 rows, 32 heads of d 64) and, with 16
-// heads a key head of d 128, 107 for 116 (64 of up to 8192), but where values cancel it loses bits that O has.
-// The maximum that weights are taken against and U are moved only when a score passes the one by 7 or a weight 2^15, so that almost every tile does without the maximum over its
-// lanes and without a look at the accumulators.
+// Weights: P b_j / U, U a power of two, as the sum of two fp16 numbers: off by at most 2^-22 of the weight or, if that is
+// more, 2^-25, where the largest is 2^10 or more: 2^-35 of the largest.  So the rounding of O is the only one to fewer
+// than 16 bits, as in fa_decode.  One number for bf16, 11 bits, takes 31.2 us for 32.2 (32 sequences of up to 2048 rows,
+// 32 heads of d 64) and, with 16 heads a key head of d 128, 107 for 116 (64 of up to 8192), but where values cancel it
+// loses bits that O has.  The maximum that weights are taken against and U are moved only when a score passes the one by 7
+// or a weight 2^15, so that almost every tile does without the maximum over its lanes and without a look at the
+// accumulators.
 template <int D, int NH, bool kF32>
 struct Mma8 {
   static constexpr int kSub = D <= 64 ? 2 : 1;
@@ -84,7 +85,7 @@ struct Mma8 {
     return D >= 128 ? (8 * (c / 2) + 2 * q + c % 2) * 16 : (4 * c + q) * kRun;
   }
 };
-constexpr float kMostScore = 7.f;     // above the maximum that weights are taken against: 2^7 of them are as exact
+constexpr float kMostScore = 7.f;  // above the maximum that weights are taken against
 // Of a weight when U is set, and ever: as far up as fp16 reaches, for the sake of the small ones, but for some room to grow.
 // With 2^8, after which U moves less often, calls are 0 to 1 % quicker, and weights reach less far down by 2^3.
 constexpr float kTopWeight = 2048.f, kMostWeight = 32768.f;
